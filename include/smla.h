@@ -293,6 +293,114 @@ int smla_decode_noalloc(const smla_decode_params* params, void* stream);
 int smla_pack_records(const void* latent, int64_t latent_stride, const void* rope,
                       int64_t rope_stride, int64_t n, void* kv_out, void* stream);
 
+/* ---- The paged cache: write, read back, attend ------------------------------
+ *
+ * A paged cache holds records in n_pages pages of page_size records each (the
+ * record layout above); sequences own pages through a block table.  With
+ * page_stride == page_size * SMLA_RECORD_BYTES the cache is also the flat
+ * cache of smla_decode, a record's row id being page * page_size + offset.
+ *
+ * Batch: sequence b owns the token rows cu_rows[b] .. cu_rows[b + 1] - 1 of the
+ * token tensors (latent, rope, q, out, lse), which are its positions up to
+ * seq_lens[b] - 1:
+ *   position of row r of sequence b = seq_lens[b] - (cu_rows[b + 1] - r).
+ * Position p lives in page block_table[b][p / page_size] at offset
+ * p % page_size.  A position < 0, past the table's max_pages pages, or in a
+ * page whose id is < 0 or >= n_pages is masked: its record is neither read
+ * nor written.  Ids >= n_pages and positions past the table set
+ * SMLA_STATUS_INDEX_OOB; negative ids are padding and set nothing.  Token rows
+ * of no sequence are left as they are.  cu_rows must not decrease; values
+ * outside [0, n_rows] are clamped.
+ *
+ * Layouts and alignment: kv_cache uint8, 16-byte aligned; page_stride (bytes)
+ * a multiple of 16, at least page_size * SMLA_RECORD_BYTES; block_table int32
+ * [n_seqs][block_table_stride], max_pages entries used; cu_rows int32
+ * [n_seqs + 1]; seq_lens int32 [n_seqs]; n_rows the rows of the token tensors;
+ * status int32 [1] or NULL.  max_pages * page_size <= 2^30, n_rows <= 2^30,
+ * n_seqs <= 2^24.
+ * All of it is device memory and read on the device: a captured graph may be
+ * replayed with other tables, lengths and row splits in the same buffers. */
+#define SMLA_DTYPE_BF16 0
+#define SMLA_DTYPE_F16 1
+#define SMLA_DTYPE_F32 2
+
+typedef struct smla_paged_batch {
+  void* kv_cache;
+  int64_t n_pages;
+  int64_t page_stride;
+  int32_t page_size;
+  int32_t max_pages;
+  const int32_t* block_table;
+  int64_t block_table_stride;
+  const int32_t* cu_rows;
+  const int32_t* seq_lens;
+  int64_t n_rows;
+  int32_t n_seqs;
+  int32_t* status;
+} smla_paged_batch;
+
+/* Writes every token row's record at its position: the rule of
+ * smla_pack_records (bit for bit for bf16 inputs) for latent and rope of type
+ * dtype, values in f32 and rope rounded to bf16 (nearest even).  A block's
+ * largest finite magnitude bounds its scale (an infinity is stored as +-448
+ * times the scale of the largest f32); a NaN latent is stored as the NaN code.
+ * latent [n_rows][latent_stride] (512 used), rope [n_rows][rope_stride] (64
+ * used), 16-byte aligned, strides multiples of 16 bytes.  The rows' positions
+ * have to lie in different slots: of two rows that a block table sends to one
+ * slot, either's bytes may remain there. */
+int smla_paged_write(const smla_paged_batch* batch, const void* latent, int64_t latent_stride, const void* rope,
+                     int64_t rope_stride, int32_t dtype, void* stream);
+
+/* Reads every token row's record back: latent[r][d] = e4m3 * scale (the f32
+ * product, rounded once to dtype), rope[r] converted to dtype.  A row whose
+ * position is masked gets zeros.  A whole history is read with
+ * cu_rows[b + 1] - cu_rows[b] = seq_lens[b]; a part of it that ends at position
+ * e with seq_lens[b] = e.  Layouts as smla_paged_write. */
+int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_stride, void* rope,
+                    int64_t rope_stride, int32_t dtype, void* stream);
+
+#define SMLA_PAGED_MAX_HEADS 128
+
+/* Attention of the token rows over their sequences' records.  For row r of
+ * sequence b at position p, the visible keys are the unmasked positions
+ * t <= p (causal = 1) or t < seq_lens[b] (causal = 0); with k_t, s_t, the sink,
+ * out and lse as in smla_decode.  A row without a visible key gives out = 0 and
+ * lse = -inf.  A visible record whose latent holds a value that is not finite
+ * (a NaN code, a scale that is not finite) makes the row's out and lse NaN;
+ * what a row may not see never reaches it.
+ *
+ * q bf16 [n_rows][num_heads][576] and out bf16 [n_rows][num_heads][512] with
+ * strides as in smla_decode (16-byte aligned, strides multiples of 8); sink f32
+ * [num_heads] or NULL; lse f32 [n_rows][num_heads] contiguous or NULL;
+ * num_heads in [1, SMLA_PAGED_MAX_HEADS].  The records of the token rows
+ * themselves are read from the cache like all others: write them first.
+ * Accuracy as the bf16 tensor-core kernel of smla_decode (k and v enter the
+ * products as bf16(e4m3 * scale), exact for scales 2^-116 .. 2^7; p is rounded
+ * to bf16; sums, maxima and the softmax statistics are f32). */
+typedef struct smla_paged_attend_params {
+  smla_paged_batch batch;
+  int32_t num_heads;
+  int32_t causal;
+  const void* q;
+  int64_t q_stride_row;
+  int64_t q_stride_head;
+  float sm_scale;
+  const float* sink;
+  void* out;
+  int64_t out_stride_row;
+  int64_t out_stride_head;
+  float* lse;
+} smla_paged_attend_params;
+
+/* Workspace bytes of smla_paged_attend for these params on the current device
+ * (0 for invalid params and empty batches).  It depends on the sizes alone
+ * (num_heads, n_rows, n_seqs, page_size, max_pages), needs no initial contents
+ * and is 256-byte aligned.  Calls that may overlap on the GPU need workspaces
+ * of their own. */
+size_t smla_paged_attend_workspace_size(const smla_paged_attend_params* params);
+
+int smla_paged_attend(const smla_paged_attend_params* params, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Name of a status code. */
 const char* smla_strerror(int status);
 

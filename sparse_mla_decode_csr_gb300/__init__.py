@@ -33,7 +33,13 @@ KERNEL_CUDA_CORE = 1
 KERNEL_TENSOR_CORE_BF16 = 2
 KERNEL_TENSOR_CORE_FP8 = 3
 NOALLOC_SCRATCH_BYTES = 64 << 20  # SMLA_NOALLOC_SCRATCH_BYTES
+PAGED_MAX_HEADS = 128
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # SMLA_DTYPE_*
+SMLA_ERR_NULL = -1
+SMLA_ERR_SHAPE = -2
+SMLA_ERR_STRIDE = -3
 SMLA_ERR_WORKSPACE = -5
+SMLA_ERR_DEVICE = -7
 
 
 class SmlaError(RuntimeError):
@@ -85,6 +91,40 @@ class PlanInfo(ctypes.Structure):
     ]
 
 
+class PagedBatch(ctypes.Structure):
+    _fields_ = [
+        ("kv_cache", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("page_stride", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("block_table", ctypes.c_void_p),
+        ("block_table_stride", ctypes.c_int64),
+        ("cu_rows", ctypes.c_void_p),
+        ("seq_lens", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int64),
+        ("n_seqs", ctypes.c_int32),
+        ("status", ctypes.c_void_p),
+    ]
+
+
+class PagedAttendParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", PagedBatch),
+        ("num_heads", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("q_stride_row", ctypes.c_int64),
+        ("q_stride_head", ctypes.c_int64),
+        ("sm_scale", ctypes.c_float),
+        ("sink", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_stride_row", ctypes.c_int64),
+        ("out_stride_head", ctypes.c_int64),
+        ("lse", ctypes.c_void_p),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -103,6 +143,16 @@ def _load():
                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                       ctypes.c_void_p]
     lib.smla_pack_records.restype = ctypes.c_int
+    for name in ("smla_paged_write", "smla_paged_read"):
+        f = getattr(lib, name)
+        f.argtypes = [ctypes.POINTER(PagedBatch), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                      ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]
+        f.restype = ctypes.c_int
+    lib.smla_paged_attend_workspace_size.argtypes = [ctypes.POINTER(PagedAttendParams)]
+    lib.smla_paged_attend_workspace_size.restype = ctypes.c_size_t
+    lib.smla_paged_attend.argtypes = [ctypes.POINTER(PagedAttendParams), ctypes.c_void_p, ctypes.c_size_t,
+                                      ctypes.c_void_p]
+    lib.smla_paged_attend.restype = ctypes.c_int
     lib.smla_strerror.argtypes = [ctypes.c_int]
     lib.smla_strerror.restype = ctypes.c_char_p
     lib.smla_device_check.argtypes = []
@@ -115,7 +165,9 @@ def _load():
 lib = _load()
 
 EXPORTED_SYMBOLS = ("smla_plan", "smla_decode_workspace_size", "smla_decode", "smla_decode_noalloc",
-                    "smla_pack_records", "smla_strerror", "smla_device_check", "smla_set_wait_limit")
+                    "smla_pack_records", "smla_paged_write", "smla_paged_read",
+                    "smla_paged_attend_workspace_size", "smla_paged_attend",
+                    "smla_strerror", "smla_device_check", "smla_set_wait_limit")
 
 
 def strerror(code: int) -> str:
@@ -286,6 +338,160 @@ def smla_pack_records(latent: torch.Tensor, rope: torch.Tensor, kv_out: torch.Te
                                n, kv_out.data_ptr(), _stream(stream))
     if rc != 0:
         raise SmlaError(rc, "smla_pack_records")
+
+
+# ---- the paged cache ----
+
+
+def _need(ok: bool, code: int, what: str) -> None:
+    if not ok:
+        raise SmlaError(code, what)
+
+
+def _on_device(what: str, *tensors) -> None:
+    """Every tensor on the current CUDA device (the launch goes there)."""
+    for t in tensors:
+        if t is not None:
+            _need(t.is_cuda and t.device.index == torch.cuda.current_device(), SMLA_ERR_DEVICE,
+                  f"{what}: a tensor is not on the current CUDA device")
+
+
+def _paged_batch(what: str, kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
+                 seq_lens: torch.Tensor, n_rows: int, status: Optional[torch.Tensor]) -> PagedBatch:
+    """The C batch of a paged cache uint8 [n_pages, page_size, 656] (pages may be
+    strided) and its int32 tables, checked."""
+    _need(kv_cache.dtype == torch.uint8 and kv_cache.dim() == 3 and kv_cache.shape[2] == RECORD_BYTES,
+          SMLA_ERR_SHAPE, f"{what}: kv_cache is uint8 [n_pages, page_size, {RECORD_BYTES}]")
+    # (a dimension of one element, or an empty cache, may carry any stride)
+    empty = kv_cache.numel() == 0
+    _need(empty or (kv_cache.stride(2) == 1 and (kv_cache.shape[1] == 1 or kv_cache.stride(1) == RECORD_BYTES)),
+          SMLA_ERR_STRIDE, f"{what}: the records of a page are contiguous")
+    for t, dims in ((block_table, 2), (cu_rows, 1), (seq_lens, 1)):
+        _need(t.dtype == torch.int32 and t.dim() == dims, SMLA_ERR_SHAPE,
+              f"{what}: block_table is int32 [n_seqs, max_pages], cu_rows and seq_lens int32 vectors")
+        _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1, SMLA_ERR_STRIDE,
+              f"{what}: block_table rows, cu_rows and seq_lens are contiguous")
+    n_seqs = int(seq_lens.shape[0])
+    _need(cu_rows.shape[0] == n_seqs + 1 and block_table.shape[0] == n_seqs, SMLA_ERR_SHAPE,
+          f"{what}: n_seqs + 1 entries of cu_rows and n_seqs rows of block_table")
+    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), SMLA_ERR_SHAPE,
+          f"{what}: status is int32 [1]")
+    _on_device(what, kv_cache, block_table, cu_rows, seq_lens, status)
+    b = PagedBatch()
+    b.kv_cache, b.n_pages = kv_cache.data_ptr(), int(kv_cache.shape[0])
+    b.page_size, b.max_pages = int(kv_cache.shape[1]), int(block_table.shape[1])
+    b.page_stride = kv_cache.stride(0) if kv_cache.shape[0] > 1 else b.page_size * RECORD_BYTES
+    b.block_table = block_table.data_ptr()
+    b.block_table_stride = block_table.stride(0) if n_seqs > 1 else b.max_pages
+    b.cu_rows, b.seq_lens = cu_rows.data_ptr(), seq_lens.data_ptr()
+    b.n_rows, b.n_seqs, b.status = int(n_rows), n_seqs, _ptr(status)
+    return b
+
+
+def _paged_copy(what, kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status) -> None:
+    _need(latent.dtype in DTYPES and rope.dtype == latent.dtype, SMLA_ERR_SHAPE,
+          f"{what}: latent and rope of one type, bf16, f16 or f32")
+    _need(latent.dim() == 2 and latent.shape[1] == LATENT_DIM and rope.dim() == 2 and
+          tuple(rope.shape) == (latent.shape[0], ROPE_DIM), SMLA_ERR_SHAPE,
+          f"{what}: latent [rows, {LATENT_DIM}] and rope [rows, {ROPE_DIM}]")
+    n = int(latent.shape[0])
+    _need(n == 0 or (latent.stride(1) == 1 and rope.stride(1) == 1), SMLA_ERR_STRIDE,
+          f"{what}: the rows of latent and rope are contiguous")
+    _on_device(what, latent, rope)
+    b = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
+    # (the stride of a single row says nothing)
+    strides = (latent.stride(0), rope.stride(0)) if n > 1 else (LATENT_DIM, ROPE_DIM)
+    rc = getattr(lib, what)(ctypes.byref(b), latent.data_ptr(), strides[0], rope.data_ptr(), strides[1],
+                            DTYPES[latent.dtype], _stream(stream))
+    if rc != 0:
+        raise SmlaError(rc, what)
+
+
+def smla_paged_write(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                     cu_rows: torch.Tensor, seq_lens: torch.Tensor, stream=None, *,
+                     status: Optional[torch.Tensor] = None) -> None:
+    """Writes the records of new token rows into a paged cache.
+
+    latent [rows, 512], rope [rows, 64]: bf16, f16 or f32.  kv_cache: uint8
+    [n_pages, page_size, 656].  Sequence b owns rows cu_rows[b]:cu_rows[b + 1],
+    which are its positions up to seq_lens[b] - 1 (seq_lens counts them);
+    position p lives in page block_table[b, p // page_size].  Rows whose page id
+    is negative are skipped; ids >= n_pages and positions past the table are
+    skipped and set STATUS_INDEX_OOB.  The rows' positions must lie in different
+    slots.  See include/smla.h."""
+    _paged_copy("smla_paged_write", kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status)
+
+
+def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor, seq_lens: torch.Tensor,
+                    latent: torch.Tensor, rope: torch.Tensor, stream=None, *,
+                    status: Optional[torch.Tensor] = None) -> None:
+    """Reads records of a paged cache back into latent [rows, 512] and rope
+    [rows, 64] (bf16, f16 or f32).  Batch as smla_paged_write: row r of sequence
+    b gets position seq_lens[b] - (cu_rows[b + 1] - r); masked positions give
+    zeros, rows of no sequence are left as they were.  See include/smla.h."""
+    _paged_copy("smla_paged_read", kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status)
+
+
+def smla_paged_attend_workspace_size(n_rows: int, num_heads: int, n_seqs: int, page_size: int, max_pages: int) -> int:
+    """Workspace bytes of smla_paged_attend for these sizes on the current device."""
+    p = PagedAttendParams()
+    p.num_heads = int(num_heads)
+    p.batch.n_rows, p.batch.n_seqs = int(n_rows), int(n_seqs)
+    p.batch.page_size, p.batch.max_pages = int(page_size), int(max_pages)
+    return int(lib.smla_paged_attend_workspace_size(ctypes.byref(p)))
+
+
+def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
+                      seq_lens: torch.Tensor, sm_scale: float, sink: Optional[torch.Tensor], out: torch.Tensor,
+                      lse: Optional[torch.Tensor], stream=None, *, causal: bool = True,
+                      status: Optional[torch.Tensor] = None, workspace_tensor: Optional[torch.Tensor] = None) -> None:
+    """Attention of new token rows over a paged cache, into ``out`` (bf16
+    [rows, H, 512]) and ``lse`` (f32 [rows, H] or None).
+
+    q: bf16 [rows, H, 576], H up to 128; batch as smla_paged_write (the rows'
+    own records are read from the cache: write them first).  A row at position
+    p sees positions 0..p (causal) or its whole sequence; sink: f32 [H] or None.
+    workspace_tensor: uint8, smla_paged_attend_workspace_size bytes; without it
+    one is allocated for this call on its stream.  See include/smla.h."""
+    what = "smla_paged_attend"
+    _need(q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[2] == QK_DIM, SMLA_ERR_SHAPE,
+          f"{what}: q is bf16 [rows, heads, {QK_DIM}]")
+    n, heads = int(q.shape[0]), int(q.shape[1])
+    _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (n, heads, LATENT_DIM), SMLA_ERR_SHAPE,
+          f"{what}: out is bf16 [rows, heads, {LATENT_DIM}]")
+    _need(q.numel() == 0 or (q.stride(2) == 1 and out.stride(2) == 1), SMLA_ERR_STRIDE,
+          f"{what}: the last dimension of q and out is contiguous")
+    _need(sink is None or (sink.dtype == torch.float32 and tuple(sink.shape) == (heads,) and sink.is_contiguous()),
+          SMLA_ERR_SHAPE, f"{what}: sink is f32 [heads]")
+    _need(lse is None or (lse.dtype == torch.float32 and tuple(lse.shape) == (n, heads) and lse.is_contiguous()),
+          SMLA_ERR_SHAPE, f"{what}: lse is contiguous f32 [rows, heads]")
+    _on_device(what, q, out, sink, lse, workspace_tensor)
+    p = PagedAttendParams()
+    p.batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
+    p.num_heads, p.causal, p.sm_scale = heads, int(bool(causal)), float(sm_scale)
+    # (the stride of a dimension of one element says nothing)
+    p.q, p.out = q.data_ptr(), out.data_ptr()
+    p.q_stride_head = q.stride(1) if heads > 1 else QK_DIM
+    p.out_stride_head = out.stride(1) if heads > 1 else LATENT_DIM
+    p.q_stride_row = q.stride(0) if n > 1 else heads * p.q_stride_head
+    p.out_stride_row = out.stride(0) if n > 1 else heads * p.out_stride_head
+    p.sink, p.lse = _ptr(sink), _ptr(lse)
+    ws = workspace_tensor
+    s = _stream(stream)
+    if ws is None:
+        nbytes = int(lib.smla_paged_attend_workspace_size(ctypes.byref(p)))
+        if nbytes:
+            # a block of this call's own, on its stream: calls on other streams and
+            # other captured graphs never share it
+            if stream is None or isinstance(stream, torch.cuda.Stream):
+                on = stream
+            else:
+                on = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+            with torch.cuda.stream(on):
+                ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    rc = lib.smla_paged_attend(ctypes.byref(p), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
+    if rc != 0:
+        raise SmlaError(rc, what)
 
 
 def smla_device_check() -> int:

@@ -129,7 +129,8 @@ int smla_set_wait_limit(uint64_t limit_ns, int stall_first_wait) {
   const int rc = smla_device_check();
   if (rc != SMLA_OK) return rc;
   if (smla::fp8_set_wait_limit(limit_ns, stall_first_wait) != cudaSuccess ||
-      smla::tc_set_wait_limit(limit_ns, stall_first_wait) != cudaSuccess)
+      smla::tc_set_wait_limit(limit_ns, stall_first_wait) != cudaSuccess ||
+      smla::paged_set_wait_limit(limit_ns, stall_first_wait) != cudaSuccess)
     return SMLA_ERR_LAUNCH;
   return SMLA_OK;
 }

@@ -62,4 +62,19 @@ cudaError_t tc_set_wait_limit(uint64_t ns, int stall);
 cudaError_t launch_pack(const void* latent, int64_t latent_stride, const void* rope,
                         int64_t rope_stride, int64_t n, void* kv_out, cudaStream_t stream);
 
+// The paged cache.  Workspace of one attend call: per pair of CTAs a merge job
+// (16 bytes), two partials' (m, l) of 128 rows, and their O.
+struct AttendPlan {
+  int32_t pairs;  // CTA pairs launched
+  int64_t merge_off, ml_off, o_off, total;
+};
+AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms);
+cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendPlan& plan, void* workspace,
+                                cudaStream_t stream);
+cudaError_t paged_set_wait_limit(uint64_t ns, int stall);
+cudaError_t launch_paged_write(const smla_paged_batch& b, const void* latent, int64_t latent_stride, const void* rope,
+                               int64_t rope_stride, int32_t dtype, cudaStream_t stream);
+cudaError_t launch_paged_read(const smla_paged_batch& b, void* latent, int64_t latent_stride, void* rope,
+                              int64_t rope_stride, int32_t dtype, cudaStream_t stream);
+
 }  // namespace smla

@@ -1,0 +1,982 @@
+// Attention of new tokens over the paged cache (smla_paged_attend): chunks of a
+// prompt, drafted tokens, single tokens.
+//
+// For token row r at position p and head h, over the visible positions t,
+//   s_t = sm_scale q . k_t (576 dims),  out = sum_t e^(s_t - m) v_t / (sum_t e^(s_t - m) + e^(sink - m)),
+// v_t the latent 512 dims of k_t.  All heads of all tokens of a sequence share
+// its keys, so (token, head) pairs are the rows of two matrix products:
+//   S[128, 64] = Q[128, 576] . K[64, 576]^T,   O[128, 512] += P[128, 64] . V[64, 512].
+//
+// Row tiles.  A row tile is floor(128 / heads) consecutive tokens of one
+// sequence with all their heads.  Its keys are the positions up to its last
+// token's, in tiles of 64.
+//
+// CTA pairs.  An f32 accumulator of 128 x 512 alone fills the 512 TMEM columns
+// of an SM, so a row tile belongs to a cluster of two CTAs and the products are
+// cta_group::2 instructions with M = 128: CTA c holds rows [64 c, 64 c + 64) of
+// Q, P, S and O (64 rows on 128 lanes: lanes 64.. hold the upper half of the
+// columns), which takes 256 columns for O and 32 per S buffer.  As B operands
+// each CTA supplies half of the N extent: its own 32 keys of the tile for QK
+// ("K": 32 x 576), and its own 256 value dims of all 64 keys for PV ("V": 64 x
+// 256, MN-major).  Every record is read and dequantised once, by the CTA that
+// owns the key: it writes K locally and each V half to the CTA that needs it
+// (distributed shared memory).
+//
+// Warps (13): 0-3 softmax and epilogue, 4-11 loaders, 12 issues the MMAs of the
+// pair (one thread of the even CTA).  Per tile g (stage g & 1):
+//   loaders   raw records of tile g + 1 are on their way in registers while tile
+//             g is dequantised; K when QK(g - 2) is done, V when PV(g - 2) is
+//   issuer    QK(g), then PV(g - 1): the tensor pipe works on the next scores
+//             while the softmax of this tile runs
+//   softmax   a row is two threads (32 keys each) that exchange their maxima;
+//             p = 2^(x - m_ref), the reference moves (and O is rescaled in TMEM)
+//             only when a score exceeds it by more than 8, so p <= 2^8
+//
+// Schedule.  A row tile takes one slot for its start and one per key tile; the
+// slots of all row tiles, in order, are split evenly over the pairs (pair c of
+// G takes [c W / G, (c + 1) W / G)).  A row tile inside one pair's range is
+// finished there; a shared one leaves f32 partials (O, m, l) that
+// paged_merge_kernel joins.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "smla_device.cuh"
+#include "smla_internal.h"
+#include "smla_paged.cuh"
+#include "smla_ptx.cuh"
+
+namespace smla {
+
+// Limit of every pipeline wait in ns (0: the default), and whether the first
+// softmax wait of each CTA is on a barrier that nothing signals (a test of the
+// timeout path); read at kernel start.
+__device__ uint64_t g_paged_wait_ns;
+__device__ int32_t g_paged_stall;
+
+namespace {
+
+using namespace ptx;
+
+constexpr int kTileKeys = 64;
+constexpr int kOwnKeys = 32;      // keys of a tile that one CTA of the pair loads
+constexpr int kPairRows = 128;
+constexpr int kCtaRows = 64;
+constexpr int kLoaderWarps = 8;
+constexpr int kKeysPerWarp = kOwnKeys / kLoaderWarps;
+constexpr int kFirstLoader = 4;
+constexpr int kIssuer = 12;
+constexpr int kAttendThreads = 13 * 32;
+constexpr int kStageK = 9 * kOwnKeys * 128;   // nine 64-dim blocks of 128-byte rows
+constexpr int kStageV = 4 * kTileKeys * 128;  // four 64-dim blocks
+constexpr int kVBlock = kTileKeys * 128;
+constexpr int kOffK = 0;
+constexpr int kOffV = kOffK + 2 * kStageK;
+constexpr int kOffQ = kOffV + 2 * kStageV;
+constexpr int kQBlock = kCtaRows * 128;
+constexpr int kOffP = kOffQ + 9 * kQBlock;
+constexpr int kOffMisc = kOffP + kCtaRows * 128;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 256;              // two S buffers of 32 columns behind O's 256
+constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
+constexpr uint32_t kIdescPV = idesc_bf16(kPairRows, 256, 0, 1);
+constexpr int kMinPairSlots = 3;              // slots below which no further pair is used
+
+struct AttendArgs {
+  PagedArgs b;
+  const uint16_t* q;
+  int64_t q_row, q_head;
+  uint16_t* out;
+  int64_t o_row, o_head;
+  float* lse;
+  const float* sink;
+  float scale_log2;
+  int32_t heads, tokens, causal;  // tokens: of a row tile
+  int32_t pairs;
+  int32_t coverage;               // positions the block table can hold
+  float* o_part;                  // [2 pairs][128][512]
+  float* ml_part;                 // [2 pairs][128][2]
+  int32_t* merge;                 // [pairs][4]: rows to merge (0: none), first token row, first pair, its last slot
+};
+
+struct Misc {
+  uint64_t k_full[2], v_full[2], q_full, p_full, s_empty[2];  // used in the even CTA
+  uint64_t qk_done[2], pv_done[2], drain, never;
+  uint32_t tmem;
+  int32_t dead;
+  uint64_t wait_ns;
+  int32_t stall;
+  int32_t first_seq, first_j;
+  int64_t first_slot, beg, end, total;
+  int64_t warp_sum[kAttendThreads / 32];
+  float tmax[2][128];
+  float lsum[128];
+  // per tile: a byte per loader warp of the pair, bits 0-3 keys that are masked
+  // (no record), bits 4-7 keys whose latent is not finite
+  uint8_t flags[4][2 * kLoaderWarps];
+};
+static_assert(sizeof(Misc) <= 2816, "shared memory");
+constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc)) + 1024;
+static_assert(kAttendSmem <= 232448, "shared memory of a CTA");
+
+// ---- cluster helpers ----
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// Orders this thread's shared-memory writes, in its own CTA and in its peer,
+// before later async-proxy (tensor core) reads of them.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives once on `bar` of both CTAs when the MMAs issued so far are complete.
+__device__ __forceinline__ void commit2(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(uint16_t(3))
+      : "memory");
+}
+
+// Gives up the pipeline of both CTAs (see wait_for).
+__device__ __noinline__ void give_up(Misc* ms, const AttendArgs& a) {
+  if (atomicExch(&ms->dead, 1) == 0 && a.b.status) atomicOr(a.b.status, SMLA_STATUS_TIMEOUT);
+  const uint32_t other = map_to(smem_u32(&ms->dead), cluster_rank() ^ 1u);
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(other), "r"(1) : "memory");
+}
+
+// Waits for the phase of `bar`; false after the limit, or once the pair has
+// given up.
+__device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
+  if (try_wait_cluster(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 0;; ++i) {
+    if ((i & 63u) == 0) {
+      if (*reinterpret_cast<volatile int32_t*>(&ms->dead)) return false;
+      const uint64_t t = globaltimer();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > ms->wait_ns) {
+        give_up(ms, a);
+        return false;
+      }
+    }
+    if (try_wait_cluster(bar, parity)) return true;
+  }
+}
+
+// The same for a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_for(ms, a, bar, parity));
+}
+
+// ---- the schedule ----
+
+// sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice-point count, by
+// the Euclidean reduction of (a, m)).
+__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t ans = 0;
+  while (n > 0) {
+    if (a >= m) {
+      ans += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return ans;
+}
+
+// What a sequence needs for its row tiles.
+struct Seq {
+  int32_t row0, rows;  // its token rows
+  int32_t past;        // position of the first one (negative: rows before the sequence's start)
+  int32_t tiles;       // row tiles
+};
+
+__device__ __forceinline__ Seq seq_at(const AttendArgs& a, int32_t b) {
+  Seq s;
+  s.row0 = cu_at(a.b, b);
+  const int32_t end = cu_at(a.b, b + 1);
+  s.rows = max(end - s.row0, 0);
+  s.past = seq_len_at(a.b, b) - s.rows;
+  s.tiles = (s.rows + a.tokens - 1) / a.tokens;
+  return s;
+}
+
+// End of the visible positions of row tile j: its last token's, within the table.
+__device__ __forceinline__ int32_t keys_end(const AttendArgs& a, const Seq& s, int32_t j) {
+  const int32_t last = a.causal ? min((j + 1) * a.tokens, s.rows) : s.rows;
+  return max(min(s.past + last, a.coverage), 0);
+}
+
+__device__ __forceinline__ int32_t key_tiles(int32_t end) { return max((end + kTileKeys - 1) / kTileKeys, 1); }
+
+// Slots of the sequence's first j row tiles.
+__device__ int64_t slots_before(const AttendArgs& a, const Seq& s, int32_t j) {
+  if (j <= 0) return 0;
+  if (!a.causal) return int64_t(j) * (1 + key_tiles(keys_end(a, s, 0)));
+  int64_t sum = j;
+  const int32_t n = min(j, s.tiles - 1);  // tiles that end at past + tokens (i + 1)
+  if (j == s.tiles) sum += key_tiles(keys_end(a, s, j - 1));
+  // tiles [0, lo) have one key tile, [lo, hi) follow the line, [hi, n) end at the table's end
+  const int64_t G = a.tokens, P = s.past, C = a.coverage;
+  int64_t lo = P <= kTileKeys ? (kTileKeys - P) / G : 0;
+  lo = min(lo, int64_t(n));
+  int64_t hi = C - P > 0 ? (C - P + G - 1) / G - 1 : 0;
+  hi = max(min(hi, int64_t(n)), lo);
+  sum += lo;
+  sum += floor_sum(hi - lo, kTileKeys, G, P + G * (lo + 1) + kTileKeys - 1);
+  sum += (n - hi) * int64_t(key_tiles(a.coverage));
+  return sum;
+}
+
+// A row tile's part that this pair works on.
+struct Unit {
+  int32_t seq, row0, tokens;  // its first token row and number of tokens
+  int32_t pos0;               // position of that token
+  int32_t end;                // end of its visible positions
+  int32_t t0, t1, tiles;      // key tiles [t0, t1) of `tiles`
+  int64_t slot;               // first slot of the row tile
+};
+
+struct Units {
+  int64_t slot, beg, end;
+  int32_t seq, j;
+  Seq s;
+
+  __device__ __forceinline__ void start(const AttendArgs& a, const Misc* ms) {
+    slot = ms->first_slot;
+    beg = ms->beg;
+    end = ms->end;
+    seq = ms->first_seq;
+    j = ms->first_j;
+    s.tiles = 0;
+    if (slot < end && seq < a.b.n_seqs) s = seq_at(a, seq);
+  }
+
+  // The next unit of this pair; false when there is none.
+  __device__ __forceinline__ bool next(const AttendArgs& a, Unit& u) {
+    while (slot < end && seq < a.b.n_seqs) {
+      if (j >= s.tiles) {
+        j = 0;
+        if (++seq < a.b.n_seqs) s = seq_at(a, seq);
+        continue;
+      }
+      u.seq = seq;
+      u.row0 = s.row0 + j * a.tokens;
+      u.tokens = min(a.tokens, s.rows - j * a.tokens);
+      u.pos0 = s.past + j * a.tokens;
+      u.end = keys_end(a, s, j);
+      u.tiles = key_tiles(u.end);
+      u.slot = slot;
+      u.t0 = int32_t(max(beg - (slot + 1), int64_t(0)));
+      u.t1 = int32_t(min(end - (slot + 1), int64_t(u.tiles)));
+      slot += 1 + u.tiles;
+      ++j;
+      if (u.t0 < u.t1) return true;
+    }
+    return false;
+  }
+};
+
+// The pair's range of slots and the row tile it starts in, by all threads.
+__device__ void find_range(const AttendArgs& a, Misc* ms, int32_t pair) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t per = (a.b.n_seqs + kAttendThreads - 1) / kAttendThreads;
+  const int32_t s0 = min(tid * per, a.b.n_seqs), s1 = min(s0 + per, a.b.n_seqs);
+  int64_t sum = 0;
+  for (int32_t s = s0; s < s1; ++s) {
+    const Seq q = seq_at(a, s);
+    sum += slots_before(a, q, q.tiles);
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) ms->warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t before = inc - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kAttendThreads / 32; ++w) {
+    const int64_t v = ms->warp_sum[w];
+    if (w < warp) before += v;
+    total += v;
+  }
+  const int64_t G = max(min(int64_t(a.pairs), total / kMinPairSlots), int64_t(1));
+  const int64_t beg = pair < G ? pair * total / G : total, end = pair < G ? (pair + 1) * total / G : total;
+  if (tid == 0) {
+    ms->beg = beg;
+    ms->end = end;
+    ms->total = total;
+    if (beg >= end) ms->first_slot = end;  // nothing to do
+  }
+  if (beg < end && before <= beg && beg < before + sum) {
+    int64_t slot = before;
+    int32_t s = s0;
+    Seq q = seq_at(a, s);
+    int64_t n = slots_before(a, q, q.tiles);
+    while (slot + n <= beg) {
+      slot += n;
+      q = seq_at(a, ++s);
+      n = slots_before(a, q, q.tiles);
+    }
+    int32_t lo = 0, hi = q.tiles - 1;  // the last row tile that starts at or before beg
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) >> 1;
+      if (slot + slots_before(a, q, mid) <= beg) lo = mid;
+      else hi = mid - 1;
+    }
+    ms->first_seq = s;
+    ms->first_j = lo;
+    ms->first_slot = slot + slots_before(a, q, lo);
+  }
+}
+
+// ---- dequantisation ----
+
+// Two E4M3 codes (bytes of w picked by sel into the upper byte of each half) as
+// bf16x2 of value * 2^-120: sign, exponent and mantissa are moved into place,
+// an exact multiplication by scale * 2^120 does the rest (subnormals included).
+__device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, uint32_t mul2) {
+  const uint32_t x = __byte_perm(w, 0, sel);
+  const uint32_t y = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(mul2));
+  return r;
+}
+
+// Whether a block scale takes the fast path: zero, or a power of two in
+// [2^-116, 2^7] (scale * 2^120 is then a normal bf16 power of two).
+__device__ __forceinline__ bool plain_scale(uint32_t bits) {
+  return bits == 0u || ((bits & 0x807FFFFFu) == 0u && bits >= (11u << 23) && bits <= (134u << 23));
+}
+
+// Whether a word of four codes holds a NaN code.
+__device__ __forceinline__ uint32_t nan_code(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// The general form: bf16(e4m3 * scale), values that are not finite become zero
+// and are reported.
+__device__ __forceinline__ bool dequant16_any(const uint4& c, uint32_t scale_bits, uint32_t (&v)[8]) {
+  const float scale = __uint_as_float(scale_bits);
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+    float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f.x = __bfloat162float(__float2bfloat16_rn(f.x * scale));
+    f.y = __bfloat162float(__float2bfloat16_rn(f.y * scale));
+    if (!isfinite(f.x)) f.x = 0.f, bad = true;
+    if (!isfinite(f.y)) f.y = 0.f, bad = true;
+    v[i] = pack_bf16x2(f.x, f.y);
+  }
+  return bad;
+}
+
+// One tile's records of a loader warp, in flight or landed.
+struct Raw {
+  uint4 lat[kKeysPerWarp];      // lane l: codes of dims [16 l, 16 l + 16)
+  uint32_t scale[kKeysPerWarp];
+  uint4 rope;                   // lane l: 16 bytes of record l / 8's rope
+};
+
+// ---- roles ----
+
+__device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
+  const uint32_t k_full = map_to(smem_u32(ms->k_full), 0), v_full = map_to(smem_u32(ms->v_full), 0);
+  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0);
+  const uint32_t v_base = map_to(base + kOffV, uint32_t(lane) >> 4);
+  const uint32_t peer_flags = map_to(smem_u32(ms->flags), rank ^ 1u);
+
+  // Three cursors over the pair's tiles: addresses are looked up one tile ahead
+  // of the loads, the loads run one tile ahead of the conversion.
+  Units units;
+  units.start(a, ms);
+  Unit u;            // unit of the lookups
+  bool more = units.next(a, u);
+  int32_t t = more ? u.t0 : 0;
+
+  // Record address of lane j < kKeysPerWarp's key at the lookup cursor (0: none).
+  auto look_up = [&](bool& starts, Unit& first, bool& any) -> uint64_t {
+    uint64_t rec = 0;
+    any = more;
+    starts = false;
+    if (!more) return 0;
+    starts = t == u.t0;
+    if (starts) first = u;
+    const int32_t pos = t * kTileKeys + int32_t(rank) * kOwnKeys + w * kKeysPerWarp + lane;
+    if (lane < kKeysPerWarp && pos < u.end) rec = reinterpret_cast<uint64_t>(record_at(a.b, u.seq, pos));
+    if (++t == u.t1) {
+      more = units.next(a, u);
+      if (more) t = u.t0;
+    }
+    return rec;
+  };
+  auto issue = [&](uint64_t rec, Raw& r) {
+    const uint64_t rope_rec = __shfl_sync(0xffffffffu, rec, lane >> 3);
+    r.rope = make_uint4(0, 0, 0, 0);
+    if (rope_rec) r.rope = ldg_v4_now(reinterpret_cast<const uint8_t*>(rope_rec) + kRopeOffset + (lane & 7) * 16);
+#pragma unroll
+    for (int j = 0; j < kKeysPerWarp; ++j) {
+      const uint64_t p = __shfl_sync(0xffffffffu, rec, j);
+      r.lat[j] = make_uint4(0, 0, 0, 0);
+      r.scale[j] = 0;
+      if (p) {
+        r.lat[j] = ldg_v4_now(reinterpret_cast<const uint8_t*>(p) + lane * 16);
+        r.scale[j] = ldg_u32_now(reinterpret_cast<const uint8_t*>(p) + kScaleOffset + 4 * (lane >> 3));
+      }
+    }
+  };
+
+  Raw raw;
+  Unit cur_unit, next_unit;
+  bool cur_starts, next_starts, cur_any, next_any;
+  uint64_t cur_rec = look_up(cur_starts, cur_unit, cur_any);
+  issue(cur_rec, raw);
+  uint64_t next_rec = look_up(next_starts, next_unit, next_any);
+  for (uint32_t g = 0; cur_any; ++g) {
+    const uint32_t stage = g & 1;
+    if (cur_starts) {
+      // q of the unit, once the last QK of the unit before is done
+      if (g > 0 && !warp_wait(ms, a, &ms->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return;
+      const int32_t rows = cur_unit.tokens * a.heads;
+      for (int i = w; i < kCtaRows; i += kLoaderWarps) {
+        const int32_t m = int32_t(rank) * kCtaRows + i;
+        const uint32_t dst = base + kOffQ + i * 128;
+        const int32_t tok = m / a.heads;
+        const uint16_t* src = a.q + int64_t(cur_unit.row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head;
+#pragma unroll
+        for (int c = lane; c < kQK / 8; c += 32) {
+          const uint32_t at = dst + (c >> 3) * kQBlock + (((c & 7) ^ (i & 7)) << 4);
+          if (m < rows) cp_async16(at, src + c * 8);
+          else st_shared_v4(at, 0, 0, 0, 0);
+        }
+      }
+      cp_async_wait_all();
+      fence_proxy_async_all();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(q_full);
+    }
+    // convert the landed records
+    uint32_t v[kKeysPerWarp][8];
+    uint32_t odd = 0;
+#pragma unroll
+    for (int j = 0; j < kKeysPerWarp; ++j)
+      odd |= nan_code(raw.lat[j].x) | nan_code(raw.lat[j].y) | nan_code(raw.lat[j].z) | nan_code(raw.lat[j].w) |
+             (plain_scale(raw.scale[j]) ? 0u : 1u);
+    const uint32_t masked = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && cur_rec == 0);
+    uint32_t flags = masked;
+    if (__any_sync(0xffffffffu, odd != 0)) {
+#pragma unroll
+      for (int j = 0; j < kKeysPerWarp; ++j) {
+        const bool bad = dequant16_any(raw.lat[j], raw.scale[j], v[j]);
+        if (__any_sync(0xffffffffu, bad)) flags |= 16u << j;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kKeysPerWarp; ++j) {
+        // scale * 2^120 as a bf16 pair (0 stays 0)
+        const uint32_t s = raw.scale[j] ? (raw.scale[j] + (120u << 23)) >> 16 : 0u;
+        const uint32_t mul2 = s | (s << 16);
+        const uint32_t c[4] = {raw.lat[j].x, raw.lat[j].y, raw.lat[j].z, raw.lat[j].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[j][2 * i] = dequant2(c[i], 0x1404, mul2);
+          v[j][2 * i + 1] = dequant2(c[i], 0x3424, mul2);
+        }
+      }
+    }
+    const uint4 rope = raw.rope;
+    // the next tile's records set out while this one is stored
+    const bool go_on = next_any;
+    if (go_on) issue(next_rec, raw);
+    if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1)) return;
+    {
+      const uint32_t k = base + kOffK + stage * kStageK;
+#pragma unroll
+      for (int j = 0; j < kKeysPerWarp; ++j) {
+        const int key = w * kKeysPerWarp + j;
+        const uint32_t row = k + (lane >> 2) * (kOwnKeys * 128) + key * 128;
+        // lanes of neighbouring blocks store their two chunks in turns: all eight
+        // 16-byte columns of a quarter warp differ
+        const int flip = (lane >> 2) & 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = i ^ flip;
+          const uint32_t at = row + ((((lane & 3) * 2 + c) ^ (key & 7)) << 4);
+          st_shared_v4(at, c ? v[j][4] : v[j][0], c ? v[j][5] : v[j][1], c ? v[j][6] : v[j][2], c ? v[j][7] : v[j][3]);
+        }
+      }
+      const int key = w * kKeysPerWarp + (lane >> 3);
+      st_shared_v4(k + 8 * (kOwnKeys * 128) + key * 128 + (((lane & 7) ^ (key & 7)) << 4), rope.x, rope.y, rope.z,
+                   rope.w);
+      if (lane == 0) {
+        const uint32_t at = (g & 3) * (2 * kLoaderWarps) + rank * kLoaderWarps + w;
+        ms->flags[0][at] = uint8_t(flags);
+        st_cluster_u8(peer_flags + at, flags);
+      }
+    }
+    fence_proxy_async_all();
+    __syncwarp();
+    if (lane == 0) arrive_cluster(k_full + 8 * stage);
+    if (g >= 2 && !warp_wait(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
+    {
+      const uint32_t vb = v_base + stage * kStageV + ((lane >> 2) & 3) * kVBlock;
+#pragma unroll
+      for (int j = 0; j < kKeysPerWarp; ++j) {
+        const int key = int(rank) * kOwnKeys + w * kKeysPerWarp + j;
+        const int flip = (lane >> 2) & 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c = i ^ flip;
+          const uint32_t at = vb + key * 128 + ((((lane & 3) * 2 + c) ^ (key & 7)) << 4);
+          st_cluster_v4(at, c ? v[j][4] : v[j][0], c ? v[j][5] : v[j][1], c ? v[j][6] : v[j][2],
+                        c ? v[j][7] : v[j][3]);
+        }
+      }
+    }
+    fence_proxy_async_all();
+    __syncwarp();
+    if (lane == 0) arrive_cluster(v_full + 8 * stage);
+    cur_rec = next_rec;
+    cur_starts = next_starts;
+    cur_any = next_any;
+    if (next_starts) cur_unit = next_unit;
+    next_rec = look_up(next_starts, next_unit, next_any);
+  }
+}
+
+// One thread of the even CTA.
+__device__ __forceinline__ void issuer_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem) {
+  const uint64_t q0 = smem_desc(base + kOffQ, 16, 1024, kSw128);
+  const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128);
+  const uint64_t p0 = smem_desc(base + kOffP, 16, 1024, kSw128);
+  const uint64_t v0 = smem_desc(base + kOffV, kVBlock, 1024, kSw128);
+  auto pv = [&](uint32_t g, bool first) -> bool {
+    const uint32_t stage = g & 1;
+    if (!wait_for(ms, a, &ms->v_full[stage], (g >> 1) & 1)) return false;
+    if (!wait_for(ms, a, &ms->p_full, g & 1)) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < kTileKeys / 16; ++k)
+        mma2(tmem + 128 * h, p0 + uint64_t(k * 2), v0 + uint64_t((stage * kStageV + h * 2 * kVBlock + k * 2048) >> 4),
+             kIdescPV, (first && k == 0) ? 0u : 1u);
+    commit2(&ms->pv_done[stage]);
+    return true;
+  };
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0, n_units = 0;
+  bool prev_first = false;
+  while (units.next(a, u)) {
+    if (!wait_for(ms, a, &ms->q_full, n_units & 1)) return;
+    ++n_units;
+    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+      const uint32_t stage = g & 1;
+      if (!wait_for(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
+      if (g >= 2 && !wait_for(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
+      tc_fence_after();
+      const uint32_t d = tmem + kTmemS + 32 * stage;
+#pragma unroll
+      for (int k = 0; k < kQK / 16; ++k)
+        mma2(d, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
+             k0 + uint64_t((stage * kStageK + (k >> 2) * (kOwnKeys * 128) + (k & 3) * 32) >> 4), kIdescQK, k > 0);
+      commit2(&ms->qk_done[stage]);
+      if (g > 0 && !pv(g - 1, prev_first)) return;
+      prev_first = t == u.t0;
+    }
+  }
+  if (g > 0) pv(g - 1, prev_first);
+}
+
+__device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem, uint32_t rank,
+                                             int32_t pair) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = (warp & 1) * 32 + lane;  // of this CTA
+  const int half = warp >> 1;              // columns: keys [32 half, +32), dims [256 half, +256)
+  const int32_t m = int32_t(rank) * kCtaRows + row;
+  const int32_t tok = m / a.heads, head = m - tok * a.heads;
+  const uint32_t lane_base = tmem + (uint32_t(warp) << 21);  // lane 32 warp
+  const uint32_t p_full = map_to(smem_u32(&ms->p_full), 0), s_empty = map_to(smem_u32(ms->s_empty), 0);
+  const uint32_t p_row = base + kOffP + row * 128;
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0;
+  // (a wait that gives up does not end this role: its warps meet at named
+  // barriers, so all of them run through every tile)
+  if (ms->stall) wait_for(ms, a, &ms->never, 0);
+  while (units.next(a, u)) {
+    const bool live = m < u.tokens * a.heads;
+    const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
+    float ref = -INFINITY, l = 0.f;
+    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+      const uint32_t stage = g & 1;
+      wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
+      tc_fence_after();
+      uint32_t s[32];
+      {
+        uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(s);
+        uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(s + 16);
+        tmem_ld16(lane_base + kTmemS + 32 * stage, lo);
+        tmem_ld16(lane_base + kTmemS + 32 * stage + 16, hi);
+      }
+      const uint2 flags = *reinterpret_cast<const uint2*>(&ms->flags[g & 3][8 * half]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(s_empty + 8 * stage);
+      float x[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(s[c]) * a.scale_log2;
+      const int32_t key0 = t * kTileKeys + 32 * half;
+      if (__any_sync(0xffffffffu, key0 + 32 > see)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = key0 + c < see ? x[c] : -INFINITY;
+      }
+      if (flags.x | flags.y) {  // (the same for the whole warp)
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const uint32_t f = ((c < 16 ? flags.x : flags.y) >> (8 * ((c >> 2) & 3))) >> (c & 3);
+          if (f & 1u) x[c] = -INFINITY;
+          else if ((f & 16u) && key0 + c < see) x[c] = __uint_as_float(0x7FC00000u);
+        }
+      }
+      float tm = x[0];
+#pragma unroll
+      for (int c = 1; c < 32; ++c) tm = fmaxf(tm, x[c]);
+      ms->tmax[stage][warp * 32 + lane] = tm;
+      named_barrier(1 + (warp & 1), 64);
+      tm = fmaxf(tm, ms->tmax[stage][(warp ^ 2) * 32 + lane]);
+      const bool move = tm > ref + kMoveMargin;
+      const float nref = move ? tm : ref;
+      const float use = nref == -INFINITY ? 0.f : nref;
+      const float alpha = move ? ex2(ref - use) : 1.f;
+      ref = nref;
+      uint32_t p[16];
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float p0 = ex2(x[2 * c] - use), p1 = ex2(x[2 * c + 1] - use);
+        sum += p0 + p1;
+        p[c] = pack_bf16x2(p0, p1);  // P as the product's bf16 operand; the sum keeps f32
+      }
+      l = l * alpha + sum;
+      if (g > 0) wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      if (t > u.t0 && __any_sync(0xffffffffu, move)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(lane_base + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+          tmem_st16(lane_base + c, o);
+        }
+        tmem_wait_st();
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        st_shared_v4(p_row + (((4 * half + c) ^ (row & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+      fence_proxy_async_all();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(p_full);
+    }
+    // the unit's end: row sums of the two halves, then O
+    ms->lsum[warp * 32 + lane] = l;
+    named_barrier(1 + (warp & 1), 64);
+    l += ms->lsum[(warp ^ 2) * 32 + lane];
+    wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    tc_fence_after();
+    const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+    const int64_t part = 2 * int64_t(pair) + (u.t0 > 0 ? 0 : 1);
+    float factor = 1.f;
+    const int64_t tok_row = int64_t(u.row0) + tok;
+    if (live && half == 0) {
+      if (!whole) {
+        a.ml_part[(part * kPairRows + m) * 2] = ref;
+        a.ml_part[(part * kPairRows + m) * 2 + 1] = l;
+      }
+    }
+    if (whole) {
+      float lse;
+      finish_head_v(ref, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+      if (live && half == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
+    }
+    uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 256 * half;
+    float* pdst = a.o_part + (part * kPairRows + m) * kLatent + 256 * half;
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 16) {
+      uint32_t o[16];
+      tmem_ld16(lane_base + c, o);
+      tmem_wait_ld();
+      if (!live) continue;
+      if (whole) {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = l == 0.f ? 0u
+                          : pack_bf16x2(__uint_as_float(o[2 * i]) * factor, __uint_as_float(o[2 * i + 1]) * factor);
+        *reinterpret_cast<uint4*>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<uint4*>(pdst + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+      }
+    }
+    tc_fence_before();
+    if (!whole && u.t0 > 0 && u.t1 == u.tiles && rank == 0 && threadIdx.x == 0) {
+      // the row tile's last part: the merge kernel joins the parts from the pair
+      // that holds its first key tile up to this one
+      const int64_t G = max(min(int64_t(a.pairs), ms->total / kMinPairSlots), int64_t(1));
+      a.merge[pair * 4 + 1] = u.row0;
+      a.merge[pair * 4 + 2] = int32_t(((u.slot + 2) * G - 1) / ms->total);
+      a.merge[pair * 4] = u.tokens * a.heads;
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
+paged_attend_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ uint8_t raw_smem[];
+  const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
+  Misc* ms = reinterpret_cast<Misc*>(raw_smem + (base - smem_u32(raw_smem)) + kOffMisc);
+  const uint32_t rank = cluster_rank();
+  const int32_t pair = blockIdx.x >> 1;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms->k_full[i], 2 * kLoaderWarps);
+      mbar_init(&ms->v_full[i], 2 * kLoaderWarps);
+      mbar_init(&ms->s_empty[i], 8);
+      mbar_init(&ms->qk_done[i], 1);
+      mbar_init(&ms->pv_done[i], 1);
+    }
+    mbar_init(&ms->q_full, 2 * kLoaderWarps);
+    mbar_init(&ms->p_full, 8);
+    mbar_init(&ms->drain, 1);
+    mbar_init(&ms->never, 1);
+    fence_mbar_init();
+    ms->dead = 0;
+    ms->wait_ns = g_paged_wait_ns ? g_paged_wait_ns : kWaitNs;
+    ms->stall = g_paged_stall;
+    if (rank == 0) a.merge[pair * 4] = 0;
+  }
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms->tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    tc_fence_before();
+  }
+  find_range(a, ms, pair);
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  if (warp < kFirstLoader) {
+    softmax_role(a, ms, base, tmem, rank, pair);
+  } else if (warp < kIssuer) {
+    loader_role(a, ms, base, rank);
+  } else if (rank == 0 && (threadIdx.x & 31) == 0) {
+    issuer_role(a, ms, base, tmem);
+    // every MMA has to be complete before the tensor memory and the shared
+    // memory it reads go away (also after a wait that gave up); the odd CTA
+    // learns of it at the cluster barrier
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(&ms->drain))
+                 : "memory");
+    if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == kIssuer) {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  }
+}
+
+// Joins the partials of a row tile shared between pairs: with m = max_c m_c,
+//   l = sum_c l_c 2^(m_c - m),  O = sum_c O_c 2^(m_c - m),
+// and the sink enters once.  A warp per row, one block per 8 rows of a pair's
+// merge job; the parts come from L2.
+constexpr int kMergeWarps = 8;
+
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ AttendArgs a) {
+  const int32_t last = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int32_t m = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  if (m >= a.merge[last * 4]) return;
+  const int32_t row0 = a.merge[last * 4 + 1], first = a.merge[last * 4 + 2];
+  float mx = -INFINITY;
+  for (int32_t c = first; c <= last; ++c) {
+    const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
+    mx = fmaxf(mx, a.ml_part[(part * kPairRows + m) * 2]);
+  }
+  const float use = mx == -INFINITY ? 0.f : mx;
+  float l = 0.f, o[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) o[i] = 0.f;
+  for (int32_t c = first; c <= last; ++c) {
+    const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
+    const float wgt = ex2(a.ml_part[(part * kPairRows + m) * 2] - use);
+    l += a.ml_part[(part * kPairRows + m) * 2 + 1] * wgt;
+    const float4* src = reinterpret_cast<const float4*>(a.o_part + (part * kPairRows + m) * kLatent) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[32 * i];
+      o[4 * i] += v.x * wgt;
+      o[4 * i + 1] += v.y * wgt;
+      o[4 * i + 2] += v.z * wgt;
+      o[4 * i + 3] += v.w * wgt;
+    }
+  }
+  const int32_t tok = m / a.heads, head = m - tok * a.heads;
+  const int64_t tok_row = int64_t(row0) + tok;
+  float factor, lse;
+  finish_head_v(mx, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+  if (lane == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
+  uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 4 * lane;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint2 v = make_uint2(pack_bf16x2(o[4 * i] * factor, o[4 * i + 1] * factor),
+                         pack_bf16x2(o[4 * i + 2] * factor, o[4 * i + 3] * factor));
+    if (l == 0.f) v = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(dst + 128 * i) = v;
+  }
+}
+
+}  // namespace
+
+AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
+  AttendPlan plan{};
+  const smla_paged_batch& b = p.batch;
+  if (b.n_rows <= 0 || b.n_seqs <= 0) return plan;
+  const int64_t tokens = p.num_heads >= kPairRows ? 1 : kPairRows / p.num_heads;
+  const int64_t coverage = int64_t(b.max_pages) * b.page_size;
+  const int64_t most_tiles = coverage > 0 ? (coverage + kTileKeys - 1) / kTileKeys : 1;
+  const int64_t row_tiles = (b.n_rows + tokens - 1) / tokens + (b.n_rows < b.n_seqs ? b.n_rows : int64_t(b.n_seqs));
+  const int64_t slots = row_tiles * (most_tiles + 1);
+  int64_t pairs = num_sms / 2;
+  if (slots / kMinPairSlots < pairs) pairs = slots / kMinPairSlots;
+  plan.pairs = int32_t(pairs < 1 ? 1 : pairs);
+  plan.merge_off = 0;
+  plan.ml_off = (int64_t(plan.pairs) * 16 + 255) & ~int64_t(255);
+  plan.o_off = plan.ml_off + ((int64_t(plan.pairs) * 2 * kPairRows * 8 + 255) & ~int64_t(255));
+  plan.total = plan.o_off + int64_t(plan.pairs) * 2 * kPairRows * kLatent * 4;
+  return plan;
+}
+
+cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendPlan& plan, void* workspace,
+                                cudaStream_t stream) {
+  AttendArgs a{};
+  a.b = make_paged_args(p.batch);
+  a.q = static_cast<const uint16_t*>(p.q);
+  a.q_row = p.q_stride_row;
+  a.q_head = p.q_stride_head;
+  a.out = static_cast<uint16_t*>(p.out);
+  a.o_row = p.out_stride_row;
+  a.o_head = p.out_stride_head;
+  a.lse = p.lse;
+  a.sink = p.sink;
+  a.scale_log2 = p.sm_scale * kLog2e;
+  a.heads = p.num_heads;
+  a.tokens = kPairRows / p.num_heads;
+  a.causal = p.causal != 0;
+  a.pairs = plan.pairs;
+  a.coverage = p.batch.max_pages * p.batch.page_size;
+  char* ws = static_cast<char*>(workspace);
+  a.merge = reinterpret_cast<int32_t*>(ws + plan.merge_off);
+  a.ml_part = reinterpret_cast<float*>(ws + plan.ml_off);
+  a.o_part = reinterpret_cast<float*>(ws + plan.o_off);
+  cudaError_t err =
+      cudaFuncSetAttribute(paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
+  if (err != cudaSuccess) return err;
+  paged_attend_kernel<<<2 * plan.pairs, kAttendThreads, kAttendSmem, stream>>>(a);
+  err = cudaGetLastError();
+  if (err != cudaSuccess || plan.pairs == 1) return err;
+  paged_merge_kernel<<<dim3(unsigned(plan.pairs), kPairRows / kMergeWarps), 32 * kMergeWarps, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t paged_set_wait_limit(uint64_t ns, int stall) {
+  const int32_t s = stall;
+  const cudaError_t err = cudaMemcpyToSymbol(g_paged_wait_ns, &ns, sizeof(ns));
+  return err != cudaSuccess ? err : cudaMemcpyToSymbol(g_paged_stall, &s, sizeof(s));
+}
+
+}  // namespace smla

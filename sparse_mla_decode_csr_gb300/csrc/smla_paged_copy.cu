@@ -1,0 +1,310 @@
+// The paged cache's writer and reader (smla_paged_write, smla_paged_read).
+//
+// Writer, per block of 128 latent values: scale = pow2ceil(max(amax, 1e-4) / 448),
+// code = E4M3(x / scale); 1 / scale is a power of two, so the quotient is exact
+// and each value is rounded once.  Reader: value = e4m3 * scale in f32, rounded
+// once to the output's type.  Both are bound by HBM at large sizes and by the
+// chain row -> sequence -> page -> record at small ones.
+//
+// A warp takes kRows consecutive token rows.  Lane l handles the 16-byte chunks
+// l, l + 32, ... of a row of the token tensor (8 values of a 16-bit type, 4 of
+// f32), so every access of a warp covers a contiguous range on both sides; a
+// scale block is 16 or all 32 lanes of one chunk step.  The rows' data is loaded
+// before the first of their records is located.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cfloat>
+#include <cstdint>
+
+#include "smla_internal.h"
+#include "smla_paged.cuh"
+
+namespace smla {
+namespace {
+
+constexpr int kWarps = 8;
+
+template <int kDtype>
+struct Elem {
+  static constexpr int kPer = kDtype == SMLA_DTYPE_F32 ? 4 : 8;  // values of a 16-byte chunk
+  static constexpr int kSteps = kLatent / (32 * kPer);           // chunk steps of a latent row
+  static constexpr int kRopeLanes = kRope / kPer;
+  static constexpr int kBytes = 16 / kPer;
+};
+
+// The kPer values of a chunk as f32, and back.
+template <int kDtype>
+__device__ __forceinline__ void unpack(const uint4& c, float (&x)[Elem<kDtype>::kPer]) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kDtype == SMLA_DTYPE_F32) {
+      x[i] = __uint_as_float(w[i]);
+    } else if constexpr (kDtype == SMLA_DTYPE_BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    } else {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <int kDtype>
+__device__ __forceinline__ uint4 pack(const float (&x)[Elem<kDtype>::kPer]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kDtype == SMLA_DTYPE_F32) {
+      w[i] = __float_as_uint(x[i]);
+    } else if constexpr (kDtype == SMLA_DTYPE_BF16) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+      const __half2 v = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Scale of a block with largest magnitude amax, and its reciprocal: the
+// smallest power of two that is not below max(amax, 1e-4) / 448.
+__device__ __forceinline__ float block_scale(float amax, float* inv) {
+  const uint32_t b = __float_as_uint(fminf(fmaxf(amax, 1e-4f), FLT_MAX) / 448.0f);
+  const uint32_t e = (b >> 23) + ((b & 0x7FFFFFu) ? 1u : 0u);
+  *inv = __uint_as_float((254u - e) << 23);
+  return __uint_as_float(e << 23);
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t w, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> (16 * i)), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// Lane j's record of token row base + j (j < kRows): nullptr for a masked
+// position; *has is whether the row belongs to a sequence.
+template <int kRows>
+__device__ __forceinline__ uint8_t* locate(const PagedArgs& a, int32_t base, bool* has) {
+  const int lane = threadIdx.x & 31;
+  int32_t b = seq_of_row(a, base);
+  const int32_t r = base + lane;
+  *has = false;
+  if (lane >= kRows || r >= a.n_rows) return nullptr;
+  int32_t end = cu_at(a, b + 1);
+  while (end <= r && b + 1 < a.n_seqs) end = cu_at(a, ++b + 1);
+  if (r >= end || cu_at(a, b) > r) return nullptr;
+  *has = true;
+  return record_at(a, b, seq_len_at(a, b) - (end - r));
+}
+
+template <int kRows, int kDtype>
+__global__ void __launch_bounds__(32 * kWarps)
+paged_write_kernel(const __grid_constant__ PagedArgs a, const uint8_t* __restrict__ latent, int64_t latent_stride,
+                   const uint8_t* __restrict__ rope, int64_t rope_stride) {
+  using E = Elem<kDtype>;
+  const int lane = threadIdx.x & 31;
+  const int64_t base64 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRows;
+  if (base64 >= a.n_rows) return;
+  const int32_t base = int32_t(base64);
+  uint4 lat[kRows][E::kSteps], rp[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (base + j < a.n_rows) {
+      const uint8_t* src = latent + int64_t(base + j) * latent_stride * E::kBytes + lane * 16;
+#pragma unroll
+      for (int i = 0; i < E::kSteps; ++i) lat[j][i] = __ldcs(reinterpret_cast<const uint4*>(src + i * 512));
+      if (lane < E::kRopeLanes)
+        rp[j] = __ldcs(reinterpret_cast<const uint4*>(rope + int64_t(base + j) * rope_stride * E::kBytes + lane * 16));
+    }
+  }
+  bool has;
+  const uint64_t mine = reinterpret_cast<uint64_t>(locate<kRows>(a, base, &has));
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    uint8_t* rec = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, j));
+    if (rec == nullptr) continue;  // (the same for the whole warp)
+#pragma unroll
+    for (int i = 0; i < E::kSteps; ++i) {
+      float x[E::kPer];
+      unpack<kDtype>(lat[j][i], x);
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < E::kPer; ++k) amax = fmaxf(amax, fabsf(x[k]));
+#pragma unroll
+      for (int o = 1; o < 128 / E::kPer; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      float inv;
+      const float scale = block_scale(amax, &inv);
+      const uint32_t c0 = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+      const int chunk = lane + 32 * i;
+      if constexpr (E::kPer == 8) {
+        const uint32_t c1 = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+        *reinterpret_cast<uint2*>(rec + chunk * 8) = make_uint2(c0, c1);
+      } else {
+        *reinterpret_cast<uint32_t*>(rec + chunk * 4) = c0;
+      }
+      constexpr int kLanes = 128 / E::kPer;  // lanes of a scale block
+      if ((lane & (kLanes - 1)) == 0) *reinterpret_cast<float*>(rec + kScaleOffset + 4 * (chunk / kLanes)) = scale;
+    }
+    if (lane < E::kRopeLanes) {
+      if constexpr (kDtype == SMLA_DTYPE_BF16) {
+        *reinterpret_cast<uint4*>(rec + kRopeOffset + lane * 16) = rp[j];
+      } else {
+        float x[E::kPer];
+        unpack<kDtype>(rp[j], x);
+        uint32_t w[E::kPer / 2];
+#pragma unroll
+        for (int k = 0; k < E::kPer / 2; ++k) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+          w[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        if constexpr (E::kPer == 8)
+          *reinterpret_cast<uint4*>(rec + kRopeOffset + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        else
+          *reinterpret_cast<uint2*>(rec + kRopeOffset + lane * 8) = make_uint2(w[0], w[1]);
+      }
+    }
+  }
+}
+
+template <int kRows, int kDtype>
+__global__ void __launch_bounds__(32 * kWarps)
+paged_read_kernel(const __grid_constant__ PagedArgs a, uint8_t* __restrict__ latent, int64_t latent_stride,
+                  uint8_t* __restrict__ rope, int64_t rope_stride) {
+  using E = Elem<kDtype>;
+  constexpr int kCodes = E::kPer / 4;  // 32-bit words of codes per chunk
+  const int lane = threadIdx.x & 31;
+  const int64_t base64 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRows;
+  if (base64 >= a.n_rows) return;
+  const int32_t base = int32_t(base64);
+  bool has;
+  const uint64_t mine = reinterpret_cast<uint64_t>(locate<kRows>(a, base, &has));
+  const uint32_t rows = __ballot_sync(0xffffffffu, has);
+  uint32_t code[kRows][E::kSteps][kCodes];
+  float scale[kRows][E::kSteps];
+  uint32_t rp[kRows][E::kPer / 2];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const uint8_t* rec = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, mine, j));
+#pragma unroll
+    for (int i = 0; i < E::kSteps; ++i) {
+      const int chunk = lane + 32 * i;
+#pragma unroll
+      for (int k = 0; k < kCodes; ++k) code[j][i][k] = 0;
+      scale[j][i] = 0.f;
+      if (rec != nullptr) {
+        if constexpr (kCodes == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(rec + chunk * 8);
+          code[j][i][0] = v.x;
+          code[j][i][1] = v.y;
+        } else {
+          code[j][i][0] = *reinterpret_cast<const uint32_t*>(rec + chunk * 4);
+        }
+        scale[j][i] = *reinterpret_cast<const float*>(rec + kScaleOffset + 4 * (chunk * E::kPer / 128));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < E::kPer / 2; ++k) rp[j][k] = 0;
+    if (rec != nullptr && lane < E::kRopeLanes) {
+      if constexpr (E::kPer == 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(rec + kRopeOffset + lane * 16);
+        rp[j][0] = v.x, rp[j][1] = v.y, rp[j][2] = v.z, rp[j][3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(rec + kRopeOffset + lane * 8);
+        rp[j][0] = v.x, rp[j][1] = v.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (!((rows >> j) & 1u)) continue;  // no sequence's row
+    uint8_t* dst = latent + int64_t(base + j) * latent_stride * E::kBytes + lane * 16;
+#pragma unroll
+    for (int i = 0; i < E::kSteps; ++i) {
+      float x[E::kPer];
+#pragma unroll
+      for (int k = 0; k < kCodes; ++k) e4m3x4_to_f32(code[j][i][k], x + 4 * k);
+#pragma unroll
+      for (int k = 0; k < E::kPer; ++k) x[k] *= scale[j][i];
+      *reinterpret_cast<uint4*>(dst + i * 512) = pack<kDtype>(x);
+    }
+    if (lane < E::kRopeLanes) {
+      float x[E::kPer];
+#pragma unroll
+      for (int k = 0; k < E::kPer / 2; ++k) {
+        x[2 * k] = __uint_as_float(rp[j][k] << 16);
+        x[2 * k + 1] = __uint_as_float(rp[j][k] & 0xFFFF0000u);
+      }
+      uint4 v = pack<kDtype>(x);
+      if constexpr (kDtype == SMLA_DTYPE_BF16) v = make_uint4(rp[j][0], rp[j][1], rp[j][2], rp[j][3]);  // bit for bit
+      *reinterpret_cast<uint4*>(rope + int64_t(base + j) * rope_stride * E::kBytes + lane * 16) = v;
+    }
+  }
+}
+
+// Rows per warp: enough warps to spread a small batch over the GPU, several
+// rows of loads in flight per warp for a large one.
+constexpr int kManyRows = 4;
+constexpr int64_t kFewRowsLimit = 152 * kWarps;
+
+template <int kRows>
+unsigned grid_of(const PagedArgs& a) {
+  return unsigned((int64_t(a.n_rows) + kWarps * kRows - 1) / (kWarps * kRows));
+}
+
+template <int kDtype>
+void write_typed(const PagedArgs& a, const uint8_t* lat, int64_t ls, const uint8_t* rope, int64_t rs, cudaStream_t st) {
+  if (a.n_rows <= kFewRowsLimit)
+    paged_write_kernel<1, kDtype><<<grid_of<1>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+  else
+    paged_write_kernel<kManyRows, kDtype><<<grid_of<kManyRows>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+}
+
+template <int kDtype>
+void read_typed(const PagedArgs& a, uint8_t* lat, int64_t ls, uint8_t* rope, int64_t rs, cudaStream_t st) {
+  if (a.n_rows <= kFewRowsLimit)
+    paged_read_kernel<1, kDtype><<<grid_of<1>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+  else
+    paged_read_kernel<kManyRows, kDtype><<<grid_of<kManyRows>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_write(const smla_paged_batch& b, const void* latent, int64_t ls, const void* rope, int64_t rs,
+                               int32_t dtype, cudaStream_t st) {
+  const PagedArgs a = make_paged_args(b);
+  const uint8_t* l = static_cast<const uint8_t*>(latent);
+  const uint8_t* r = static_cast<const uint8_t*>(rope);
+  if (dtype == SMLA_DTYPE_BF16) write_typed<SMLA_DTYPE_BF16>(a, l, ls, r, rs, st);
+  else if (dtype == SMLA_DTYPE_F16) write_typed<SMLA_DTYPE_F16>(a, l, ls, r, rs, st);
+  else write_typed<SMLA_DTYPE_F32>(a, l, ls, r, rs, st);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_read(const smla_paged_batch& b, void* latent, int64_t ls, void* rope, int64_t rs,
+                              int32_t dtype, cudaStream_t st) {
+  const PagedArgs a = make_paged_args(b);
+  uint8_t* l = static_cast<uint8_t*>(latent);
+  uint8_t* r = static_cast<uint8_t*>(rope);
+  if (dtype == SMLA_DTYPE_BF16) read_typed<SMLA_DTYPE_BF16>(a, l, ls, r, rs, st);
+  else if (dtype == SMLA_DTYPE_F16) read_typed<SMLA_DTYPE_F16>(a, l, ls, r, rs, st);
+  else read_typed<SMLA_DTYPE_F32>(a, l, ls, r, rs, st);
+  return cudaGetLastError();
+}
+
+}  // namespace smla
