@@ -22,12 +22,17 @@
 // owns the key: it writes K locally and each V half to the CTA that needs it
 // (distributed shared memory).
 //
-// Warps (13): 0-3 softmax and epilogue, 4-11 loaders, 12 issues the MMAs of the
-// pair (one thread of the even CTA).  Per tile g (stage g & 1):
+// Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 one thread each that
+// issues MMAs (even CTA only), 15 relay.  Per tile g (stage g & 1):
 //   loaders   raw records of tile g + 1 are on their way in registers while tile
 //             g is dequantised; K when QK(g - 2) is done, V when PV(g - 2) is
-//   issuer    QK(g), then PV(g - 1): the tensor pipe works on the next scores
-//             while the softmax of this tile runs
+//   issuers   12 and 13 the even and odd K-steps of QK into two accumulators, 14
+//             PV: a thread issues a cta_group::2 MMA at most every 48 cycles
+//             (measured), three times the time that a QK step takes
+//   relay     tells the issuers that both CTAs' K and V are written.  The fence
+//             at cluster scope that this needs (V and the key flags are partly
+//             the peer's memory) takes ~1000 cycles, more with loads in flight,
+//             so neither the loaders nor the issuers wait for it
 //   softmax   a row is two threads (32 keys each) that exchange their maxima;
 //             p = 2^(x - m_ref), the reference moves (and O is rescaled in TMEM)
 //             only when a score exceeds it by more than 8, so p <= 2^8
@@ -67,8 +72,10 @@ constexpr int kCtaRows = 64;
 constexpr int kLoaderWarps = 8;
 constexpr int kKeysPerWarp = kOwnKeys / kLoaderWarps;
 constexpr int kFirstLoader = 4;
-constexpr int kIssuer = 12;
-constexpr int kAttendThreads = 13 * 32;
+constexpr int kIssuerQk = 12;  // and 13
+constexpr int kIssuerPv = 14;
+constexpr int kRelay = 15;
+constexpr int kAttendThreads = 16 * 32;
 constexpr int kStageK = 9 * kOwnKeys * 128;   // nine 64-dim blocks of 128-byte rows
 constexpr int kStageV = 4 * kTileKeys * 128;  // four 64-dim blocks
 constexpr int kVBlock = kTileKeys * 128;
@@ -79,7 +86,7 @@ constexpr int kQBlock = kCtaRows * 128;
 constexpr int kOffP = kOffQ + 9 * kQBlock;
 constexpr int kOffMisc = kOffP + kCtaRows * 128;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 256;              // two S buffers of 32 columns behind O's 256
+constexpr uint32_t kTmemS = 256;              // two S buffers of two accumulators of 32 columns behind O's 256
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
@@ -105,6 +112,7 @@ struct AttendArgs {
 
 struct Misc {
   uint64_t k_full[2], v_full[2], q_full, p_full, s_empty[2];  // used in the even CTA
+  uint64_t k_ready[2], v_ready[2];
   uint64_t qk_done[2], pv_done[2], drain, never;
   uint32_t tmem;
   int32_t dead;
@@ -141,20 +149,15 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void arrive_cluster(uint32_t mapped_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
+// Arrives on a barrier of either CTA.  Used where what it announces lies in this
+// SM's own shared or tensor memory (and, for shared memory, a proxy fence came
+// before); a release at cluster scope would cost ~1000 cycles each time.
+__device__ __forceinline__ void arrive_at(uint32_t mapped_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
 
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
+__device__ __forceinline__ void arrive_release_cluster(uint32_t mapped_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
 
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -170,9 +173,12 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// Orders this thread's shared-memory writes, in its own CTA and in its peer,
-// before later async-proxy (tensor core) reads of them.
-__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+// Orders this thread's shared-memory writes in its own CTA and in its peer
+// before later async-proxy (tensor core) reads of them.  (The fence without a
+// state space also waits for the loader's global loads in flight, ~2000 cycles.)
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
 
 __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -202,7 +208,7 @@ __device__ __noinline__ void give_up(Misc* ms, const AttendArgs& a) {
 // Waits for the phase of `bar`; false after the limit, or once the pair has
 // given up.
 __device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if ((i & 63u) == 0) {
@@ -214,7 +220,7 @@ __device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t
         return false;
       }
     }
-    if (try_wait_cluster(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
   }
 }
 
@@ -449,7 +455,6 @@ struct Raw {
 
 __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
-  const uint32_t k_full = map_to(smem_u32(ms->k_full), 0), v_full = map_to(smem_u32(ms->v_full), 0);
   const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0);
   const uint32_t v_base = map_to(base + kOffV, uint32_t(lane) >> 4);
   const uint32_t peer_flags = map_to(smem_u32(ms->flags), rank ^ 1u);
@@ -462,21 +467,33 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   bool more = units.next(a, u);
   int32_t t = more ? u.t0 : 0;
 
-  // Record address of lane j < kKeysPerWarp's key at the lookup cursor (0: none).
-  auto look_up = [&](bool& starts, Unit& first, bool& any) -> uint64_t {
-    uint64_t rec = 0;
+  // Page id and offset of lane j < kKeysPerWarp's key at the lookup cursor (id
+  // -1: none).  The id is first looked at a tile later, when the loads set out.
+  auto look_up = [&](bool& starts, Unit& first, bool& any, int32_t& id, int32_t& offset) {
+    id = -1;
     any = more;
     starts = false;
-    if (!more) return 0;
+    if (!more) return;
     starts = t == u.t0;
     if (starts) first = u;
     const int32_t pos = t * kTileKeys + int32_t(rank) * kOwnKeys + w * kKeysPerWarp + lane;
-    if (lane < kKeysPerWarp && pos < u.end) rec = reinterpret_cast<uint64_t>(record_at(a.b, u.seq, pos));
+    if (lane < kKeysPerWarp && pos < u.end) {  // (u.end lies within the table)
+      const uint32_t page = page_of(a.b, uint32_t(pos));
+      offset = pos - int32_t(page) * a.b.page_size;
+      id = int32_t(ldg_u32_now(a.b.table + int64_t(u.seq) * a.b.table_stride + page));
+    }
     if (++t == u.t1) {
       more = units.next(a, u);
       if (more) t = u.t0;
     }
-    return rec;
+  };
+  auto address = [&](int32_t id, int32_t offset) -> uint64_t {
+    if (id < 0) return 0;
+    if (id >= a.b.n_pages) {
+      if (a.b.status) atomicOr(a.b.status, SMLA_STATUS_INDEX_OOB);
+      return 0;
+    }
+    return reinterpret_cast<uint64_t>(a.b.kv) + int64_t(id) * a.b.page_stride + int64_t(offset) * kRecordBytes;
   };
   auto issue = [&](uint64_t rec, Raw& r) {
     const uint64_t rope_rec = __shfl_sync(0xffffffffu, rec, lane >> 3);
@@ -497,9 +514,11 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   Raw raw;
   Unit cur_unit, next_unit;
   bool cur_starts, next_starts, cur_any, next_any;
-  uint64_t cur_rec = look_up(cur_starts, cur_unit, cur_any);
-  issue(cur_rec, raw);
-  uint64_t next_rec = look_up(next_starts, next_unit, next_any);
+  int32_t next_id, next_offset = 0;
+  look_up(cur_starts, cur_unit, cur_any, next_id, next_offset);
+  uint64_t rec = address(next_id, next_offset);
+  issue(rec, raw);
+  look_up(next_starts, next_unit, next_any, next_id, next_offset);
   for (uint32_t g = 0; cur_any; ++g) {
     const uint32_t stage = g & 1;
     if (cur_starts) {
@@ -519,9 +538,9 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
         }
       }
       cp_async_wait_all();
-      fence_proxy_async_all();
+      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) arrive_cluster(q_full);
+      if (lane == 0) arrive_at(q_full);
     }
     // convert the landed records
     uint32_t v[kKeysPerWarp][8];
@@ -530,7 +549,7 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     for (int j = 0; j < kKeysPerWarp; ++j)
       odd |= nan_code(raw.lat[j].x) | nan_code(raw.lat[j].y) | nan_code(raw.lat[j].z) | nan_code(raw.lat[j].w) |
              (plain_scale(raw.scale[j]) ? 0u : 1u);
-    const uint32_t masked = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && cur_rec == 0);
+    const uint32_t masked = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == 0);
     uint32_t flags = masked;
     if (__any_sync(0xffffffffu, odd != 0)) {
 #pragma unroll
@@ -554,8 +573,8 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     }
     const uint4 rope = raw.rope;
     // the next tile's records set out while this one is stored
-    const bool go_on = next_any;
-    if (go_on) issue(next_rec, raw);
+    rec = address(next_id, next_offset);
+    if (next_any) issue(rec, raw);
     if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1)) return;
     {
       const uint32_t k = base + kOffK + stage * kStageK;
@@ -582,9 +601,9 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
         st_cluster_u8(peer_flags + at, flags);
       }
     }
-    fence_proxy_async_all();
+    fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) arrive_cluster(k_full + 8 * stage);
+    if (lane == 0) mbar_arrive(&ms->k_ready[stage]);
     if (g >= 2 && !warp_wait(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
     {
       const uint32_t vb = v_base + stage * kStageV + ((lane >> 2) & 3) * kVBlock;
@@ -601,42 +620,43 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
         }
       }
     }
-    fence_proxy_async_all();
+    fence_proxy_async_cluster();
     __syncwarp();
-    if (lane == 0) arrive_cluster(v_full + 8 * stage);
-    cur_rec = next_rec;
+    if (lane == 0) mbar_arrive(&ms->v_ready[stage]);
     cur_starts = next_starts;
     cur_any = next_any;
     if (next_starts) cur_unit = next_unit;
-    next_rec = look_up(next_starts, next_unit, next_any);
+    look_up(next_starts, next_unit, next_any, next_id, next_offset);
   }
 }
 
-// One thread of the even CTA.
-__device__ __forceinline__ void issuer_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem) {
+// One thread of each CTA: passes on that the CTA's loaders have written K and V.
+__device__ __forceinline__ void relay_role(const AttendArgs& a, Misc* ms) {
+  const uint32_t k_full = map_to(smem_u32(ms->k_full), 0), v_full = map_to(smem_u32(ms->v_full), 0);
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0;
+  while (units.next(a, u)) {
+    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+      const uint32_t stage = g & 1, parity = (g >> 1) & 1;
+      if (!wait_for(ms, a, &ms->k_ready[stage], parity)) return;
+      arrive_release_cluster(k_full + 8 * stage);
+      if (!wait_for(ms, a, &ms->v_ready[stage], parity)) return;
+      arrive_release_cluster(v_full + 8 * stage);
+    }
+  }
+}
+
+// One thread of the even CTA each: K-steps which, which + 2, ... of every QK.
+__device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
+                                               uint32_t which) {
   const uint64_t q0 = smem_desc(base + kOffQ, 16, 1024, kSw128);
   const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128);
-  const uint64_t p0 = smem_desc(base + kOffP, 16, 1024, kSw128);
-  const uint64_t v0 = smem_desc(base + kOffV, kVBlock, 1024, kSw128);
-  auto pv = [&](uint32_t g, bool first) -> bool {
-    const uint32_t stage = g & 1;
-    if (!wait_for(ms, a, &ms->v_full[stage], (g >> 1) & 1)) return false;
-    if (!wait_for(ms, a, &ms->p_full, g & 1)) return false;
-    tc_fence_after();
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int k = 0; k < kTileKeys / 16; ++k)
-        mma2(tmem + 128 * h, p0 + uint64_t(k * 2), v0 + uint64_t((stage * kStageV + h * 2 * kVBlock + k * 2048) >> 4),
-             kIdescPV, (first && k == 0) ? 0u : 1u);
-    commit2(&ms->pv_done[stage]);
-    return true;
-  };
   Units units;
   units.start(a, ms);
   Unit u;
   uint32_t g = 0, n_units = 0;
-  bool prev_first = false;
   while (units.next(a, u)) {
     if (!wait_for(ms, a, &ms->q_full, n_units & 1)) return;
     ++n_units;
@@ -645,17 +665,41 @@ __device__ __forceinline__ void issuer_role(const AttendArgs& a, Misc* ms, uint3
       if (!wait_for(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
       if (g >= 2 && !wait_for(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
       tc_fence_after();
-      const uint32_t d = tmem + kTmemS + 32 * stage;
+      const uint32_t d = tmem + kTmemS + 64 * stage + 32 * which;
+      const uint64_t qd = q0 + which * 2, kd = k0 + uint64_t((stage * kStageK) >> 4) + which * 2;
 #pragma unroll
-      for (int k = 0; k < kQK / 16; ++k)
-        mma2(d, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
-             k0 + uint64_t((stage * kStageK + (k >> 2) * (kOwnKeys * 128) + (k & 3) * 32) >> 4), kIdescQK, k > 0);
+      for (int k = 0; k < kQK / 16; k += 2)
+        mma2(d, qd + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
+             kd + uint64_t(((k >> 2) * (kOwnKeys * 128) + (k & 3) * 32) >> 4), kIdescQK, k > 0);
       commit2(&ms->qk_done[stage]);
-      if (g > 0 && !pv(g - 1, prev_first)) return;
-      prev_first = t == u.t0;
     }
   }
-  if (g > 0) pv(g - 1, prev_first);
+}
+
+// One thread of the even CTA: O += P V of every tile.
+__device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem) {
+  const uint64_t p0 = smem_desc(base + kOffP, 16, 1024, kSw128);
+  const uint64_t v0 = smem_desc(base + kOffV, kVBlock, 1024, kSw128);
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0;
+  while (units.next(a, u)) {
+    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+      const uint32_t stage = g & 1;
+      if (!wait_for(ms, a, &ms->v_full[stage], (g >> 1) & 1)) return;
+      if (!wait_for(ms, a, &ms->p_full, g & 1)) return;
+      tc_fence_after();
+      const uint64_t vd = v0 + uint64_t((stage * kStageV) >> 4);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 16; ++k)
+          mma2(tmem + 128 * h, p0 + uint64_t(k * 2), vd + uint64_t((h * 2 * kVBlock + k * 2048) >> 4), kIdescPV,
+               (t == u.t0 && k == 0) ? 0u : 1u);
+      commit2(&ms->pv_done[stage]);
+    }
+  }
 }
 
 __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem, uint32_t rank,
@@ -683,21 +727,25 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       const uint32_t stage = g & 1;
       wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
-      uint32_t s[32];
+      uint32_t s[64];  // the two accumulators' 32 columns
       {
         uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(s);
         uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(s + 16);
-        tmem_ld16(lane_base + kTmemS + 32 * stage, lo);
-        tmem_ld16(lane_base + kTmemS + 32 * stage + 16, hi);
+        uint32_t(&lo2)[16] = *reinterpret_cast<uint32_t(*)[16]>(s + 32);
+        uint32_t(&hi2)[16] = *reinterpret_cast<uint32_t(*)[16]>(s + 48);
+        tmem_ld16(lane_base + kTmemS + 64 * stage, lo);
+        tmem_ld16(lane_base + kTmemS + 64 * stage + 16, hi);
+        tmem_ld16(lane_base + kTmemS + 64 * stage + 32, lo2);
+        tmem_ld16(lane_base + kTmemS + 64 * stage + 48, hi2);
       }
       const uint2 flags = *reinterpret_cast<const uint2*>(&ms->flags[g & 3][8 * half]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(s_empty + 8 * stage);
+      if (lane == 0) arrive_at(s_empty + 8 * stage);
       float x[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) x[c] = __uint_as_float(s[c]) * a.scale_log2;
+      for (int c = 0; c < 32; ++c) x[c] = (__uint_as_float(s[c]) + __uint_as_float(s[32 + c])) * a.scale_log2;
       const int32_t key0 = t * kTileKeys + 32 * half;
       if (__any_sync(0xffffffffu, key0 + 32 > see)) {
 #pragma unroll
@@ -748,10 +796,10 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         st_shared_v4(p_row + (((4 * half + c) ^ (row & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-      fence_proxy_async_all();
+      fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_cluster(p_full);
+      if (lane == 0) arrive_at(p_full);
     }
     // the unit's end: row sums of the two halves, then O
     ms->lsum[warp * 32 + lane] = l;
@@ -818,15 +866,17 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ms->k_full[i], 2 * kLoaderWarps);
-      mbar_init(&ms->v_full[i], 2 * kLoaderWarps);
+      mbar_init(&ms->k_ready[i], kLoaderWarps);
+      mbar_init(&ms->v_ready[i], kLoaderWarps);
+      mbar_init(&ms->k_full[i], 2);
+      mbar_init(&ms->v_full[i], 2);
       mbar_init(&ms->s_empty[i], 8);
-      mbar_init(&ms->qk_done[i], 1);
+      mbar_init(&ms->qk_done[i], 2);
       mbar_init(&ms->pv_done[i], 1);
     }
     mbar_init(&ms->q_full, 2 * kLoaderWarps);
     mbar_init(&ms->p_full, 8);
-    mbar_init(&ms->drain, 1);
+    mbar_init(&ms->drain, 3);
     mbar_init(&ms->never, 1);
     fence_mbar_init();
     ms->dead = 0;
@@ -834,7 +884,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
     ms->stall = g_paged_stall;
     if (rank == 0) a.merge[pair * 4] = 0;
   }
-  if (warp == kIssuer) {
+  if (warp == kRelay) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms->tmem)),
                  "r"(kTmemCols)
                  : "memory");
@@ -847,10 +897,13 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   const uint32_t tmem = ms->tmem;
   if (warp < kFirstLoader) {
     softmax_role(a, ms, base, tmem, rank, pair);
-  } else if (warp < kIssuer) {
+  } else if (warp < kIssuerQk) {
     loader_role(a, ms, base, rank);
+  } else if (warp == kRelay) {
+    if ((threadIdx.x & 31) == 0) relay_role(a, ms);
   } else if (rank == 0 && (threadIdx.x & 31) == 0) {
-    issuer_role(a, ms, base, tmem);
+    if (warp == kIssuerPv) issuer_pv_role(a, ms, base, tmem);
+    else issuer_qk_role(a, ms, base, tmem, uint32_t(warp - kIssuerQk));
     // every MMA has to be complete before the tensor memory and the shared
     // memory it reads go away (also after a wait that gave up); the odd CTA
     // learns of it at the cluster barrier
@@ -864,7 +917,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == kIssuer) {
+  if (warp == kRelay) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
