@@ -189,6 +189,24 @@ __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_
       : "memory");
 }
 
+// Two f32 operations in one instruction.
+__device__ __forceinline__ void add2(float a0, float a1, float b0, float b1, float& r0, float& r1) {
+  asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, float& r0, float& r1) {
+  add2(__uint_as_float(a0), __uint_as_float(a1), __uint_as_float(b0), __uint_as_float(b1), r0, r1);
+}
+// r = x * m + c
+__device__ __forceinline__ void fma2(float x0, float x1, float m, float c, float& r0, float& r1) {
+  asm("{\n\t.reg .b64 x, m, c, r;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 m, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 r, x, m, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+      : "=f"(r0), "=f"(r1)
+      : "f"(x0), "f"(x1), "f"(m), "f"(c));
+}
+
 // Arrives once on `bar` of both CTAs when the MMAs issued so far are complete.
 __device__ __forceinline__ void commit2(uint64_t* bar) {
   asm volatile(
@@ -408,32 +426,42 @@ __device__ void find_range(const AttendArgs& a, Misc* ms, int32_t pair) {
 // Two E4M3 codes (bytes of w picked by sel into the upper byte of each half) as
 // bf16x2 of value * 2^-120: sign, exponent and mantissa are moved into place,
 // an exact multiplication by scale * 2^120 does the rest (subnormals included).
-__device__ __forceinline__ uint32_t dequant2(uint32_t w, uint32_t sel, uint32_t mul2) {
+// mag is the magnitude field alone: 0x07F0 in a half is a NaN code.
+__device__ __forceinline__ uint32_t place2(uint32_t w, uint32_t sel, uint32_t& mag) {
   const uint32_t x = __byte_perm(w, 0, sel);
-  const uint32_t y = ((x >> 4) & 0x07F007F0u) | (x & 0x80008000u);
+  mag = (x >> 4) & 0x07F007F0u;
+  return mag | (x & 0x80008000u);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(mul2));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
-// Whether a block scale takes the fast path: zero, or a power of two in
-// [2^-116, 2^7] (scale * 2^120 is then a normal bf16 power of two).
-__device__ __forceinline__ bool plain_scale(uint32_t bits) {
-  return bits == 0u || ((bits & 0x807FFFFFu) == 0u && bits >= (11u << 23) && bits <= (134u << 23));
+// Eight codes by one scale factor (a bf16x2 pair).
+__device__ __forceinline__ void dequant8(const uint2& c, uint32_t mul2, uint32_t (&v)[4], uint32_t& top) {
+  uint32_t m0, m1, m2, m3;
+  v[0] = mul_bf16x2(place2(c.x, 0x1404, m0), mul2);
+  v[1] = mul_bf16x2(place2(c.x, 0x3424, m1), mul2);
+  v[2] = mul_bf16x2(place2(c.y, 0x1404, m2), mul2);
+  v[3] = mul_bf16x2(place2(c.y, 0x3424, m3), mul2);
+  top = __vimax3_u16x2(__vimax3_u16x2(top, m0, m1), m2, m3);
 }
 
-// Whether a word of four codes holds a NaN code.
-__device__ __forceinline__ uint32_t nan_code(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+// Zero if a block scale takes the fast path: a power of two in [2^-120, 2^7]
+// (scale * 2^120 is then a normal bf16 power of two).
+__device__ __forceinline__ uint32_t odd_scale(uint32_t bits) { return (bits - (7u << 23)) & 0xC07FFFFFu; }
 
 // The general form: bf16(e4m3 * scale), values that are not finite become zero
 // and are reported.
-__device__ __forceinline__ bool dequant16_any(const uint4& c, uint32_t scale_bits, uint32_t (&v)[8]) {
+__device__ __forceinline__ bool dequant8_any(const uint2& c, uint32_t scale_bits, uint32_t (&v)[4]) {
   const float scale = __uint_as_float(scale_bits);
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? c.x : c.y;
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> (16 * (i & 1))), __NV_E4M3);
     float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     f.x = __bfloat162float(__float2bfloat16_rn(f.x * scale));
     f.y = __bfloat162float(__float2bfloat16_rn(f.y * scale));
@@ -444,11 +472,19 @@ __device__ __forceinline__ bool dequant16_any(const uint4& c, uint32_t scale_bit
   return bad;
 }
 
-// One tile's records of a loader warp, in flight or landed.
+__device__ __forceinline__ uint2 ldg_v2_now(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+
+// One tile's records of a loader warp, in flight or landed.  Lane l holds the
+// codes of dims [256 i + 8 l, + 8): a 16-byte chunk of bf16 each, and eight
+// neighbouring lanes fill a 128-byte row of K or V.
 struct Raw {
-  uint4 lat[kKeysPerWarp];      // lane l: codes of dims [16 l, 16 l + 16)
-  uint32_t scale[kKeysPerWarp];
-  uint4 rope;                   // lane l: 16 bytes of record l / 8's rope
+  uint2 lat[kKeysPerWarp][2];
+  uint32_t scale[kKeysPerWarp][2];
+  uint4 rope;  // lane l: 16 bytes of record l / 8's rope
 };
 
 // ---- roles ----
@@ -456,8 +492,16 @@ struct Raw {
 __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
   const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0);
-  const uint32_t v_base = map_to(base + kOffV, uint32_t(lane) >> 4);
   const uint32_t peer_flags = map_to(smem_u32(ms->flags), rank ^ 1u);
+  // where this lane's chunks go: row key = 4 w + j of block lane / 8, swizzled
+  // column (lane & 7) ^ (key & 7)
+  const uint32_t col = uint32_t((lane & 7) ^ ((w & 1) * 4));
+  const uint32_t k_at = base + kOffK + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
+  const uint32_t v_local = base + kOffV + (lane >> 3) * kVBlock + (rank * kOwnKeys + w * kKeysPerWarp) * 128;
+  const uint32_t v_peer = map_to(v_local, rank ^ 1u);
+  const uint32_t rope_key = w * kKeysPerWarp + (lane >> 3);
+  const uint32_t rope_at =
+      base + kOffK + 8 * (kOwnKeys * 128) + rope_key * 128 + ((uint32_t(lane & 7) ^ (rope_key & 7)) << 4);
 
   // Three cursors over the pair's tiles: addresses are looked up one tile ahead
   // of the loads, the loads run one tile ahead of the conversion.
@@ -495,19 +539,32 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     }
     return reinterpret_cast<uint64_t>(a.b.kv) + int64_t(id) * a.b.page_stride + int64_t(offset) * kRecordBytes;
   };
-  auto issue = [&](uint64_t rec, Raw& r) {
+  auto load = [&](const uint8_t* p, int j, Raw& r) {
+    r.lat[j][0] = ldg_v2_now(p + lane * 8);
+    r.lat[j][1] = ldg_v2_now(p + lane * 8 + 256);
+    r.scale[j][0] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4));
+    r.scale[j][1] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4) + 8);
+  };
+  // rec: lane j's record; masked: the keys without one
+  auto issue = [&](uint64_t rec, uint32_t masked, Raw& r) {
+    const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
+    const uint64_t run = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == first + uint64_t(lane) * kRecordBytes);
+    if (masked == 0 && run == (1u << kKeysPerWarp) - 1) {  // all in a row, as in pages of a multiple of 4 records
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(first);
+#pragma unroll
+      for (int j = 0; j < kKeysPerWarp; ++j) load(p + j * kRecordBytes, j, r);
+      r.rope = ldg_v4_now(p + (lane >> 3) * kRecordBytes + kRopeOffset + (lane & 7) * 16);
+      return;
+    }
     const uint64_t rope_rec = __shfl_sync(0xffffffffu, rec, lane >> 3);
     r.rope = make_uint4(0, 0, 0, 0);
     if (rope_rec) r.rope = ldg_v4_now(reinterpret_cast<const uint8_t*>(rope_rec) + kRopeOffset + (lane & 7) * 16);
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j) {
       const uint64_t p = __shfl_sync(0xffffffffu, rec, j);
-      r.lat[j] = make_uint4(0, 0, 0, 0);
-      r.scale[j] = 0;
-      if (p) {
-        r.lat[j] = ldg_v4_now(reinterpret_cast<const uint8_t*>(p) + lane * 16);
-        r.scale[j] = ldg_u32_now(reinterpret_cast<const uint8_t*>(p) + kScaleOffset + 4 * (lane >> 3));
-      }
+      r.lat[j][0] = r.lat[j][1] = make_uint2(0, 0);
+      r.scale[j][0] = r.scale[j][1] = 0x3F800000u;  // zeros by the fast path
+      if (p) load(reinterpret_cast<const uint8_t*>(p), j, r);
     }
   };
 
@@ -517,13 +574,24 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   int32_t next_id, next_offset = 0;
   look_up(cur_starts, cur_unit, cur_any, next_id, next_offset);
   uint64_t rec = address(next_id, next_offset);
-  issue(rec, raw);
+  uint32_t masked = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == 0), masked_next = 0;
+  issue(rec, masked, raw);
   look_up(next_starts, next_unit, next_any, next_id, next_offset);
   for (uint32_t g = 0; cur_any; ++g) {
     const uint32_t stage = g & 1;
+    // V of tile g - 1 is announced here: its stores to the peer have had the time
+    // of a conversion to land, so that the fence does not wait for them
+    auto announce_v = [&]() {
+      fence_proxy_async_cluster();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->v_ready[stage ^ 1]);
+    };
     if (cur_starts) {
-      // q of the unit, once the last QK of the unit before is done
-      if (g > 0 && !warp_wait(ms, a, &ms->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return;
+      if (g > 0) {
+        announce_v();
+        // q of the unit, once the last QK of the unit before is done
+        if (!warp_wait(ms, a, &ms->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return;
+      }
       const int32_t rows = cur_unit.tokens * a.heads;
       for (int i = w; i < kCtaRows; i += kLoaderWarps) {
         const int32_t m = int32_t(rank) * kCtaRows + i;
@@ -543,86 +611,69 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
       if (lane == 0) arrive_at(q_full);
     }
     // convert the landed records
-    uint32_t v[kKeysPerWarp][8];
-    uint32_t odd = 0;
+    uint32_t v[kKeysPerWarp][2][4];
+    uint32_t odd = 0, top = 0;
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j)
-      odd |= nan_code(raw.lat[j].x) | nan_code(raw.lat[j].y) | nan_code(raw.lat[j].z) | nan_code(raw.lat[j].w) |
-             (plain_scale(raw.scale[j]) ? 0u : 1u);
-    const uint32_t masked = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == 0);
-    uint32_t flags = masked;
-    if (__any_sync(0xffffffffu, odd != 0)) {
 #pragma unroll
-      for (int j = 0; j < kKeysPerWarp; ++j) {
-        const bool bad = dequant16_any(raw.lat[j], raw.scale[j], v[j]);
-        if (__any_sync(0xffffffffu, bad)) flags |= 16u << j;
+      for (int i = 0; i < 2; ++i) {
+        odd |= odd_scale(raw.scale[j][i]);
+        const uint32_t mul2 = __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232);
+        dequant8(raw.lat[j][i], mul2, v[j][i], top);
       }
-    } else {
+    uint32_t flags = masked;
+    const bool nan = (top & 0xFFFFu) == 0x07F0u || (top >> 16) == 0x07F0u;
+    if (__any_sync(0xffffffffu, odd != 0 || nan)) {
 #pragma unroll
       for (int j = 0; j < kKeysPerWarp; ++j) {
-        // scale * 2^120 as a bf16 pair (0 stays 0)
-        const uint32_t s = raw.scale[j] ? (raw.scale[j] + (120u << 23)) >> 16 : 0u;
-        const uint32_t mul2 = s | (s << 16);
-        const uint32_t c[4] = {raw.lat[j].x, raw.lat[j].y, raw.lat[j].z, raw.lat[j].w};
+        bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[j][2 * i] = dequant2(c[i], 0x1404, mul2);
-          v[j][2 * i + 1] = dequant2(c[i], 0x3424, mul2);
-        }
+        for (int i = 0; i < 2; ++i) bad |= dequant8_any(raw.lat[j][i], raw.scale[j][i], v[j][i]);
+        if (__any_sync(0xffffffffu, bad)) flags |= 16u << j;
       }
     }
     const uint4 rope = raw.rope;
     // the next tile's records set out while this one is stored
     rec = address(next_id, next_offset);
-    if (next_any) issue(rec, raw);
+    masked_next = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == 0);
+    if (next_any) issue(rec, masked_next, raw);
+    if (g > 0 && !cur_starts) announce_v();
     if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1)) return;
-    {
-      const uint32_t k = base + kOffK + stage * kStageK;
+    const uint32_t k = k_at + stage * kStageK;
 #pragma unroll
-      for (int j = 0; j < kKeysPerWarp; ++j) {
-        const int key = w * kKeysPerWarp + j;
-        const uint32_t row = k + (lane >> 2) * (kOwnKeys * 128) + key * 128;
-        // lanes of neighbouring blocks store their two chunks in turns: all eight
-        // 16-byte columns of a quarter warp differ
-        const int flip = (lane >> 2) & 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = i ^ flip;
-          const uint32_t at = row + ((((lane & 3) * 2 + c) ^ (key & 7)) << 4);
-          st_shared_v4(at, c ? v[j][4] : v[j][0], c ? v[j][5] : v[j][1], c ? v[j][6] : v[j][2], c ? v[j][7] : v[j][3]);
-        }
-      }
-      const int key = w * kKeysPerWarp + (lane >> 3);
-      st_shared_v4(k + 8 * (kOwnKeys * 128) + key * 128 + (((lane & 7) ^ (key & 7)) << 4), rope.x, rope.y, rope.z,
-                   rope.w);
-      if (lane == 0) {
-        const uint32_t at = (g & 3) * (2 * kLoaderWarps) + rank * kLoaderWarps + w;
-        ms->flags[0][at] = uint8_t(flags);
-        st_cluster_u8(peer_flags + at, flags);
-      }
+    for (int j = 0; j < kKeysPerWarp; ++j) {
+      const uint32_t at = k + j * 128 + ((col ^ j) << 4);
+      st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
+      st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
+    }
+    st_shared_v4(rope_at + stage * kStageK, rope.x, rope.y, rope.z, rope.w);
+    if (lane == 0) {
+      const uint32_t at = (g & 3) * (2 * kLoaderWarps) + rank * kLoaderWarps + w;
+      ms->flags[0][at] = uint8_t(flags);
+      st_cluster_u8(peer_flags + at, flags);
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms->k_ready[stage]);
     if (g >= 2 && !warp_wait(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
-    {
-      const uint32_t vb = v_base + stage * kStageV + ((lane >> 2) & 3) * kVBlock;
+    // the even CTA's PV takes dims [0, 256), the odd one's the rest
 #pragma unroll
-      for (int j = 0; j < kKeysPerWarp; ++j) {
-        const int key = int(rank) * kOwnKeys + w * kKeysPerWarp + j;
-        const int flip = (lane >> 2) & 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int c = i ^ flip;
-          const uint32_t at = vb + key * 128 + ((((lane & 3) * 2 + c) ^ (key & 7)) << 4);
-          st_cluster_v4(at, c ? v[j][4] : v[j][0], c ? v[j][5] : v[j][1], c ? v[j][6] : v[j][2],
-                        c ? v[j][7] : v[j][3]);
-        }
+    for (int j = 0; j < kKeysPerWarp; ++j) {
+      const uint32_t off = stage * kStageV + j * 128 + ((col ^ j) << 4);
+      if (rank == 0) {
+        st_cluster_v4(v_peer + off, v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
+        st_shared_v4(v_local + off, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
+      } else {
+        st_cluster_v4(v_peer + off, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
+        st_shared_v4(v_local + off, v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
       }
     }
-    fence_proxy_async_cluster();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&ms->v_ready[stage]);
+    if (!next_any) {  // the last tile
+      fence_proxy_async_cluster();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->v_ready[stage]);
+    }
+    masked = masked_next;
     cur_starts = next_starts;
     cur_any = next_any;
     if (next_starts) cur_unit = next_unit;
@@ -712,6 +763,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   const uint32_t lane_base = tmem + (uint32_t(warp) << 21);  // lane 32 warp
   const uint32_t p_full = map_to(smem_u32(&ms->p_full), 0), s_empty = map_to(smem_u32(ms->s_empty), 0);
   const uint32_t p_row = base + kOffP + row * 128;
+  // scores are scaled after the mask and the maximum, so the factor has to be positive
+  const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
   Units units;
   units.start(a, ms);
   Unit u;
@@ -743,9 +796,14 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(s_empty + 8 * stage);
-      float x[32];
+      float x[32];  // scores before the scale (times its sign)
 #pragma unroll
-      for (int c = 0; c < 32; ++c) x[c] = (__uint_as_float(s[c]) + __uint_as_float(s[32 + c])) * a.scale_log2;
+      for (int c = 0; c < 32; c += 2) add2(s[c], s[c + 1], s[32 + c], s[33 + c], x[c], x[c + 1]);
+      if (a.scale_log2 <= 0.f) {
+        const float by = a.scale_log2 < 0.f ? -1.f : 0.f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] *= by;
+      }
       const int32_t key0 = t * kTileKeys + 32 * half;
       if (__any_sync(0xffffffffu, key0 + 32 > see)) {
 #pragma unroll
@@ -764,21 +822,24 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       for (int c = 1; c < 32; ++c) tm = fmaxf(tm, x[c]);
       ms->tmax[stage][warp * 32 + lane] = tm;
       named_barrier(1 + (warp & 1), 64);
-      tm = fmaxf(tm, ms->tmax[stage][(warp ^ 2) * 32 + lane]);
+      tm = fmaxf(tm, ms->tmax[stage][(warp ^ 2) * 32 + lane]) * scale;
       const bool move = tm > ref + kMoveMargin;
       const float nref = move ? tm : ref;
       const float use = nref == -INFINITY ? 0.f : nref;
       const float alpha = move ? ex2(ref - use) : 1.f;
       ref = nref;
       uint32_t p[16];
-      float sum = 0.f;
+      float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
       for (int c = 0; c < 16; ++c) {
-        const float p0 = ex2(x[2 * c] - use), p1 = ex2(x[2 * c + 1] - use);
-        sum += p0 + p1;
-        p[c] = pack_bf16x2(p0, p1);  // P as the product's bf16 operand; the sum keeps f32
+        float y0, y1;
+        fma2(x[2 * c], x[2 * c + 1], scale, -use, y0, y1);
+        y0 = ex2(y0);
+        y1 = ex2(y1);
+        add2(sum0, sum1, y0, y1, sum0, sum1);
+        p[c] = pack_bf16x2(y0, y1);  // P as the product's bf16 operand; the sum keeps f32
       }
-      l = l * alpha + sum;
+      l = l * alpha + (sum0 + sum1);
       if (g > 0) wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
       if (t > u.t0 && __any_sync(0xffffffffu, move)) {
         tc_fence_after();

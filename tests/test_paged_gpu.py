@@ -295,8 +295,9 @@ def test_attend_sharp_softmax_moves_the_reference():
     c = Batch([(6, 700), (1, 1500)], 64, std=3.0)
     q, sk, out, lse, _ = attend(c, 16, sm_scale=1.0, sink=True)
     check(c, q, out, lse, 1.0, sk, True)
-    q, sk, out, lse, _ = attend(c, 16, sm_scale=-0.3)
-    check(c, q, out, lse, -0.3, sk, True)
+    for scale in (-0.3, 0.0):
+        q, sk, out, lse, _ = attend(c, 16, sm_scale=scale)
+        check(c, q, out, lse, scale, sk, True)
 
 
 def test_attend_rows_without_keys():
