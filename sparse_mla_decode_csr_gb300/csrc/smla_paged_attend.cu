@@ -19,20 +19,18 @@
 // each CTA supplies half of the N extent: its own 32 keys of the tile for QK
 // ("K": 32 x 576), and its own 256 value dims of all 64 keys for PV ("V": 64 x
 // 256, MN-major).  Every record is read and dequantised once, by the CTA that
-// owns the key: it writes K locally and each V half to the CTA that needs it
-// (distributed shared memory).
+// owns the key, into K; bulk copies take K's latent blocks to the V of the CTA
+// that needs them, its own or its peer's (both are 128-byte-swizzled rows of 64
+// dims, so a 32-key block is one contiguous piece of 4 KB).
 //
 // Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 one thread each that
-// issues MMAs (even CTA only), 15 relay.  Per tile g (stage g & 1):
+// issues MMAs (even CTA only), 15 copier.  Per tile g (stage g & 1):
 //   loaders   raw records of tile g + 1 are on their way in registers while tile
-//             g is dequantised; K when QK(g - 2) is done, V when PV(g - 2) is
+//             g is dequantised; K when QK(g - 2) and the copies out of it are done
+//   copier    one thread: K -> V of both CTAs when PV(g - 2) is done
 //   issuers   12 and 13 the even and odd K-steps of QK into two accumulators, 14
 //             PV: a thread issues a cta_group::2 MMA at most every 48 cycles
 //             (measured), three times the time that a QK step takes
-//   relay     tells the issuers that both CTAs' K and V are written.  The fence
-//             at cluster scope that this needs (V and the key flags are partly
-//             the peer's memory) takes ~1000 cycles, more with loads in flight,
-//             so neither the loaders nor the issuers wait for it
 //   softmax   a row is two threads (32 keys each) that exchange their maxima;
 //             p = 2^(x - m_ref), the reference moves (and O is rescaled in TMEM)
 //             only when a score exceeds it by more than 8, so p <= 2^8
@@ -74,7 +72,7 @@ constexpr int kKeysPerWarp = kOwnKeys / kLoaderWarps;
 constexpr int kFirstLoader = 4;
 constexpr int kIssuerQk = 12;  // and 13
 constexpr int kIssuerPv = 14;
-constexpr int kRelay = 15;
+constexpr int kCopier = 15;
 constexpr int kAttendThreads = 16 * 32;
 constexpr int kStageK = 9 * kOwnKeys * 128;   // nine 64-dim blocks of 128-byte rows
 constexpr int kStageV = 4 * kTileKeys * 128;  // four 64-dim blocks
@@ -111,8 +109,8 @@ struct AttendArgs {
 };
 
 struct Misc {
-  uint64_t k_full[2], v_full[2], q_full, p_full, s_empty[2];  // used in the even CTA
-  uint64_t k_ready[2], v_ready[2];
+  uint64_t k_full[2], q_full, p_full, s_empty[2];  // used in the even CTA
+  uint64_t k_ready[2], v_land[2], v_full[2];
   uint64_t qk_done[2], pv_done[2], drain, never;
   uint32_t tmem;
   int32_t dead;
@@ -123,8 +121,8 @@ struct Misc {
   int64_t warp_sum[kAttendThreads / 32];
   float tmax[2][128];
   float lsum[128];
-  // per tile: a byte per loader warp of the pair, bits 0-3 keys that are masked
-  // (no record), bits 4-7 keys whose latent is not finite
+  // per tile: a byte per loader warp of the pair, bits 0-3: keys before the end
+  // that have no record
   uint8_t flags[4][2 * kLoaderWarps];
 };
 static_assert(sizeof(Misc) <= 2816, "shared memory");
@@ -149,35 +147,24 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Arrives on a barrier of either CTA.  Used where what it announces lies in this
-// SM's own shared or tensor memory (and, for shared memory, a proxy fence came
-// before); a release at cluster scope would cost ~1000 cycles each time.
+// Arrives on a barrier of either CTA.  What it announces lies in this SM's own
+// shared or tensor memory (and, for shared memory, a proxy fence came before), so
+// no release at cluster scope is made: that would cost ~1000 cycles each time.
 __device__ __forceinline__ void arrive_at(uint32_t mapped_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
 }
 
-__device__ __forceinline__ void arrive_release_cluster(uint32_t mapped_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
-}
-
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
-
-__device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Copy of `bytes` from this CTA's shared memory to either CTA's, completing on
+// the barrier there.
+__device__ __forceinline__ void bulk_s2s(uint32_t mapped_dst, uint32_t src, uint32_t bytes, uint32_t mapped_bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(mapped_dst),
+      "r"(src), "r"(bytes), "r"(mapped_bar)
+      : "memory");
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// Orders this thread's shared-memory writes in its own CTA and in its peer
-// before later async-proxy (tensor core) reads of them.  (The fence without a
-// state space also waits for the loader's global loads in flight, ~2000 cycles.)
-__device__ __forceinline__ void fence_proxy_async_cluster() {
-  asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
 __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -491,14 +478,11 @@ struct Raw {
 
 __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
-  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0);
-  const uint32_t peer_flags = map_to(smem_u32(ms->flags), rank ^ 1u);
+  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0);
   // where this lane's chunks go: row key = 4 w + j of block lane / 8, swizzled
   // column (lane & 7) ^ (key & 7)
   const uint32_t col = uint32_t((lane & 7) ^ ((w & 1) * 4));
   const uint32_t k_at = base + kOffK + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
-  const uint32_t v_local = base + kOffV + (lane >> 3) * kVBlock + (rank * kOwnKeys + w * kKeysPerWarp) * 128;
-  const uint32_t v_peer = map_to(v_local, rank ^ 1u);
   const uint32_t rope_key = w * kKeysPerWarp + (lane >> 3);
   const uint32_t rope_at =
       base + kOffK + 8 * (kOwnKeys * 128) + rope_key * 128 + ((uint32_t(lane & 7) ^ (rope_key & 7)) << 4);
@@ -511,20 +495,25 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   bool more = units.next(a, u);
   int32_t t = more ? u.t0 : 0;
 
-  // Page id and offset of lane j < kKeysPerWarp's key at the lookup cursor (id
-  // -1: none).  The id is first looked at a tile later, when the loads set out.
+  // Page id and offset at the lookup cursor: lanes 0-3 this warp's keys, lanes
+  // 4-7 the peer warp's (both CTAs need to know which keys have no record).  The
+  // id is first looked at a tile later, when the loads set out; kPast: a key at
+  // or after the end.
+  constexpr int32_t kPast = INT32_MIN;
   auto look_up = [&](bool& starts, Unit& first, bool& any, int32_t& id, int32_t& offset) {
-    id = -1;
+    id = kPast;
     any = more;
     starts = false;
     if (!more) return;
     starts = t == u.t0;
     if (starts) first = u;
-    const int32_t pos = t * kTileKeys + int32_t(rank) * kOwnKeys + w * kKeysPerWarp + lane;
-    if (lane < kKeysPerWarp && pos < u.end) {  // (u.end lies within the table)
+    const int32_t owner = int32_t(rank) ^ (lane >> 2);
+    const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 3);
+    if (lane < 2 * kKeysPerWarp && pos < u.end) {  // (u.end lies within the table)
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
       id = int32_t(ldg_u32_now(a.b.table + int64_t(u.seq) * a.b.table_stride + page));
+      if (id == kPast) id = -1;
     }
     if (++t == u.t1) {
       more = units.next(a, u);
@@ -545,11 +534,12 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     r.scale[j][0] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4));
     r.scale[j][1] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4) + 8);
   };
-  // rec: lane j's record; masked: the keys without one
-  auto issue = [&](uint64_t rec, uint32_t masked, Raw& r) {
+  // rec: lane j's record (0: none)
+  auto issue = [&](uint64_t rec, Raw& r) {
     const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
-    const uint64_t run = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == first + uint64_t(lane) * kRecordBytes);
-    if (masked == 0 && run == (1u << kKeysPerWarp) - 1) {  // all in a row, as in pages of a multiple of 4 records
+    const uint32_t run = __ballot_sync(
+        0xffffffffu, lane >= kKeysPerWarp || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
+    if (run == 0xffffffffu) {  // all in a row, as in pages of a multiple of 4 records
       const uint8_t* p = reinterpret_cast<const uint8_t*>(first);
 #pragma unroll
       for (int j = 0; j < kKeysPerWarp; ++j) load(p + j * kRecordBytes, j, r);
@@ -574,24 +564,14 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   int32_t next_id, next_offset = 0;
   look_up(cur_starts, cur_unit, cur_any, next_id, next_offset);
   uint64_t rec = address(next_id, next_offset);
-  uint32_t masked = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == 0), masked_next = 0;
-  issue(rec, masked, raw);
+  uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && next_id != kPast);
+  issue(rec, raw);
   look_up(next_starts, next_unit, next_any, next_id, next_offset);
   for (uint32_t g = 0; cur_any; ++g) {
     const uint32_t stage = g & 1;
-    // V of tile g - 1 is announced here: its stores to the peer have had the time
-    // of a conversion to land, so that the fence does not wait for them
-    auto announce_v = [&]() {
-      fence_proxy_async_cluster();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->v_ready[stage ^ 1]);
-    };
     if (cur_starts) {
-      if (g > 0) {
-        announce_v();
-        // q of the unit, once the last QK of the unit before is done
-        if (!warp_wait(ms, a, &ms->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return;
-      }
+      // q of the unit, once the last QK of the unit before is done
+      if (g > 0 && !warp_wait(ms, a, &ms->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return;
       const int32_t rows = cur_unit.tokens * a.heads;
       for (int i = w; i < kCtaRows; i += kLoaderWarps) {
         const int32_t m = int32_t(rank) * kCtaRows + i;
@@ -621,7 +601,7 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
         const uint32_t mul2 = __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232);
         dequant8(raw.lat[j][i], mul2, v[j][i], top);
       }
-    uint32_t flags = masked;
+    uint4 rope = raw.rope;
     const bool nan = (top & 0xFFFFu) == 0x07F0u || (top >> 16) == 0x07F0u;
     if (__any_sync(0xffffffffu, odd != 0 || nan)) {
 #pragma unroll
@@ -629,16 +609,20 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) bad |= dequant8_any(raw.lat[j][i], raw.scale[j][i], v[j][i]);
-        if (__any_sync(0xffffffffu, bad)) flags |= 16u << j;
+        // a latent that is not finite is zero in V, where rows that may not see the
+        // key would meet it as 0 * NaN, and a NaN in the key's rope, which V lacks:
+        // its scores are NaN, and the mask drops them
+        if (__any_sync(0xffffffffu, bad) && lane == 8 * j) rope.x = 0x7FC07FC0u;
       }
     }
-    const uint4 rope = raw.rope;
+    const uint32_t cur_holes = holes;
     // the next tile's records set out while this one is stored
     rec = address(next_id, next_offset);
-    masked_next = __ballot_sync(0xffffffffu, lane < kKeysPerWarp && rec == 0);
-    if (next_any) issue(rec, masked_next, raw);
-    if (g > 0 && !cur_starts) announce_v();
-    if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1)) return;
+    holes = __ballot_sync(0xffffffffu, rec == 0 && next_id != kPast);
+    if (next_any) issue(rec, raw);
+    if (g >= 2 && (!warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1) ||
+                   !warp_wait(ms, a, &ms->v_full[stage], ((g - 2) >> 1) & 1)))
+      return;
     const uint32_t k = k_at + stage * kStageK;
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j) {
@@ -647,33 +631,13 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
       st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
     }
     st_shared_v4(rope_at + stage * kStageK, rope.x, rope.y, rope.z, rope.w);
-    if (lane == 0) {
-      const uint32_t at = (g & 3) * (2 * kLoaderWarps) + rank * kLoaderWarps + w;
-      ms->flags[0][at] = uint8_t(flags);
-      st_cluster_u8(peer_flags + at, flags);
-    }
+    if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t((cur_holes >> (4 * lane)) & 15u);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&ms->k_ready[stage]);
-    if (g >= 2 && !warp_wait(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
-    // the even CTA's PV takes dims [0, 256), the odd one's the rest
-#pragma unroll
-    for (int j = 0; j < kKeysPerWarp; ++j) {
-      const uint32_t off = stage * kStageV + j * 128 + ((col ^ j) << 4);
-      if (rank == 0) {
-        st_cluster_v4(v_peer + off, v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
-        st_shared_v4(v_local + off, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
-      } else {
-        st_cluster_v4(v_peer + off, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
-        st_shared_v4(v_local + off, v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
-      }
+    if (lane == 0) {
+      mbar_arrive(&ms->k_ready[stage]);
+      arrive_at(k_full + 8 * stage);
     }
-    if (!next_any) {  // the last tile
-      fence_proxy_async_cluster();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ms->v_ready[stage]);
-    }
-    masked = masked_next;
     cur_starts = next_starts;
     cur_any = next_any;
     if (next_starts) cur_unit = next_unit;
@@ -681,9 +645,17 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   }
 }
 
-// One thread of each CTA: passes on that the CTA's loaders have written K and V.
-__device__ __forceinline__ void relay_role(const AttendArgs& a, Misc* ms) {
-  const uint32_t k_full = map_to(smem_u32(ms->k_full), 0), v_full = map_to(smem_u32(ms->v_full), 0);
+// One thread of each CTA: copies the latent blocks of K to V, dims [0, 256) to the
+// even CTA's and the rest to the odd one's, and tells both CTAs when its V is
+// complete (PV may read it, the loaders may overwrite the K it came from).
+__device__ __forceinline__ void copier_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
+  uint32_t land[2], full[2], v_at[2];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    land[r] = map_to(smem_u32(ms->v_land), r);
+    full[r] = map_to(smem_u32(ms->v_full), r);
+    v_at[r] = map_to(base + kOffV + rank * (kOwnKeys * 128), r);
+  }
   Units units;
   units.start(a, ms);
   Unit u;
@@ -692,9 +664,21 @@ __device__ __forceinline__ void relay_role(const AttendArgs& a, Misc* ms) {
     for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
       const uint32_t stage = g & 1, parity = (g >> 1) & 1;
       if (!wait_for(ms, a, &ms->k_ready[stage], parity)) return;
-      arrive_release_cluster(k_full + 8 * stage);
-      if (!wait_for(ms, a, &ms->v_ready[stage], parity)) return;
-      arrive_release_cluster(v_full + 8 * stage);
+      if (g >= 2 && !wait_for(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
+      mbar_arrive_expect_tx(&ms->v_land[stage], kStageV);
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          bulk_s2s(v_at[r] + stage * kStageV + b * kVBlock, base + kOffK + stage * kStageK + (4 * r + b) * (kOwnKeys * 128),
+                   kOwnKeys * 128, land[r] + 8 * stage);
+      // (the limit of its own: copies in flight are waited for after a give-up too)
+      if (!mbar_wait(&ms->v_land[stage], parity, kWaitNs)) {
+        give_up(ms, a);
+        return;
+      }
+      arrive_at(full[0] + 8 * stage);
+      arrive_at(full[1] + 8 * stage);
     }
   }
 }
@@ -814,7 +798,6 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
         for (int c = 0; c < 32; ++c) {
           const uint32_t f = ((c < 16 ? flags.x : flags.y) >> (8 * ((c >> 2) & 3))) >> (c & 3);
           if (f & 1u) x[c] = -INFINITY;
-          else if ((f & 16u) && key0 + c < see) x[c] = __uint_as_float(0x7FC00000u);
         }
       }
       float tm = x[0];
@@ -928,8 +911,8 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->k_ready[i], kLoaderWarps);
-      mbar_init(&ms->v_ready[i], kLoaderWarps);
-      mbar_init(&ms->k_full[i], 2);
+      mbar_init(&ms->k_full[i], 2 * kLoaderWarps);
+      mbar_init(&ms->v_land[i], 1);
       mbar_init(&ms->v_full[i], 2);
       mbar_init(&ms->s_empty[i], 8);
       mbar_init(&ms->qk_done[i], 2);
@@ -945,7 +928,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
     ms->stall = g_paged_stall;
     if (rank == 0) a.merge[pair * 4] = 0;
   }
-  if (warp == kRelay) {
+  if (warp == kCopier) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ms->tmem)),
                  "r"(kTmemCols)
                  : "memory");
@@ -960,8 +943,8 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
     softmax_role(a, ms, base, tmem, rank, pair);
   } else if (warp < kIssuerQk) {
     loader_role(a, ms, base, rank);
-  } else if (warp == kRelay) {
-    if ((threadIdx.x & 31) == 0) relay_role(a, ms);
+  } else if (warp == kCopier) {
+    if ((threadIdx.x & 31) == 0) copier_role(a, ms, base, rank);
   } else if (rank == 0 && (threadIdx.x & 31) == 0) {
     if (warp == kIssuerPv) issuer_pv_role(a, ms, base, tmem);
     else issuer_qk_role(a, ms, base, tmem, uint32_t(warp - kIssuerQk));
@@ -978,7 +961,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == kRelay) {
+  if (warp == kCopier) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   }
