@@ -25,8 +25,10 @@
 //
 // Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 one thread each that
 // issues MMAs (even CTA only), 15 copier.  Per tile g (stage g & 1):
-//   loaders   raw records of tile g + 1 are on their way in registers while tile
-//             g is dequantised; K when QK(g - 2) and the copies out of it are done
+//   loaders   two groups of four warps take turns at the tiles, a warp 8 of the
+//             CTA's 32 keys in two batches; the next batch's records are on their
+//             way in registers while one is dequantised; K is written when QK(g - 2)
+//             and the copies out of it are done
 //   copier    one thread: K -> V of both CTAs when PV(g - 2) is done
 //   issuers   12 and 13 the even and odd K-steps of QK into two accumulators, 14
 //             PV: a thread issues a cta_group::2 MMA at most every 48 cycles
@@ -67,8 +69,9 @@ constexpr int kTileKeys = 64;
 constexpr int kOwnKeys = 32;      // keys of a tile that one CTA of the pair loads
 constexpr int kPairRows = 128;
 constexpr int kCtaRows = 64;
-constexpr int kLoaderWarps = 8;
+constexpr int kLoaderWarps = 4;   // of each of the two loader groups
 constexpr int kKeysPerWarp = kOwnKeys / kLoaderWarps;
+constexpr int kBatch = 4;         // keys that a loader warp converts at a time
 constexpr int kFirstLoader = 4;
 constexpr int kIssuerQk = 12;  // and 13
 constexpr int kIssuerPv = 14;
@@ -121,9 +124,8 @@ struct Misc {
   int64_t warp_sum[kAttendThreads / 32];
   float tmax[2][128];
   float lsum[128];
-  // per tile: a byte per loader warp of the pair, bits 0-3: keys before the end
-  // that have no record
-  uint8_t flags[4][2 * kLoaderWarps];
+  // per tile: a byte per 8 keys, bit: a key before the end that has no record
+  uint8_t flags[4][kTileKeys / 8];
 };
 static_assert(sizeof(Misc) <= 2816, "shared memory");
 constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc)) + 1024;
@@ -152,6 +154,19 @@ __device__ __forceinline__ void cluster_sync() {
 // no release at cluster scope is made: that would cost ~1000 cycles each time.
 __device__ __forceinline__ void arrive_at(uint32_t mapped_bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped_bar) : "memory");
+}
+
+// Whether the phase of `bar` is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // Copy of `bytes` from this CTA's shared memory to either CTA's, completing on
@@ -204,16 +219,16 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
 }
 
 // Gives up the pipeline of both CTAs (see wait_for).
-__device__ __noinline__ void give_up(Misc* ms, const AttendArgs& a) {
-  if (atomicExch(&ms->dead, 1) == 0 && a.b.status) atomicOr(a.b.status, SMLA_STATUS_TIMEOUT);
+__device__ __noinline__ void give_up(Misc* ms, int32_t* status) {
+  if (atomicExch(&ms->dead, 1) == 0 && status) atomicOr(status, SMLA_STATUS_TIMEOUT);
   const uint32_t other = map_to(smem_u32(&ms->dead), cluster_rank() ^ 1u);
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(other), "r"(1) : "memory");
 }
 
 // Waits for the phase of `bar`; false after the limit, or once the pair has
-// given up.
-__device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+// given up.  (Out of line, like everything that a tile does not go through: the
+// roles' loops compete for the instruction cache.)
+__device__ __noinline__ bool wait_on(Misc* ms, int32_t* status, uint64_t* bar, uint32_t parity) {
   uint64_t t0 = 0;
   for (uint32_t i = 0;; ++i) {
     if ((i & 63u) == 0) {
@@ -221,12 +236,16 @@ __device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t
       const uint64_t t = globaltimer();
       if (t0 == 0) t0 = t;
       if (t - t0 > ms->wait_ns) {
-        give_up(ms, a);
+        give_up(ms, status);
         return false;
       }
     }
     if (mbar_try_wait(bar, parity)) return true;
   }
+}
+
+__device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
+  return mbar_try_wait(bar, parity) || wait_on(ms, a.b.status, bar, parity);
 }
 
 // The same for a whole warp: one answer for all lanes.
@@ -329,7 +348,7 @@ struct Units {
   }
 
   // The next unit of this pair; false when there is none.
-  __device__ __forceinline__ bool next(const AttendArgs& a, Unit& u) {
+  __device__ __noinline__ bool next(const AttendArgs& a, Unit& u) {
     while (slot < end && seq < a.b.n_seqs) {
       if (j >= s.tiles) {
         j = 0;
@@ -410,14 +429,21 @@ __device__ void find_range(const AttendArgs& a, Misc* ms, int32_t pair) {
 
 // ---- dequantisation ----
 
-// Two E4M3 codes (bytes of w picked by sel into the upper byte of each half) as
+// Two E4M3 codes (bytes of w picked by sel into the lower byte of each half) as
 // bf16x2 of value * 2^-120: sign, exponent and mantissa are moved into place,
-// an exact multiplication by scale * 2^120 does the rest (subnormals included).
-// mag is the magnitude field alone: 0x07F0 in a half is a NaN code.
+//   16 m + 256 (x - m) = 256 x - 240 m,  m = x & 0x7F,
+// by multiplications, since the shifts and logic of the usual form alone keep
+// the ALU pipe busy longer than the tensor work of a tile lasts; an exact product
+// with scale * 2^120 does the rest (subnormals included).  mag returns m, which
+// is 0x7F for a NaN code.
 __device__ __forceinline__ uint32_t place2(uint32_t w, uint32_t sel, uint32_t& mag) {
   const uint32_t x = __byte_perm(w, 0, sel);
-  mag = (x >> 4) & 0x07F007F0u;
-  return mag | (x & 0x80008000u);
+  mag = x & 0x007F007Fu;
+  uint32_t y;
+  asm("{\n\t.reg .u32 t;\n\tmul.lo.u32 t, %2, 0xFFFFFF10;\n\tmad.lo.u32 %0, %1, 256, t;\n\t}"
+      : "=r"(y)
+      : "r"(x), "r"(mag));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -429,10 +455,10 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // Eight codes by one scale factor (a bf16x2 pair).
 __device__ __forceinline__ void dequant8(const uint2& c, uint32_t mul2, uint32_t (&v)[4], uint32_t& top) {
   uint32_t m0, m1, m2, m3;
-  v[0] = mul_bf16x2(place2(c.x, 0x1404, m0), mul2);
-  v[1] = mul_bf16x2(place2(c.x, 0x3424, m1), mul2);
-  v[2] = mul_bf16x2(place2(c.y, 0x1404, m2), mul2);
-  v[3] = mul_bf16x2(place2(c.y, 0x3424, m3), mul2);
+  v[0] = mul_bf16x2(place2(c.x, 0x4140, m0), mul2);
+  v[1] = mul_bf16x2(place2(c.x, 0x4342, m1), mul2);
+  v[2] = mul_bf16x2(place2(c.y, 0x4140, m2), mul2);
+  v[3] = mul_bf16x2(place2(c.y, 0x4342, m3), mul2);
   top = __vimax3_u16x2(__vimax3_u16x2(top, m0, m1), m2, m3);
 }
 
@@ -442,21 +468,26 @@ __device__ __forceinline__ uint32_t odd_scale(uint32_t bits) { return (bits - (7
 
 // The general form: bf16(e4m3 * scale), values that are not finite become zero
 // and are reported.
-__device__ __forceinline__ bool dequant8_any(const uint2& c, uint32_t scale_bits, uint32_t (&v)[4]) {
+struct Dequant8 {
+  uint32_t v[4];
+  uint32_t bad;
+};
+__device__ __noinline__ Dequant8 dequant8_any(uint32_t c0, uint32_t c1, uint32_t scale_bits) {
   const float scale = __uint_as_float(scale_bits);
-  bool bad = false;
+  Dequant8 r;
+  r.bad = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? c.x : c.y;
+    const uint32_t w = i < 2 ? c0 : c1;
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(w >> (16 * (i & 1))), __NV_E4M3);
     float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     f.x = __bfloat162float(__float2bfloat16_rn(f.x * scale));
     f.y = __bfloat162float(__float2bfloat16_rn(f.y * scale));
-    if (!isfinite(f.x)) f.x = 0.f, bad = true;
-    if (!isfinite(f.y)) f.y = 0.f, bad = true;
-    v[i] = pack_bf16x2(f.x, f.y);
+    if (!isfinite(f.x)) f.x = 0.f, r.bad = 1;
+    if (!isfinite(f.y)) f.y = 0.f, r.bad = 1;
+    r.v[i] = pack_bf16x2(f.x, f.y);
   }
-  return bad;
+  return r;
 }
 
 __device__ __forceinline__ uint2 ldg_v2_now(const void* p) {
@@ -465,59 +496,104 @@ __device__ __forceinline__ uint2 ldg_v2_now(const void* p) {
   return v;
 }
 
-// One tile's records of a loader warp, in flight or landed.  Lane l holds the
+// One batch of a loader warp's records, in flight or landed.  Lane l holds the
 // codes of dims [256 i + 8 l, + 8): a 16-byte chunk of bf16 each, and eight
 // neighbouring lanes fill a 128-byte row of K or V.
 struct Raw {
-  uint2 lat[kKeysPerWarp][2];
-  uint32_t scale[kKeysPerWarp][2];
+  uint2 lat[kBatch][2];
+  uint32_t scale[kBatch][2];
   uint4 rope;  // lane l: 16 bytes of record l / 8's rope
 };
+
+__device__ __forceinline__ void load_record(const uint8_t* p, int j, Raw& r) {
+  const int lane = threadIdx.x & 31;
+  r.lat[j][0] = ldg_v2_now(p + lane * 8);
+  r.lat[j][1] = ldg_v2_now(p + lane * 8 + 256);
+  r.scale[j][0] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4));
+  r.scale[j][1] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4) + 8);
+}
+
+// The loads of records anywhere (rec: lane j's, 0: none, read as zeros).
+__device__ __noinline__ Raw load_scattered(uint64_t rec) {
+  const int lane = threadIdx.x & 31;
+  Raw r;
+  const uint64_t rope_rec = __shfl_sync(0xffffffffu, rec, lane >> 3);
+  r.rope = make_uint4(0, 0, 0, 0);
+  if (rope_rec) r.rope = ldg_v4_now(reinterpret_cast<const uint8_t*>(rope_rec) + kRopeOffset + (lane & 7) * 16);
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const uint64_t p = __shfl_sync(0xffffffffu, rec, j);
+    r.lat[j][0] = r.lat[j][1] = make_uint2(0, 0);
+    r.scale[j][0] = r.scale[j][1] = 0x3F800000u;  // zeros by the fast path
+    if (p) load_record(reinterpret_cast<const uint8_t*>(p), j, r);
+  }
+  return r;
+}
+
+// q of a unit's rows of this CTA, by one loader group (w: the warp of it).
+__device__ __noinline__ void load_q(const AttendArgs& a, uint32_t base, uint32_t rank, int w, int32_t row0,
+                                    int32_t rows) {
+  const int lane = threadIdx.x & 31;
+  for (int i = w; i < kCtaRows; i += kLoaderWarps) {
+    const int32_t m = int32_t(rank) * kCtaRows + i;
+    const uint32_t dst = base + kOffQ + i * 128;
+    const int32_t tok = m / a.heads;
+    const uint16_t* src = a.q + int64_t(row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head;
+#pragma unroll
+    for (int c = lane; c < kQK / 8; c += 32) {
+      const uint32_t at = dst + (c >> 3) * kQBlock + (((c & 7) ^ (i & 7)) << 4);
+      if (m < rows) cp_async16(at, src + c * 8);
+      else st_shared_v4(at, 0, 0, 0, 0);
+    }
+  }
+  cp_async_wait_all();
+  fence_proxy_async_smem();
+  __syncwarp();
+}
 
 // ---- roles ----
 
 __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
-  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0);
-  // where this lane's chunks go: row key = 4 w + j of block lane / 8, swizzled
-  // column (lane & 7) ^ (key & 7)
-  const uint32_t col = uint32_t((lane & 7) ^ ((w & 1) * 4));
-  const uint32_t k_at = base + kOffK + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
-  const uint32_t rope_key = w * kKeysPerWarp + (lane >> 3);
-  const uint32_t rope_at =
-      base + kOffK + 8 * (kOwnKeys * 128) + rope_key * 128 + ((uint32_t(lane & 7) ^ (rope_key & 7)) << 4);
+  const int lane = threadIdx.x & 31, index = (threadIdx.x >> 5) - kFirstLoader;
+  const uint32_t group = index / kLoaderWarps;  // takes the tiles g with g % 2 == group
+  const int w = index % kLoaderWarps;           // keys [8 w, 8 w + 8) of the CTA's 32
+  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0) + 8 * group;
+  // where this lane's chunks go: row key = 8 w + 4 b + j of block lane / 8,
+  // swizzled column (lane & 7) ^ (key & 7)
+  const uint32_t stage_k = base + kOffK + group * kStageK;
+  const uint32_t k_at = stage_k + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
+  const uint32_t rope_at = stage_k + 8 * (kOwnKeys * 128) + (w * kKeysPerWarp + (lane >> 3)) * 128;
 
-  // Three cursors over the pair's tiles: addresses are looked up one tile ahead
-  // of the loads, the loads run one tile ahead of the conversion.
+  // A cursor over the group's tiles, two batches each: addresses are looked up
+  // one batch ahead of the loads, the loads run one batch ahead of the conversion.
   Units units;
   units.start(a, ms);
-  Unit u;            // unit of the lookups
-  bool more = units.next(a, u);
-  int32_t t = more ? u.t0 : 0;
+  bool more;
+  int32_t t, t0, t1, end, seq, row0, rows;  // of the cursor's unit
+  auto next_unit = [&]() {
+    Unit u;
+    more = units.next(a, u);
+    t = t0 = u.t0, t1 = u.t1, end = u.end, seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
+  };
+  next_unit();
+  auto step = [&]() {
+    if (more && ++t == t1) next_unit();
+  };
+  if (group == 1) step();
 
-  // Page id and offset at the lookup cursor: lanes 0-3 this warp's keys, lanes
-  // 4-7 the peer warp's (both CTAs need to know which keys have no record).  The
-  // id is first looked at a tile later, when the loads set out; kPast: a key at
-  // or after the end.
-  constexpr int32_t kPast = INT32_MIN;
-  auto look_up = [&](bool& starts, Unit& first, bool& any, int32_t& id, int32_t& offset) {
-    id = kPast;
-    any = more;
-    starts = false;
-    if (!more) return;
-    starts = t == u.t0;
-    if (starts) first = u;
+  // Page id and offset at the cursor: lanes 0-3 this warp's keys of batch b,
+  // lanes 4-7 the peer warp's (both CTAs need to know which keys have no record).
+  // The id is first looked at a batch later, when the loads set out; in: a key
+  // before the end.
+  auto look_up = [&](int b, int32_t& id, int32_t& offset, bool& in) {
+    id = -1;
     const int32_t owner = int32_t(rank) ^ (lane >> 2);
-    const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 3);
-    if (lane < 2 * kKeysPerWarp && pos < u.end) {  // (u.end lies within the table)
+    const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + b * kBatch + (lane & 3);
+    in = more && lane < 2 * kBatch && pos < end;  // (the end lies within the table)
+    if (in) {
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
-      id = int32_t(ldg_u32_now(a.b.table + int64_t(u.seq) * a.b.table_stride + page));
-      if (id == kPast) id = -1;
-    }
-    if (++t == u.t1) {
-      more = units.next(a, u);
-      if (more) t = u.t0;
+      id = int32_t(ldg_u32_now(a.b.table + int64_t(seq) * a.b.table_stride + page));
     }
   };
   auto address = [&](int32_t id, int32_t offset) -> uint64_t {
@@ -528,120 +604,111 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     }
     return reinterpret_cast<uint64_t>(a.b.kv) + int64_t(id) * a.b.page_stride + int64_t(offset) * kRecordBytes;
   };
-  auto load = [&](const uint8_t* p, int j, Raw& r) {
-    r.lat[j][0] = ldg_v2_now(p + lane * 8);
-    r.lat[j][1] = ldg_v2_now(p + lane * 8 + 256);
-    r.scale[j][0] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4));
-    r.scale[j][1] = ldg_u32_now(p + kScaleOffset + 4 * (lane >> 4) + 8);
-  };
   // rec: lane j's record (0: none)
   auto issue = [&](uint64_t rec, Raw& r) {
     const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
     const uint32_t run = __ballot_sync(
-        0xffffffffu, lane >= kKeysPerWarp || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
+        0xffffffffu, lane >= kBatch || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
     if (run == 0xffffffffu) {  // all in a row, as in pages of a multiple of 4 records
       const uint8_t* p = reinterpret_cast<const uint8_t*>(first);
 #pragma unroll
-      for (int j = 0; j < kKeysPerWarp; ++j) load(p + j * kRecordBytes, j, r);
+      for (int j = 0; j < kBatch; ++j) load_record(p + j * kRecordBytes, j, r);
       r.rope = ldg_v4_now(p + (lane >> 3) * kRecordBytes + kRopeOffset + (lane & 7) * 16);
-      return;
-    }
-    const uint64_t rope_rec = __shfl_sync(0xffffffffu, rec, lane >> 3);
-    r.rope = make_uint4(0, 0, 0, 0);
-    if (rope_rec) r.rope = ldg_v4_now(reinterpret_cast<const uint8_t*>(rope_rec) + kRopeOffset + (lane & 7) * 16);
-#pragma unroll
-    for (int j = 0; j < kKeysPerWarp; ++j) {
-      const uint64_t p = __shfl_sync(0xffffffffu, rec, j);
-      r.lat[j][0] = r.lat[j][1] = make_uint2(0, 0);
-      r.scale[j][0] = r.scale[j][1] = 0x3F800000u;  // zeros by the fast path
-      if (p) load(reinterpret_cast<const uint8_t*>(p), j, r);
+    } else {
+      r = load_scattered(rec);
     }
   };
 
   Raw raw;
-  Unit cur_unit, next_unit;
-  bool cur_starts, next_starts, cur_any, next_any;
   int32_t next_id, next_offset = 0;
-  look_up(cur_starts, cur_unit, cur_any, next_id, next_offset);
+  bool next_in;
+  look_up(0, next_id, next_offset, next_in);
   uint64_t rec = address(next_id, next_offset);
-  uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && next_id != kPast);
+  uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && next_in);
   issue(rec, raw);
-  look_up(next_starts, next_unit, next_any, next_id, next_offset);
-  for (uint32_t g = 0; cur_any; ++g) {
-    const uint32_t stage = g & 1;
-    if (cur_starts) {
-      // q of the unit, once the last QK of the unit before is done
-      if (g > 0 && !warp_wait(ms, a, &ms->qk_done[(g - 1) & 1], ((g - 1) >> 1) & 1)) return;
-      const int32_t rows = cur_unit.tokens * a.heads;
-      for (int i = w; i < kCtaRows; i += kLoaderWarps) {
-        const int32_t m = int32_t(rank) * kCtaRows + i;
-        const uint32_t dst = base + kOffQ + i * 128;
-        const int32_t tok = m / a.heads;
-        const uint16_t* src = a.q + int64_t(cur_unit.row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head;
+  look_up(1, next_id, next_offset, next_in);
+  uint32_t seen = 0;  // bit j: key j of the warp's 8, bits 8..: the peer's
+  bool any = more;    // the batch being converted exists, and its tile starts a unit
+  bool starts = more && t == t0;
+  for (uint32_t g = group; any;) {
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+      if (b == 0 && starts) {
+        // q of the unit, once the last QK of the unit before is done.  (That is on
+        // the other group's barrier.  A parity tells a phase from its neighbours only:
+        // QK(g - 2) on this group's own says that QK(g - 3) is past.)
+        if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
+        if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
+        load_q(a, base, rank, w, row0, rows);
+        if (lane == 0) arrive_at(q_full);
+      }
+      // convert the landed records
+      uint32_t v[kBatch][2][4];
+      uint32_t odd = 0, top = 0;
 #pragma unroll
-        for (int c = lane; c < kQK / 8; c += 32) {
-          const uint32_t at = dst + (c >> 3) * kQBlock + (((c & 7) ^ (i & 7)) << 4);
-          if (m < rows) cp_async16(at, src + c * 8);
-          else st_shared_v4(at, 0, 0, 0, 0);
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          odd |= odd_scale(raw.scale[j][i]);
+          const uint32_t mul2 = __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232);
+          dequant8(raw.lat[j][i], mul2, v[j][i], top);
+        }
+      uint4 rope = raw.rope;
+      const bool nan = (top & 0xFFFFu) == 0x7Fu || (top >> 16) == 0x7Fu;
+      if (__any_sync(0xffffffffu, odd != 0 || nan)) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const Dequant8 d = dequant8_any(raw.lat[j][i].x, raw.lat[j][i].y, raw.scale[j][i]);
+            bad |= d.bad != 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[j][i][k] = d.v[k];
+          }
+          // a latent that is not finite is zero in V, where rows that may not see the
+          // key would meet it as 0 * NaN, and a NaN in the key's rope, which V lacks:
+          // its scores are NaN, and the mask drops them
+          if (__any_sync(0xffffffffu, bad) && lane == 8 * j) rope.x = 0x7FC07FC0u;
         }
       }
-      cp_async_wait_all();
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) arrive_at(q_full);
-    }
-    // convert the landed records
-    uint32_t v[kKeysPerWarp][2][4];
-    uint32_t odd = 0, top = 0;
+      seen |= ((holes & 15u) | ((holes & 0xF0u) << 4)) << (4 * b);
+      // the next batch's records set out while this one is stored
+      rec = address(next_id, next_offset);
+      holes = __ballot_sync(0xffffffffu, rec == 0 && next_in);
+      if (b == 0 || more) issue(rec, raw);
+      if (b == 0 && g >= 2 &&
+          (!warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1) ||
+           !warp_wait(ms, a, &ms->v_full[group], ((g - 2) >> 1) & 1)))
+        return;
+      const uint32_t col = uint32_t(lane & 7) ^ uint32_t(4 * b);
 #pragma unroll
-    for (int j = 0; j < kKeysPerWarp; ++j)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        odd |= odd_scale(raw.scale[j][i]);
-        const uint32_t mul2 = __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232);
-        dequant8(raw.lat[j][i], mul2, v[j][i], top);
+      for (int j = 0; j < kBatch; ++j) {
+        const uint32_t at = k_at + (4 * b + j) * 128 + ((col ^ j) << 4);
+        st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
+        st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
       }
-    uint4 rope = raw.rope;
-    const bool nan = (top & 0xFFFFu) == 0x07F0u || (top >> 16) == 0x07F0u;
-    if (__any_sync(0xffffffffu, odd != 0 || nan)) {
-#pragma unroll
-      for (int j = 0; j < kKeysPerWarp; ++j) {
-        bool bad = false;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) bad |= dequant8_any(raw.lat[j][i], raw.scale[j][i], v[j][i]);
-        // a latent that is not finite is zero in V, where rows that may not see the
-        // key would meet it as 0 * NaN, and a NaN in the key's rope, which V lacks:
-        // its scores are NaN, and the mask drops them
-        if (__any_sync(0xffffffffu, bad) && lane == 8 * j) rope.x = 0x7FC07FC0u;
+      st_shared_v4(rope_at + 4 * b * 128 + ((col ^ uint32_t(lane >> 3)) << 4), rope.x, rope.y, rope.z, rope.w);
+      if (b == 1) {
+        if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t(seen >> (8 * lane));
+        seen = 0;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ms->k_ready[group]);
+          arrive_at(k_full);
+        }
+        // the cursor is at the next tile, whose first batch is in flight
+        look_up(1, next_id, next_offset, next_in);
+        any = more;
+        starts = more && t == t0;
+      } else {
+        step();
+        step();
+        look_up(0, next_id, next_offset, next_in);
       }
     }
-    const uint32_t cur_holes = holes;
-    // the next tile's records set out while this one is stored
-    rec = address(next_id, next_offset);
-    holes = __ballot_sync(0xffffffffu, rec == 0 && next_id != kPast);
-    if (next_any) issue(rec, raw);
-    if (g >= 2 && (!warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1) ||
-                   !warp_wait(ms, a, &ms->v_full[stage], ((g - 2) >> 1) & 1)))
-      return;
-    const uint32_t k = k_at + stage * kStageK;
-#pragma unroll
-    for (int j = 0; j < kKeysPerWarp; ++j) {
-      const uint32_t at = k + j * 128 + ((col ^ j) << 4);
-      st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
-      st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
-    }
-    st_shared_v4(rope_at + stage * kStageK, rope.x, rope.y, rope.z, rope.w);
-    if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t((cur_holes >> (4 * lane)) & 15u);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&ms->k_ready[stage]);
-      arrive_at(k_full + 8 * stage);
-    }
-    cur_starts = next_starts;
-    cur_any = next_any;
-    if (next_starts) cur_unit = next_unit;
-    look_up(next_starts, next_unit, next_any, next_id, next_offset);
+    g += 2;
   }
 }
 
@@ -658,13 +725,20 @@ __device__ __forceinline__ void copier_role(const AttendArgs& a, Misc* ms, uint3
   }
   Units units;
   units.start(a, ms);
-  Unit u;
-  uint32_t g = 0;
-  while (units.next(a, u)) {
-    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
-      const uint32_t stage = g & 1, parity = (g >> 1) & 1;
-      if (!wait_for(ms, a, &ms->k_ready[stage], parity)) return;
-      if (g >= 2 && !wait_for(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
+  bool more;
+  int32_t t, t1;
+  auto next_unit = [&]() {
+    Unit u;
+    more = units.next(a, u);
+    t = u.t0, t1 = u.t1;
+  };
+  next_unit();
+  uint32_t g = 0, done = 0;  // tiles copied, tiles whose V has landed here
+  uint64_t t0 = 0;
+  for (uint32_t idle = 1; more || done < g; ++idle) {
+    const uint32_t stage = g & 1, last = done & 1;
+    if (more && mbar_test(&ms->k_ready[stage], (g >> 1) & 1) &&
+        (g < 2 || mbar_test(&ms->pv_done[stage], ((g - 2) >> 1) & 1))) {
       mbar_arrive_expect_tx(&ms->v_land[stage], kStageV);
 #pragma unroll
       for (int b = 0; b < 4; ++b)
@@ -672,18 +746,38 @@ __device__ __forceinline__ void copier_role(const AttendArgs& a, Misc* ms, uint3
         for (int r = 0; r < 2; ++r)
           bulk_s2s(v_at[r] + stage * kStageV + b * kVBlock, base + kOffK + stage * kStageK + (4 * r + b) * (kOwnKeys * 128),
                    kOwnKeys * 128, land[r] + 8 * stage);
-      // (the limit of its own: copies in flight are waited for after a give-up too)
-      if (!mbar_wait(&ms->v_land[stage], parity, kWaitNs)) {
-        give_up(ms, a);
+      ++g;
+      if (++t == t1) next_unit();
+      idle = 0;
+    }
+    if (done < g && mbar_test(&ms->v_land[last], (done >> 1) & 1)) {
+      arrive_at(full[0] + 8 * last);
+      arrive_at(full[1] + 8 * last);
+      ++done;
+      idle = 0;
+    }
+    if (idle == 0) {
+      t0 = 0;
+      continue;
+    }
+    __nanosleep(40);
+    if ((idle & 63u) == 0) {
+      const uint64_t now = globaltimer();
+      if (t0 == 0) t0 = now;
+      const bool late = now - t0 > ms->wait_ns;
+      if (late) give_up(ms, a.b.status);
+      if (late || *reinterpret_cast<volatile int32_t*>(&ms->dead)) {
+        // copies in flight are waited for, with a limit of their own
+        for (; done < g; ++done) mbar_wait(&ms->v_land[done & 1], (done >> 1) & 1, kWaitNs);
         return;
       }
-      arrive_at(full[0] + 8 * stage);
-      arrive_at(full[1] + 8 * stage);
     }
   }
 }
 
-// One thread of the even CTA each: K-steps which, which + 2, ... of every QK.
+// A warp of the even CTA each: K-steps which, which + 2, ... of every QK.  (The
+// whole warp runs the loop and lane 0 issues, so that descriptors stay in uniform
+// registers.)
 __device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                uint32_t which) {
   const uint64_t q0 = smem_desc(base + kOffQ, 16, 1024, kSw128);
@@ -693,25 +787,29 @@ __device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, ui
   Unit u;
   uint32_t g = 0, n_units = 0;
   while (units.next(a, u)) {
-    if (!wait_for(ms, a, &ms->q_full, n_units & 1)) return;
+    if (!warp_wait(ms, a, &ms->q_full, n_units & 1)) return;
     ++n_units;
-    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+    const int32_t t0 = u.t0, t1 = u.t1;
+    for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      if (!wait_for(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
-      if (g >= 2 && !wait_for(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
+      if (!warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
+      if (g >= 2 && !warp_wait(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
       tc_fence_after();
       const uint32_t d = tmem + kTmemS + 64 * stage + 32 * which;
       const uint64_t qd = q0 + which * 2, kd = k0 + uint64_t((stage * kStageK) >> 4) + which * 2;
+      if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int k = 0; k < kQK / 16; k += 2)
-        mma2(d, qd + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
+        for (int k = 0; k < kQK / 16; k += 2)
+          mma2(d, qd + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
              kd + uint64_t(((k >> 2) * (kOwnKeys * 128) + (k & 3) * 32) >> 4), kIdescQK, k > 0);
-      commit2(&ms->qk_done[stage]);
+        commit2(&ms->qk_done[stage]);
+      }
+      __syncwarp();
     }
   }
 }
 
-// One thread of the even CTA: O += P V of every tile.
+// A warp of the even CTA: O += P V of every tile.
 __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem) {
   const uint64_t p0 = smem_desc(base + kOffP, 16, 1024, kSw128);
   const uint64_t v0 = smem_desc(base + kOffV, kVBlock, 1024, kSw128);
@@ -720,19 +818,23 @@ __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, ui
   Unit u;
   uint32_t g = 0;
   while (units.next(a, u)) {
-    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+    const int32_t t0 = u.t0, t1 = u.t1;
+    for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      if (!wait_for(ms, a, &ms->v_full[stage], (g >> 1) & 1)) return;
-      if (!wait_for(ms, a, &ms->p_full, g & 1)) return;
+      if (!warp_wait(ms, a, &ms->v_full[stage], (g >> 1) & 1)) return;
+      if (!warp_wait(ms, a, &ms->p_full, g & 1)) return;
       tc_fence_after();
       const uint64_t vd = v0 + uint64_t((stage * kStageV) >> 4);
+      if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          mma2(tmem + 128 * h, p0 + uint64_t(k * 2), vd + uint64_t((h * 2 * kVBlock + k * 2048) >> 4), kIdescPV,
-               (t == u.t0 && k == 0) ? 0u : 1u);
-      commit2(&ms->pv_done[stage]);
+          for (int k = 0; k < kTileKeys / 16; ++k)
+            mma2(tmem + 128 * h, p0 + uint64_t(k * 2), vd + uint64_t((h * 2 * kVBlock + k * 2048) >> 4), kIdescPV,
+               (t == t0 && k == 0) ? 0u : 1u);
+        commit2(&ms->pv_done[stage]);
+      }
+      __syncwarp();
     }
   }
 }
@@ -760,7 +862,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
     const bool live = m < u.tokens * a.heads;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
     float ref = -INFINITY, l = 0.f;
-    for (int32_t t = u.t0; t < u.t1; ++t, ++g) {
+    const int32_t t0 = u.t0, t1 = u.t1;
+    for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
       wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
@@ -775,7 +878,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
         tmem_ld16(lane_base + kTmemS + 64 * stage + 32, lo2);
         tmem_ld16(lane_base + kTmemS + 64 * stage + 48, hi2);
       }
-      const uint2 flags = *reinterpret_cast<const uint2*>(&ms->flags[g & 3][8 * half]);
+      const uint32_t flags = *reinterpret_cast<const uint32_t*>(&ms->flags[g & 3][4 * half]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -789,16 +892,12 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
         for (int c = 0; c < 32; ++c) x[c] *= by;
       }
       const int32_t key0 = t * kTileKeys + 32 * half;
-      if (__any_sync(0xffffffffu, key0 + 32 > see)) {
+      if (__any_sync(0xffffffffu, key0 + 32 > see) || flags) {
+        // bit c: key c is seen
+        const int32_t n = see - key0;
+        const uint32_t seen = ~flags & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = key0 + c < see ? x[c] : -INFINITY;
-      }
-      if (flags.x | flags.y) {  // (the same for the whole warp)
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const uint32_t f = ((c < 16 ? flags.x : flags.y) >> (8 * ((c >> 2) & 3))) >> (c & 3);
-          if (f & 1u) x[c] = -INFINITY;
-        }
+        for (int c = 0; c < 32; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
       }
       float tm = x[0];
 #pragma unroll
@@ -824,7 +923,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       }
       l = l * alpha + (sum0 + sum1);
       if (g > 0) wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
-      if (t > u.t0 && __any_sync(0xffffffffu, move)) {
+      if (t > t0 && __any_sync(0xffffffffu, move)) {
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < 256; c += 16) {
@@ -945,16 +1044,19 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
     loader_role(a, ms, base, rank);
   } else if (warp == kCopier) {
     if ((threadIdx.x & 31) == 0) copier_role(a, ms, base, rank);
-  } else if (rank == 0 && (threadIdx.x & 31) == 0) {
+  } else if (rank == 0) {
     if (warp == kIssuerPv) issuer_pv_role(a, ms, base, tmem);
     else issuer_qk_role(a, ms, base, tmem, uint32_t(warp - kIssuerQk));
     // every MMA has to be complete before the tensor memory and the shared
     // memory it reads go away (also after a wait that gave up); the odd CTA
     // learns of it at the cluster barrier
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_u32(&ms->drain))
-                 : "memory");
-    if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       smem_u32(&ms->drain))
+                   : "memory");
+      if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
+    }
   }
   __syncwarp();
   tc_fence_before();
