@@ -26,9 +26,9 @@
 // Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 one thread each that
 // issues MMAs (even CTA only), 15 copier.  Per tile g (stage g & 1):
 //   loaders   two groups of four warps take turns at the tiles, a warp 8 of the
-//             CTA's 32 keys in two batches; the next batch's records are on their
-//             way in registers while one is dequantised; K is written when QK(g - 2)
-//             and the copies out of it are done
+//             CTA's 32 keys: records into registers, dequantised there, and as soon
+//             as QK(g - 2) and the copies out of its K are done, stored.  What a
+//             stage waits for after that is the stores alone
 //   copier    one thread: K -> V of both CTAs when PV(g - 2) is done
 //   issuers   12 and 13 the even and odd K-steps of QK into two accumulators, 14
 //             PV: a thread issues a cta_group::2 MMA at most every 48 cycles
@@ -71,7 +71,6 @@ constexpr int kPairRows = 128;
 constexpr int kCtaRows = 64;
 constexpr int kLoaderWarps = 4;   // of each of the two loader groups
 constexpr int kKeysPerWarp = kOwnKeys / kLoaderWarps;
-constexpr int kBatch = 4;         // keys that a loader warp converts at a time
 constexpr int kFirstLoader = 4;
 constexpr int kIssuerQk = 12;  // and 13
 constexpr int kIssuerPv = 14;
@@ -434,15 +433,13 @@ __device__ void find_range(const AttendArgs& a, Misc* ms, int32_t pair) {
 //   16 m + 256 (x - m) = 256 x - 240 m,  m = x & 0x7F,
 // by multiplications, since the shifts and logic of the usual form alone keep
 // the ALU pipe busy longer than the tensor work of a tile lasts; an exact product
-// with scale * 2^120 does the rest (subnormals included).  mag returns m, which
-// is 0x7F for a NaN code.
-__device__ __forceinline__ uint32_t place2(uint32_t w, uint32_t sel, uint32_t& mag) {
+// with scale * 2^120 does the rest (subnormals included).
+__device__ __forceinline__ uint32_t place2(uint32_t w, uint32_t sel) {
   const uint32_t x = __byte_perm(w, 0, sel);
-  mag = x & 0x007F007Fu;
   uint32_t y;
   asm("{\n\t.reg .u32 t;\n\tmul.lo.u32 t, %2, 0xFFFFFF10;\n\tmad.lo.u32 %0, %1, 256, t;\n\t}"
       : "=r"(y)
-      : "r"(x), "r"(mag));
+      : "r"(x), "r"(x & 0x007F007Fu));
   return y;
 }
 
@@ -453,13 +450,17 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // Eight codes by one scale factor (a bf16x2 pair).
-__device__ __forceinline__ void dequant8(const uint2& c, uint32_t mul2, uint32_t (&v)[4], uint32_t& top) {
-  uint32_t m0, m1, m2, m3;
-  v[0] = mul_bf16x2(place2(c.x, 0x4140, m0), mul2);
-  v[1] = mul_bf16x2(place2(c.x, 0x4342, m1), mul2);
-  v[2] = mul_bf16x2(place2(c.y, 0x4140, m2), mul2);
-  v[3] = mul_bf16x2(place2(c.y, 0x4342, m3), mul2);
-  top = __vimax3_u16x2(__vimax3_u16x2(top, m0, m1), m2, m3);
+__device__ __forceinline__ void dequant8(const uint2& c, uint32_t mul2, uint32_t (&v)[4]) {
+  v[0] = mul_bf16x2(place2(c.x, 0x4140), mul2);
+  v[1] = mul_bf16x2(place2(c.x, 0x4342), mul2);
+  v[2] = mul_bf16x2(place2(c.y, 0x4140), mul2);
+  v[3] = mul_bf16x2(place2(c.y, 0x4342), mul2);
+}
+
+// Running OR that has an upper bit of a byte set once a NaN code (0x7F or 0xFF)
+// was met.
+__device__ __forceinline__ uint32_t nan_codes(const uint2& c, uint32_t top) {
+  return top | ((c.x & 0x7F7F7F7Fu) + 0x01010101u) | ((c.y & 0x7F7F7F7Fu) + 0x01010101u);
 }
 
 // Zero if a block scale takes the fast path: a power of two in [2^-120, 2^7]
@@ -496,13 +497,13 @@ __device__ __forceinline__ uint2 ldg_v2_now(const void* p) {
   return v;
 }
 
-// One batch of a loader warp's records, in flight or landed.  Lane l holds the
+// One tile's records of a loader warp, in flight or landed.  Lane l holds the
 // codes of dims [256 i + 8 l, + 8): a 16-byte chunk of bf16 each, and eight
 // neighbouring lanes fill a 128-byte row of K or V.
 struct Raw {
-  uint2 lat[kBatch][2];
-  uint32_t scale[kBatch][2];
-  uint4 rope;  // lane l: 16 bytes of record l / 8's rope
+  uint2 lat[kKeysPerWarp][2];
+  uint32_t scale[kKeysPerWarp][2];
+  uint4 rope[2];  // lane l: 16 bytes of the rope of records l / 8 and 4 + l / 8
 };
 
 __device__ __forceinline__ void load_record(const uint8_t* p, int j, Raw& r) {
@@ -517,11 +518,14 @@ __device__ __forceinline__ void load_record(const uint8_t* p, int j, Raw& r) {
 __device__ __noinline__ Raw load_scattered(uint64_t rec) {
   const int lane = threadIdx.x & 31;
   Raw r;
-  const uint64_t rope_rec = __shfl_sync(0xffffffffu, rec, lane >> 3);
-  r.rope = make_uint4(0, 0, 0, 0);
-  if (rope_rec) r.rope = ldg_v4_now(reinterpret_cast<const uint8_t*>(rope_rec) + kRopeOffset + (lane & 7) * 16);
 #pragma unroll
-  for (int j = 0; j < kBatch; ++j) {
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t p = __shfl_sync(0xffffffffu, rec, 4 * i + (lane >> 3));
+    r.rope[i] = make_uint4(0, 0, 0, 0);
+    if (p) r.rope[i] = ldg_v4_now(reinterpret_cast<const uint8_t*>(p) + kRopeOffset + (lane & 7) * 16);
+  }
+#pragma unroll
+  for (int j = 0; j < kKeysPerWarp; ++j) {
     const uint64_t p = __shfl_sync(0xffffffffu, rec, j);
     r.lat[j][0] = r.lat[j][1] = make_uint2(0, 0);
     r.scale[j][0] = r.scale[j][1] = 0x3F800000u;  // zeros by the fast path
@@ -558,14 +562,15 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   const uint32_t group = index / kLoaderWarps;  // takes the tiles g with g % 2 == group
   const int w = index % kLoaderWarps;           // keys [8 w, 8 w + 8) of the CTA's 32
   const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0) + 8 * group;
-  // where this lane's chunks go: row key = 8 w + 4 b + j of block lane / 8,
-  // swizzled column (lane & 7) ^ (key & 7)
+  // where this lane's chunks go: row key = 8 w + j of block lane / 8, swizzled
+  // column (lane & 7) ^ j
   const uint32_t stage_k = base + kOffK + group * kStageK;
   const uint32_t k_at = stage_k + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
-  const uint32_t rope_at = stage_k + 8 * (kOwnKeys * 128) + (w * kKeysPerWarp + (lane >> 3)) * 128;
+  const uint32_t rope_at = stage_k + 8 * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
 
-  // A cursor over the group's tiles, two batches each: addresses are looked up
-  // one batch ahead of the loads, the loads run one batch ahead of the conversion.
+  // A cursor over the group's tiles: the records' addresses are looked up while
+  // the tile before is converted; their loads set out as soon as its registers are
+  // free and land while the other group works.
   Units units;
   units.start(a, ms);
   bool more;
@@ -581,15 +586,14 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   };
   if (group == 1) step();
 
-  // Page id and offset at the cursor: lanes 0-3 this warp's keys of batch b,
-  // lanes 4-7 the peer warp's (both CTAs need to know which keys have no record).
-  // The id is first looked at a batch later, when the loads set out; in: a key
-  // before the end.
-  auto look_up = [&](int b, int32_t& id, int32_t& offset, bool& in) {
+  // Page id and offset at the cursor: lanes 0-7 this warp's keys, lanes 8-15 the
+  // peer warp's (both CTAs need to know which keys have no record).  The id is
+  // first looked at when the loads set out; in: a key before the end.
+  auto look_up = [&](int32_t& id, int32_t& offset, bool& in) {
     id = -1;
-    const int32_t owner = int32_t(rank) ^ (lane >> 2);
-    const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + b * kBatch + (lane & 3);
-    in = more && lane < 2 * kBatch && pos < end;  // (the end lies within the table)
+    const int32_t owner = int32_t(rank) ^ (lane >> 3);
+    const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 7);
+    in = more && lane < 2 * kKeysPerWarp && pos < end;  // (the end lies within the table)
     if (in) {
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
@@ -608,107 +612,95 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   auto issue = [&](uint64_t rec, Raw& r) {
     const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
     const uint32_t run = __ballot_sync(
-        0xffffffffu, lane >= kBatch || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
-    if (run == 0xffffffffu) {  // all in a row, as in pages of a multiple of 4 records
+        0xffffffffu, lane >= kKeysPerWarp || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
+    if (run == 0xffffffffu) {  // all in a row, as in pages of a multiple of 8 records
       const uint8_t* p = reinterpret_cast<const uint8_t*>(first);
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) load_record(p + j * kRecordBytes, j, r);
-      r.rope = ldg_v4_now(p + (lane >> 3) * kRecordBytes + kRopeOffset + (lane & 7) * 16);
+      for (int j = 0; j < kKeysPerWarp; ++j) load_record(p + j * kRecordBytes, j, r);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        r.rope[i] = ldg_v4_now(p + (4 * i + (lane >> 3)) * kRecordBytes + kRopeOffset + (lane & 7) * 16);
     } else {
       r = load_scattered(rec);
     }
   };
 
   Raw raw;
-  int32_t next_id, next_offset = 0;
-  bool next_in;
-  look_up(0, next_id, next_offset, next_in);
-  uint64_t rec = address(next_id, next_offset);
-  uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && next_in);
-  issue(rec, raw);
-  look_up(1, next_id, next_offset, next_in);
-  uint32_t seen = 0;  // bit j: key j of the warp's 8, bits 8..: the peer's
-  bool any = more;    // the batch being converted exists, and its tile starts a unit
-  bool starts = more && t == t0;
-  for (uint32_t g = group; any;) {
-#pragma unroll 1
-    for (int b = 0; b < 2; ++b) {
-      if (b == 0 && starts) {
-        // q of the unit, once the last QK of the unit before is done.  (That is on
-        // the other group's barrier.  A parity tells a phase from its neighbours only:
-        // QK(g - 2) on this group's own says that QK(g - 3) is past.)
-        if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
-        if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
-        load_q(a, base, rank, w, row0, rows);
-        if (lane == 0) arrive_at(q_full);
-      }
-      // convert the landed records
-      uint32_t v[kBatch][2][4];
-      uint32_t odd = 0, top = 0;
+  int32_t id, offset = 0;
+  bool in;
+  look_up(id, offset, in);
+  for (uint32_t g = group; more; g += 2) {
+    const uint64_t rec = address(id, offset);
+    const uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && in);
+    issue(rec, raw);
+    if (t == t0) {
+      // q of the unit, once the last QK of the unit before is done.  (That is on
+      // the other group's barrier.  A parity tells a phase from its neighbours only:
+      // QK(g - 2) on this group's own says that QK(g - 3) is past.)
+      if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
+      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
+      load_q(a, base, rank, w, row0, rows);
+      if (lane == 0) arrive_at(q_full);
+    }
+    step();
+    step();
+    look_up(id, offset, in);
+    // convert the landed records
+    uint32_t v[kKeysPerWarp][2][4];
+    uint32_t odd = 0, top = 0;
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
+    for (int j = 0; j < kKeysPerWarp; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) odd |= odd_scale(raw.scale[j][i]);
+#pragma unroll
+    for (int j = 0; j < kKeysPerWarp; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) top = nan_codes(raw.lat[j][i], top);
+    if (__any_sync(0xffffffffu, odd != 0 || (top & 0x80808080u) != 0)) {
+#pragma unroll
+      for (int j = 0; j < kKeysPerWarp; ++j) {
+        bool bad = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          odd |= odd_scale(raw.scale[j][i]);
-          const uint32_t mul2 = __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232);
-          dequant8(raw.lat[j][i], mul2, v[j][i], top);
+          const Dequant8 d = dequant8_any(raw.lat[j][i].x, raw.lat[j][i].y, raw.scale[j][i]);
+          bad |= d.bad != 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[j][i][k] = d.v[k];
         }
-      uint4 rope = raw.rope;
-      const bool nan = (top & 0xFFFFu) == 0x7Fu || (top >> 16) == 0x7Fu;
-      if (__any_sync(0xffffffffu, odd != 0 || nan)) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          bool bad = false;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const Dequant8 d = dequant8_any(raw.lat[j][i].x, raw.lat[j][i].y, raw.scale[j][i]);
-            bad |= d.bad != 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) v[j][i][k] = d.v[k];
-          }
-          // a latent that is not finite is zero in V, where rows that may not see the
-          // key would meet it as 0 * NaN, and a NaN in the key's rope, which V lacks:
-          // its scores are NaN, and the mask drops them
-          if (__any_sync(0xffffffffu, bad) && lane == 8 * j) rope.x = 0x7FC07FC0u;
-        }
+        // a latent that is not finite is zero in V, where rows that may not see the
+        // key would meet it as 0 * NaN, and a NaN in the key's rope, which V lacks:
+        // its scores are NaN, and the mask drops them
+        if (__any_sync(0xffffffffu, bad) && lane == 8 * (j & 3)) raw.rope[j >> 2].x = 0x7FC07FC0u;
       }
-      seen |= ((holes & 15u) | ((holes & 0xF0u) << 4)) << (4 * b);
-      // the next batch's records set out while this one is stored
-      rec = address(next_id, next_offset);
-      holes = __ballot_sync(0xffffffffu, rec == 0 && next_in);
-      if (b == 0 || more) issue(rec, raw);
-      if (b == 0 && g >= 2 &&
-          (!warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1) ||
-           !warp_wait(ms, a, &ms->v_full[group], ((g - 2) >> 1) & 1)))
-        return;
-      const uint32_t col = uint32_t(lane & 7) ^ uint32_t(4 * b);
+    } else {
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const uint32_t at = k_at + (4 * b + j) * 128 + ((col ^ j) << 4);
-        st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
-        st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
-      }
-      st_shared_v4(rope_at + 4 * b * 128 + ((col ^ uint32_t(lane >> 3)) << 4), rope.x, rope.y, rope.z, rope.w);
-      if (b == 1) {
-        if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t(seen >> (8 * lane));
-        seen = 0;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ms->k_ready[group]);
-          arrive_at(k_full);
-        }
-        // the cursor is at the next tile, whose first batch is in flight
-        look_up(1, next_id, next_offset, next_in);
-        any = more;
-        starts = more && t == t0;
-      } else {
-        step();
-        step();
-        look_up(0, next_id, next_offset, next_in);
-      }
+      for (int j = 0; j < kKeysPerWarp; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          dequant8(raw.lat[j][i], __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232), v[j][i]);
     }
-    g += 2;
+    if (g >= 2 && (!warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1) ||
+                   !warp_wait(ms, a, &ms->v_full[group], ((g - 2) >> 1) & 1)))
+      return;
+#pragma unroll
+    for (int j = 0; j < kKeysPerWarp; ++j) {
+      const uint32_t at = k_at + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
+      st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
+      st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t key = 4 * i + (lane >> 3);
+      const uint4 r = raw.rope[i];
+      st_shared_v4(rope_at + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
+    }
+    if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t(holes >> (8 * lane));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&ms->k_ready[group]);
+      arrive_at(k_full);
+    }
   }
 }
 
