@@ -341,68 +341,79 @@ def smla_pack_records(latent: torch.Tensor, rope: torch.Tensor, kv_out: torch.Te
 
 
 # ---- the paged cache ----
+#
+# These calls can take less time on the GPU than their checks do here, so the
+# checks read each tensor's properties once and the messages are made on failure.
 
 
-def _need(ok: bool, code: int, what: str) -> None:
-    if not ok:
-        raise SmlaError(code, what)
+def _fail(code: int, what: str, why: str):
+    raise SmlaError(code, f"{what}: {why}")
 
 
-def _on_device(what: str, *tensors) -> None:
-    """Every tensor on the current CUDA device (the launch goes there)."""
+def _launch_stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _current_device(what: str, tensors) -> int:
+    """The current CUDA device, on which every tensor has to be (the launch goes there)."""
+    first = tensors[0].get_device()
     for t in tensors:
-        if t is not None:
-            _need(t.is_cuda and t.device.index == torch.cuda.current_device(), SMLA_ERR_DEVICE,
-                  f"{what}: a tensor is not on the current CUDA device")
+        if t is not None and (not t.is_cuda or t.get_device() != first):
+            _fail(SMLA_ERR_DEVICE, what, "the tensors are not on one CUDA device")
+    if first != torch.cuda.current_device():
+        _fail(SMLA_ERR_DEVICE, what, "a tensor is not on the current CUDA device")
+    return first
 
 
 def _paged_batch(what: str, kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
-                 seq_lens: torch.Tensor, n_rows: int, status: Optional[torch.Tensor]) -> PagedBatch:
+                 seq_lens: torch.Tensor, n_rows: int, status: Optional[torch.Tensor]) -> tuple:
     """The C batch of a paged cache uint8 [n_pages, page_size, 656] (pages may be
-    strided) and its int32 tables, checked."""
-    _need(kv_cache.dtype == torch.uint8 and kv_cache.dim() == 3 and kv_cache.shape[2] == RECORD_BYTES,
-          SMLA_ERR_SHAPE, f"{what}: kv_cache is uint8 [n_pages, page_size, {RECORD_BYTES}]")
+    strided) and its int32 tables, checked: the fields of PagedBatch."""
+    if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 3 or kv_cache.shape[2] != RECORD_BYTES:
+        _fail(SMLA_ERR_SHAPE, what, f"kv_cache is uint8 [n_pages, page_size, {RECORD_BYTES}]")
+    n_pages, page_size, _ = kv_cache.shape
+    page_stride, record_stride, byte_stride = kv_cache.stride()
     # (a dimension of one element, or an empty cache, may carry any stride)
-    empty = kv_cache.numel() == 0
-    _need(empty or (kv_cache.stride(2) == 1 and (kv_cache.shape[1] == 1 or kv_cache.stride(1) == RECORD_BYTES)),
-          SMLA_ERR_STRIDE, f"{what}: the records of a page are contiguous")
-    for t, dims in ((block_table, 2), (cu_rows, 1), (seq_lens, 1)):
-        _need(t.dtype == torch.int32 and t.dim() == dims, SMLA_ERR_SHAPE,
-              f"{what}: block_table is int32 [n_seqs, max_pages], cu_rows and seq_lens int32 vectors")
-        _need(t.numel() == 0 or t.shape[-1] == 1 or t.stride(-1) == 1, SMLA_ERR_STRIDE,
-              f"{what}: block_table rows, cu_rows and seq_lens are contiguous")
-    n_seqs = int(seq_lens.shape[0])
-    _need(cu_rows.shape[0] == n_seqs + 1 and block_table.shape[0] == n_seqs, SMLA_ERR_SHAPE,
-          f"{what}: n_seqs + 1 entries of cu_rows and n_seqs rows of block_table")
-    _need(status is None or (status.dtype == torch.int32 and status.numel() >= 1), SMLA_ERR_SHAPE,
-          f"{what}: status is int32 [1]")
-    _on_device(what, kv_cache, block_table, cu_rows, seq_lens, status)
-    b = PagedBatch()
-    b.kv_cache, b.n_pages = kv_cache.data_ptr(), int(kv_cache.shape[0])
-    b.page_size, b.max_pages = int(kv_cache.shape[1]), int(block_table.shape[1])
-    b.page_stride = kv_cache.stride(0) if kv_cache.shape[0] > 1 else b.page_size * RECORD_BYTES
-    b.block_table = block_table.data_ptr()
-    b.block_table_stride = block_table.stride(0) if n_seqs > 1 else b.max_pages
-    b.cu_rows, b.seq_lens = cu_rows.data_ptr(), seq_lens.data_ptr()
-    b.n_rows, b.n_seqs, b.status = int(n_rows), n_seqs, _ptr(status)
-    return b
+    if n_pages and page_size and (byte_stride != 1 or (page_size > 1 and record_stride != RECORD_BYTES)):
+        _fail(SMLA_ERR_STRIDE, what, "the records of a page are contiguous")
+    i32 = torch.int32
+    if (block_table.dtype != i32 or cu_rows.dtype != i32 or seq_lens.dtype != i32 or block_table.dim() != 2 or
+            cu_rows.dim() != 1 or seq_lens.dim() != 1):
+        _fail(SMLA_ERR_SHAPE, what, "block_table is int32 [n_seqs, max_pages], cu_rows and seq_lens int32 vectors")
+    n_seqs, max_pages = block_table.shape
+    table_stride, entry_stride = block_table.stride()
+    if seq_lens.shape[0] != n_seqs or cu_rows.shape[0] != n_seqs + 1:
+        _fail(SMLA_ERR_SHAPE, what, "n_seqs + 1 entries of cu_rows and n_seqs of seq_lens for n_seqs rows of block_table")
+    if n_seqs and ((max_pages > 1 and entry_stride != 1) or cu_rows.stride(0) != 1 or
+                   (n_seqs > 1 and seq_lens.stride(0) != 1)):
+        _fail(SMLA_ERR_STRIDE, what, "block_table rows, cu_rows and seq_lens are contiguous")
+    if status is not None and (status.dtype != i32 or status.numel() < 1):
+        _fail(SMLA_ERR_SHAPE, what, "status is int32 [1]")
+    return (kv_cache.data_ptr(), n_pages, page_stride if n_pages > 1 else page_size * RECORD_BYTES, page_size, max_pages,
+            block_table.data_ptr(), table_stride if n_seqs > 1 else max_pages, cu_rows.data_ptr(), seq_lens.data_ptr(),
+            n_rows, n_seqs, None if status is None else status.data_ptr())
 
 
-def _paged_copy(what, kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status) -> None:
-    _need(latent.dtype in DTYPES and rope.dtype == latent.dtype, SMLA_ERR_SHAPE,
-          f"{what}: latent and rope of one type, bf16, f16 or f32")
-    _need(latent.dim() == 2 and latent.shape[1] == LATENT_DIM and rope.dim() == 2 and
-          tuple(rope.shape) == (latent.shape[0], ROPE_DIM), SMLA_ERR_SHAPE,
-          f"{what}: latent [rows, {LATENT_DIM}] and rope [rows, {ROPE_DIM}]")
-    n = int(latent.shape[0])
-    _need(n == 0 or (latent.stride(1) == 1 and rope.stride(1) == 1), SMLA_ERR_STRIDE,
-          f"{what}: the rows of latent and rope are contiguous")
-    _on_device(what, latent, rope)
-    b = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
-    # (the stride of a single row says nothing)
-    strides = (latent.stride(0), rope.stride(0)) if n > 1 else (LATENT_DIM, ROPE_DIM)
-    rc = getattr(lib, what)(ctypes.byref(b), latent.data_ptr(), strides[0], rope.data_ptr(), strides[1],
-                            DTYPES[latent.dtype], _stream(stream))
+def _paged_copy(what, call, kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status) -> None:
+    dtype = DTYPES.get(latent.dtype)
+    if dtype is None or rope.dtype != latent.dtype:
+        _fail(SMLA_ERR_SHAPE, what, "latent and rope of one type, bf16, f16 or f32")
+    if latent.dim() != 2 or rope.dim() != 2:
+        _fail(SMLA_ERR_SHAPE, what, f"latent [rows, {LATENT_DIM}] and rope [rows, {ROPE_DIM}]")
+    n, dims = latent.shape
+    if dims != LATENT_DIM or rope.shape[0] != n or rope.shape[1] != ROPE_DIM:
+        _fail(SMLA_ERR_SHAPE, what, f"latent [rows, {LATENT_DIM}] and rope [rows, {ROPE_DIM}]")
+    ls, l1 = latent.stride()
+    rs, r1 = rope.stride()
+    if n and (l1 != 1 or r1 != 1):
+        _fail(SMLA_ERR_STRIDE, what, "the rows of latent and rope are contiguous")
+    if n <= 1:  # (the stride of a single row says nothing)
+        ls, rs = LATENT_DIM, ROPE_DIM
+    batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
+    device = _current_device(what, (latent, rope, kv_cache, block_table, cu_rows, seq_lens, status))
+    rc = call(PagedBatch(*batch), latent.data_ptr(), ls, rope.data_ptr(), rs, dtype, _launch_stream(stream, device))
     if rc != 0:
         raise SmlaError(rc, what)
 
@@ -419,7 +430,8 @@ def smla_paged_write(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.T
     is negative are skipped; ids >= n_pages and positions past the table are
     skipped and set STATUS_INDEX_OOB.  The rows' positions must lie in different
     slots.  See include/smla.h."""
-    _paged_copy("smla_paged_write", kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status)
+    _paged_copy("smla_paged_write", lib.smla_paged_write, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
+                stream, status)
 
 
 def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor, seq_lens: torch.Tensor,
@@ -429,7 +441,8 @@ def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: 
     [rows, 64] (bf16, f16 or f32).  Batch as smla_paged_write: row r of sequence
     b gets position seq_lens[b] - (cu_rows[b + 1] - r); masked positions give
     zeros, rows of no sequence are left as they were.  See include/smla.h."""
-    _paged_copy("smla_paged_read", kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status)
+    _paged_copy("smla_paged_read", lib.smla_paged_read, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
+                stream, status)
 
 
 def smla_paged_attend_workspace_size(n_rows: int, num_heads: int, n_seqs: int, page_size: int, max_pages: int) -> int:
@@ -454,42 +467,46 @@ def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
     workspace_tensor: uint8, smla_paged_attend_workspace_size bytes; without it
     one is allocated for this call on its stream.  See include/smla.h."""
     what = "smla_paged_attend"
-    _need(q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[2] == QK_DIM, SMLA_ERR_SHAPE,
-          f"{what}: q is bf16 [rows, heads, {QK_DIM}]")
-    n, heads = int(q.shape[0]), int(q.shape[1])
-    _need(out.dtype == torch.bfloat16 and tuple(out.shape) == (n, heads, LATENT_DIM), SMLA_ERR_SHAPE,
-          f"{what}: out is bf16 [rows, heads, {LATENT_DIM}]")
-    _need(q.numel() == 0 or (q.stride(2) == 1 and out.stride(2) == 1), SMLA_ERR_STRIDE,
-          f"{what}: the last dimension of q and out is contiguous")
-    _need(sink is None or (sink.dtype == torch.float32 and tuple(sink.shape) == (heads,) and sink.is_contiguous()),
-          SMLA_ERR_SHAPE, f"{what}: sink is f32 [heads]")
-    _need(lse is None or (lse.dtype == torch.float32 and tuple(lse.shape) == (n, heads) and lse.is_contiguous()),
-          SMLA_ERR_SHAPE, f"{what}: lse is contiguous f32 [rows, heads]")
-    _on_device(what, q, out, sink, lse, workspace_tensor)
-    p = PagedAttendParams()
-    p.batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
-    p.num_heads, p.causal, p.sm_scale = heads, int(bool(causal)), float(sm_scale)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != QK_DIM:
+        _fail(SMLA_ERR_SHAPE, what, f"q is bf16 [rows, heads, {QK_DIM}]")
+    n, heads, _ = q.shape
+    if out.dtype != torch.bfloat16 or out.shape != (n, heads, LATENT_DIM):
+        _fail(SMLA_ERR_SHAPE, what, f"out is bf16 [rows, heads, {LATENT_DIM}]")
+    q_row, q_head, q1 = q.stride()
+    o_row, o_head, o1 = out.stride()
+    if n and (q1 != 1 or o1 != 1):
+        _fail(SMLA_ERR_STRIDE, what, "the last dimension of q and out is contiguous")
     # (the stride of a dimension of one element says nothing)
-    p.q, p.out = q.data_ptr(), out.data_ptr()
-    p.q_stride_head = q.stride(1) if heads > 1 else QK_DIM
-    p.out_stride_head = out.stride(1) if heads > 1 else LATENT_DIM
-    p.q_stride_row = q.stride(0) if n > 1 else heads * p.q_stride_head
-    p.out_stride_row = out.stride(0) if n > 1 else heads * p.out_stride_head
-    p.sink, p.lse = _ptr(sink), _ptr(lse)
+    if heads == 1:
+        q_head, o_head = QK_DIM, LATENT_DIM
+    if n <= 1:
+        q_row, o_row = heads * q_head, heads * o_head
+    if sink is not None and (sink.dtype != torch.float32 or sink.shape != (heads,) or not sink.is_contiguous()):
+        _fail(SMLA_ERR_SHAPE, what, "sink is f32 [heads]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
+        _fail(SMLA_ERR_SHAPE, what, "lse is contiguous f32 [rows, heads]")
+    batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
+    device = _current_device(what, (q, out, sink, lse, kv_cache, block_table, cu_rows, seq_lens, status,
+                                    workspace_tensor))
+    p = PagedAttendParams(PagedBatch(*batch), heads, 1 if causal else 0, q.data_ptr(), q_row, q_head, float(sm_scale),
+                          None if sink is None else sink.data_ptr(), out.data_ptr(), o_row, o_head,
+                          None if lse is None else lse.data_ptr())
+    s = _launch_stream(stream, device)
     ws = workspace_tensor
-    s = _stream(stream)
     if ws is None:
-        nbytes = int(lib.smla_paged_attend_workspace_size(ctypes.byref(p)))
+        nbytes = lib.smla_paged_attend_workspace_size(p)
         if nbytes:
             # a block of this call's own, on its stream: calls on other streams and
             # other captured graphs never share it
-            if stream is None or isinstance(stream, torch.cuda.Stream):
-                on = stream
-            else:
-                on = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
-            with torch.cuda.stream(on):
+            if stream is None:
                 ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    rc = lib.smla_paged_attend(ctypes.byref(p), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), s)
+            else:
+                if not isinstance(stream, torch.cuda.Stream):
+                    stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
+                with torch.cuda.stream(stream):
+                    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    rc = lib.smla_paged_attend(p, None if ws is None else ws.data_ptr(),
+                               0 if ws is None else ws.numel() * ws.element_size(), s)
     if rc != 0:
         raise SmlaError(rc, what)
 

@@ -2,6 +2,7 @@
 // code; the kernels are in smla_paged_copy.cu and smla_paged_attend.cu).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -64,11 +65,23 @@ int check_attend(const smla_paged_attend_params* p, bool* empty) {
   return SMLA_OK;
 }
 
-int sm_count(int* n) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *n < 2)
-    return SMLA_ERR_DEVICE;
+// The current device's SM count, and whether it can run the kernels; asked once
+// per device (a call can take less time on the GPU than the queries here).
+constexpr int kMaxDevices = 64;
+std::atomic<int32_t> g_sms[kMaxDevices];  // 0: not asked yet, -1: not an sm_103
+
+int device_sms(int* n) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SMLA_ERR_DEVICE;
+  int32_t v = g_sms[dev].load(std::memory_order_relaxed);
+  if (v == 0) {
+    int count = 0;
+    if (cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SMLA_ERR_DEVICE;
+    v = smla_device_check() == SMLA_OK && count >= 2 ? count : -1;
+    g_sms[dev].store(v, std::memory_order_relaxed);
+  }
+  if (v < 0) return SMLA_ERR_DEVICE;
+  *n = v;
   return SMLA_OK;
 }
 
@@ -84,7 +97,8 @@ int smla_paged_write(const smla_paged_batch* batch, const void* latent, int64_t 
   bool empty;
   int rc = check_copy(batch, latent, latent_stride, rope, rope_stride, dtype, &empty);
   if (rc != SMLA_OK || empty) return rc;
-  rc = smla_device_check();
+  int sms = 0;
+  rc = device_sms(&sms);
   if (rc != SMLA_OK) return rc;
   const cudaError_t err =
       launch_paged_write(*batch, latent, latent_stride, rope, rope_stride, dtype, static_cast<cudaStream_t>(stream));
@@ -96,7 +110,8 @@ int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_
   bool empty;
   int rc = check_copy(batch, latent, latent_stride, rope, rope_stride, dtype, &empty);
   if (rc != SMLA_OK || empty) return rc;
-  rc = smla_device_check();
+  int sms = 0;
+  rc = device_sms(&sms);
   if (rc != SMLA_OK) return rc;
   const cudaError_t err =
       launch_paged_read(*batch, latent, latent_stride, rope, rope_stride, dtype, static_cast<cudaStream_t>(stream));
@@ -113,7 +128,7 @@ size_t smla_paged_attend_workspace_size(const smla_paged_attend_params* params) 
       int64_t(b.max_pages) * b.page_size > (int64_t(1) << 30))
     return 0;
   empty = b.n_rows == 0 || b.n_seqs == 0;
-  if (empty || sm_count(&sms) != SMLA_OK) return 0;
+  if (empty || device_sms(&sms) != SMLA_OK) return 0;
   return size_t(paged_attend_plan(*params, sms).total);
 }
 
@@ -121,10 +136,8 @@ int smla_paged_attend(const smla_paged_attend_params* params, void* workspace, s
   bool empty;
   int rc = check_attend(params, &empty);
   if (rc != SMLA_OK || empty) return rc;
-  rc = smla_device_check();
-  if (rc != SMLA_OK) return rc;
   int sms = 0;
-  rc = sm_count(&sms);
+  rc = device_sms(&sms);
   if (rc != SMLA_OK) return rc;
   const AttendPlan plan = paged_attend_plan(*params, sms);
   if (workspace == nullptr || uint64_t(workspace_bytes) < uint64_t(plan.total)) return SMLA_ERR_WORKSPACE;

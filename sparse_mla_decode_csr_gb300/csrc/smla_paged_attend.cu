@@ -85,13 +85,20 @@ constexpr int kOffQ = kOffV + 2 * kStageV;
 constexpr int kQBlock = kCtaRows * 128;
 constexpr int kOffP = kOffQ + 9 * kQBlock;
 constexpr int kOffMisc = kOffP + kCtaRows * 128;
+// narrow kernel: K of all 64 keys, in two stages; V is the same memory
+constexpr int kStageNarrow = 9 * kTileKeys * 128;
+constexpr int kOffQNarrow = 2 * kStageNarrow;
+constexpr int kOffPNarrow = kOffQNarrow + 9 * kQBlock;
+constexpr int kOffMiscNarrow = kOffPNarrow + kCtaRows * 128;
+constexpr int kNarrowThreads = 14 * 32;
+constexpr int kNarrowQk = 12;  // and 13: PV
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;              // two S buffers of two accumulators of 32 columns behind O's 256
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(kPairRows, 256, 0, 1);
-constexpr int kMinPairSlots = 3;              // slots below which no further pair is used
+constexpr int kMinWorkerSlots = 3;            // slots below which no further worker is used
 
 struct AttendArgs {
   PagedArgs b;
@@ -103,11 +110,12 @@ struct AttendArgs {
   const float* sink;
   float scale_log2;
   int32_t heads, tokens, causal;  // tokens: of a row tile
-  int32_t pairs;
+  int32_t workers;                // pairs of CTAs, or CTAs of the narrow kernel
+  int32_t part_rows;              // rows of a partial: 128, or 64
   int32_t coverage;               // positions the block table can hold
-  float* o_part;                  // [2 pairs][128][512]
-  float* ml_part;                 // [2 pairs][128][2]
-  int32_t* merge;                 // [pairs][4]: rows to merge (0: none), first token row, first pair, its last slot
+  float* o_part;                  // [2 workers][part_rows][512]
+  float* ml_part;                 // [2 workers][part_rows][2]
+  int32_t* merge;                 // [workers][4]: rows to merge (0: none), first token row, first worker
 };
 
 struct Misc {
@@ -120,15 +128,17 @@ struct Misc {
   int32_t stall;
   int32_t first_seq, first_j;
   int64_t first_slot, beg, end, total;
-  int64_t warp_sum[kAttendThreads / 32];
+  int64_t warp_sum[16];
   float tmax[2][128];
   float lsum[128];
+  float alpha[2][kCtaRows], factor[kCtaRows];  // narrow kernel: per row
   // per tile: a byte per 8 keys, bit: a key before the end that has no record
   uint8_t flags[4][kTileKeys / 8];
 };
-static_assert(sizeof(Misc) <= 2816, "shared memory");
-constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc)) + 1024;
-static_assert(kAttendSmem <= 232448, "shared memory of a CTA");
+static_assert(sizeof(Misc) <= 3072, "shared memory");
+constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc));
+constexpr int kNarrowSmem = kOffMiscNarrow + int(sizeof(Misc));
+static_assert(kAttendSmem <= 232448 && kNarrowSmem <= 232448, "shared memory of a CTA");
 
 // ---- cluster helpers ----
 
@@ -220,8 +230,12 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
 // Gives up the pipeline of both CTAs (see wait_for).
 __device__ __noinline__ void give_up(Misc* ms, int32_t* status) {
   if (atomicExch(&ms->dead, 1) == 0 && status) atomicOr(status, SMLA_STATUS_TIMEOUT);
-  const uint32_t other = map_to(smem_u32(&ms->dead), cluster_rank() ^ 1u);
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(other), "r"(1) : "memory");
+  uint32_t ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  if (ctas == 2) {
+    const uint32_t other = map_to(smem_u32(&ms->dead), cluster_rank() ^ 1u);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(other), "r"(1) : "memory");
+  }
 }
 
 // Waits for the phase of `bar`; false after the limit, or once the pair has
@@ -371,10 +385,11 @@ struct Units {
   }
 };
 
-// The pair's range of slots and the row tile it starts in, by all threads.
-__device__ void find_range(const AttendArgs& a, Misc* ms, int32_t pair) {
+// The worker's range of slots and the row tile it starts in, by all threads.
+template <int kThreads>
+__device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_t worker) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t per = (a.b.n_seqs + kAttendThreads - 1) / kAttendThreads;
+  const int32_t per = (a.b.n_seqs + kThreads - 1) / kThreads;
   const int32_t s0 = min(tid * per, a.b.n_seqs), s1 = min(s0 + per, a.b.n_seqs);
   int64_t sum = 0;
   for (int32_t s = s0; s < s1; ++s) {
@@ -391,13 +406,13 @@ __device__ void find_range(const AttendArgs& a, Misc* ms, int32_t pair) {
   __syncthreads();
   int64_t before = inc - sum, total = 0;
 #pragma unroll
-  for (int w = 0; w < kAttendThreads / 32; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     const int64_t v = ms->warp_sum[w];
     if (w < warp) before += v;
     total += v;
   }
-  const int64_t G = max(min(int64_t(a.pairs), total / kMinPairSlots), int64_t(1));
-  const int64_t beg = pair < G ? pair * total / G : total, end = pair < G ? (pair + 1) * total / G : total;
+  const int64_t G = max(min(int64_t(a.workers), total / kMinWorkerSlots), int64_t(1));
+  const int64_t beg = worker < G ? worker * total / G : total, end = worker < G ? (worker + 1) * total / G : total;
   if (tid == 0) {
     ms->beg = beg;
     ms->end = end;
@@ -534,13 +549,13 @@ __device__ __noinline__ Raw load_scattered(uint64_t rec) {
   return r;
 }
 
-// q of a unit's rows of this CTA, by one loader group (w: the warp of it).
-__device__ __noinline__ void load_q(const AttendArgs& a, uint32_t base, uint32_t rank, int w, int32_t row0,
+// q of a unit's rows of this CTA, zeros behind them, by `warps` warps (w: which).
+__device__ __noinline__ void load_q(const AttendArgs& a, uint32_t q_at, uint32_t rank, int w, int warps, int32_t row0,
                                     int32_t rows) {
   const int lane = threadIdx.x & 31;
-  for (int i = w; i < kCtaRows; i += kLoaderWarps) {
+  for (int i = w; i < kCtaRows; i += warps) {
     const int32_t m = int32_t(rank) * kCtaRows + i;
-    const uint32_t dst = base + kOffQ + i * 128;
+    const uint32_t dst = q_at + i * 128;
     const int32_t tok = m / a.heads;
     const uint16_t* src = a.q + int64_t(row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head;
 #pragma unroll
@@ -557,16 +572,21 @@ __device__ __noinline__ void load_q(const AttendArgs& a, uint32_t base, uint32_t
 
 // ---- roles ----
 
+// kPair: two groups of four warps take turns at the tiles, a CTA loads 32 keys of
+// each.  Else (the narrow kernel) all eight warps load the 64 keys of every tile.
+template <bool kPair>
 __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
+  constexpr int kWarps = kPair ? kLoaderWarps : 2 * kLoaderWarps;
+  constexpr int kRowsK = kPair ? kOwnKeys : kTileKeys;  // keys in a 64-dim block of K
+  constexpr int kStage = kPair ? kStageK : kStageNarrow;
   const int lane = threadIdx.x & 31, index = (threadIdx.x >> 5) - kFirstLoader;
-  const uint32_t group = index / kLoaderWarps;  // takes the tiles g with g % 2 == group
-  const int w = index % kLoaderWarps;           // keys [8 w, 8 w + 8) of the CTA's 32
-  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0) + 8 * group;
+  const uint32_t group = kPair ? index / kLoaderWarps : 0;  // takes the tiles g with g % 2 == group
+  const int w = index % kWarps;                             // keys [8 w, 8 w + 8) of the CTA's
+  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0);
   // where this lane's chunks go: row key = 8 w + j of block lane / 8, swizzled
   // column (lane & 7) ^ j
-  const uint32_t stage_k = base + kOffK + group * kStageK;
-  const uint32_t k_at = stage_k + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
-  const uint32_t rope_at = stage_k + 8 * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
+  const uint32_t k_at = base + kOffK + (lane >> 3) * (kRowsK * 128) + w * kKeysPerWarp * 128;
+  const uint32_t rope_at = base + kOffK + 8 * (kRowsK * 128) + w * kKeysPerWarp * 128;
 
   // A cursor over the group's tiles: the records' addresses are looked up while
   // the tile before is converted; their loads set out as soon as its registers are
@@ -586,14 +606,14 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   };
   if (group == 1) step();
 
-  // Page id and offset at the cursor: lanes 0-7 this warp's keys, lanes 8-15 the
-  // peer warp's (both CTAs need to know which keys have no record).  The id is
+  // Page id and offset at the cursor: lanes 0-7 this warp's keys, in a pair lanes
+  // 8-15 the peer warp's (both CTAs need to know which keys have no record).  The id is
   // first looked at when the loads set out; in: a key before the end.
   auto look_up = [&](int32_t& id, int32_t& offset, bool& in) {
     id = -1;
-    const int32_t owner = int32_t(rank) ^ (lane >> 3);
+    const int32_t owner = kPair ? int32_t(rank) ^ (lane >> 3) : 0;
     const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 7);
-    in = more && lane < 2 * kKeysPerWarp && pos < end;  // (the end lies within the table)
+    in = more && lane < (kPair ? 2 : 1) * kKeysPerWarp && pos < end;  // (the end lies within the table)
     if (in) {
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
@@ -629,21 +649,23 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   int32_t id, offset = 0;
   bool in;
   look_up(id, offset, in);
-  for (uint32_t g = group; more; g += 2) {
+  for (uint32_t g = group; more; g += kPair ? 2 : 1) {
+    const uint32_t stage = kPair ? group : g & 1;
     const uint64_t rec = address(id, offset);
     const uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && in);
     issue(rec, raw);
     if (t == t0) {
-      // q of the unit, once the last QK of the unit before is done.  (That is on
-      // the other group's barrier.  A parity tells a phase from its neighbours only:
-      // QK(g - 2) on this group's own says that QK(g - 3) is past.)
-      if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
-      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
-      load_q(a, base, rank, w, row0, rows);
+      // q of the unit, once the last QK of the unit before is done.  (A parity tells
+      // a phase from its neighbours only, so QK(g - 3) has to be known as past: in a
+      // pair, where that is the other group's barrier, QK(g - 2) says so; else the
+      // wait for PV(g - 3) has.)
+      if (kPair && g >= 2 && !warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1)) return;
+      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[stage ^ 1], ((g - 1) >> 1) & 1)) return;
+      load_q(a, base + (kPair ? kOffQ : kOffQNarrow), rank, w, kWarps, row0, rows);
       if (lane == 0) arrive_at(q_full);
     }
     step();
-    step();
+    if (kPair) step();
     look_up(id, offset, in);
     // convert the landed records
     uint32_t v[kKeysPerWarp][2][4];
@@ -679,27 +701,30 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
         for (int i = 0; i < 2; ++i)
           dequant8(raw.lat[j][i], __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232), v[j][i]);
     }
-    if (g >= 2 && (!warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1) ||
-                   !warp_wait(ms, a, &ms->v_full[group], ((g - 2) >> 1) & 1)))
-      return;
+    if (g >= 2) {
+      const uint32_t parity = ((g - 2) >> 1) & 1;
+      if (kPair ? !warp_wait(ms, a, &ms->qk_done[stage], parity) || !warp_wait(ms, a, &ms->v_full[stage], parity)
+                : !warp_wait(ms, a, &ms->pv_done[stage], parity))
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j) {
-      const uint32_t at = k_at + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
+      const uint32_t at = k_at + stage * kStage + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
       st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
-      st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
+      st_shared_v4(at + 4 * (kRowsK * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t key = 4 * i + (lane >> 3);
       const uint4 r = raw.rope[i];
-      st_shared_v4(rope_at + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
+      st_shared_v4(rope_at + stage * kStage + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
     }
-    if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t(holes >> (8 * lane));
+    if (lane < (kPair ? 2 : 1)) ms->flags[g & 3][(kPair ? rank ^ lane : 0) * kLoaderWarps + w] = uint8_t(holes >> (8 * lane));
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&ms->k_ready[group]);
-      arrive_at(k_full);
+      if (kPair) mbar_arrive(&ms->k_ready[stage]);
+      arrive_at(k_full + 8 * stage);
     }
   }
 }
@@ -831,6 +856,15 @@ __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, ui
   }
 }
 
+// The last part of a row tile: the merge kernel joins the parts from the worker
+// that holds its first key tile up to this one.
+__device__ __noinline__ void name_merge(const AttendArgs& a, const Misc* ms, int32_t worker, const Unit& u) {
+  const int64_t G = max(min(int64_t(a.workers), ms->total / kMinWorkerSlots), int64_t(1));
+  a.merge[worker * 4 + 1] = u.row0;
+  a.merge[worker * 4 + 2] = int32_t(((u.slot + 2) * G - 1) / ms->total);
+  a.merge[worker * 4] = u.tokens * a.heads;
+}
+
 __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem, uint32_t rank,
                                              int32_t pair) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -948,8 +982,8 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
     const int64_t tok_row = int64_t(u.row0) + tok;
     if (live && half == 0) {
       if (!whole) {
-        a.ml_part[(part * kPairRows + m) * 2] = ref;
-        a.ml_part[(part * kPairRows + m) * 2 + 1] = l;
+        a.ml_part[(part * a.part_rows + m) * 2] = ref;
+        a.ml_part[(part * a.part_rows + m) * 2 + 1] = l;
       }
     }
     if (whole) {
@@ -958,7 +992,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       if (live && half == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
     }
     uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 256 * half;
-    float* pdst = a.o_part + (part * kPairRows + m) * kLatent + 256 * half;
+    float* pdst = a.o_part + (part * a.part_rows + m) * kLatent + 256 * half;
 #pragma unroll 1
     for (int c = 0; c < 256; c += 16) {
       uint32_t o[16];
@@ -981,21 +1015,23 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
     }
     tc_fence_before();
     if (!whole && u.t0 > 0 && u.t1 == u.tiles && rank == 0 && threadIdx.x == 0) {
-      // the row tile's last part: the merge kernel joins the parts from the pair
-      // that holds its first key tile up to this one
-      const int64_t G = max(min(int64_t(a.pairs), ms->total / kMinPairSlots), int64_t(1));
-      a.merge[pair * 4 + 1] = u.row0;
-      a.merge[pair * 4 + 2] = int32_t(((u.slot + 2) * G - 1) / ms->total);
-      a.merge[pair * 4] = u.tokens * a.heads;
+      name_merge(a, ms, pair, u);
     }
   }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 paged_attend_kernel(const __grid_constant__ AttendArgs a) {
-  extern __shared__ uint8_t raw_smem[];
-  const uint32_t base = (smem_u32(raw_smem) + 1023u) & ~1023u;
-  Misc* ms = reinterpret_cast<Misc*>(raw_smem + (base - smem_u32(raw_smem)) + kOffMisc);
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  const uint32_t base = smem_u32(raw_smem);
+  if (base & 1023u) {  // (the operands' swizzle needs it; the same in every CTA)
+    if (threadIdx.x == 0) {
+      a.merge[(blockIdx.x >> 1) * 4] = 0;
+      if (a.b.status) atomicOr(a.b.status, SMLA_STATUS_SMEM_LAYOUT);
+    }
+    return;
+  }
+  Misc* ms = reinterpret_cast<Misc*>(raw_smem + kOffMisc);
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1;
   const int warp = threadIdx.x >> 5;
@@ -1025,7 +1061,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
                  : "memory");
     tc_fence_before();
   }
-  find_range(a, ms, pair);
+  find_range<kAttendThreads>(a, ms, pair);
   __syncthreads();
   cluster_sync();
   tc_fence_after();
@@ -1033,7 +1069,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   if (warp < kFirstLoader) {
     softmax_role(a, ms, base, tmem, rank, pair);
   } else if (warp < kIssuerQk) {
-    loader_role(a, ms, base, rank);
+    loader_role<true>(a, ms, base, rank);
   } else if (warp == kCopier) {
     if ((threadIdx.x & 31) == 0) copier_role(a, ms, base, rank);
   } else if (rank == 0) {
@@ -1061,6 +1097,273 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   }
 }
 
+// ---- the narrow kernel ----
+//
+// Up to kN = 16, 32 or 64 rows a tile (single tokens, a few drafted ones): no
+// pair, since half of its rows or more would be empty, and each CTA loads all 64
+// keys of a tile once for both products.
+//   S[64, 64] = Q K^T as above (M = 64: rows 16 w .. sit in lanes 32 w .. of TMEM);
+//   O^T[128 b .. + 128, kN] += V^T P^T, b = 0 .. 3: the four M = 128 blocks of
+// dims take 4 kN columns, and V^T is the K tile read MN-major, so nothing is copied.
+// A row's scores are one thread's; the factors of O's columns go through shared
+// memory.
+
+// kRows: whether this warp has rows (with kN < 64 some only rescale and store O).
+template <int kN, bool kRows>
+__device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
+                                                    int32_t worker) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t m = 16 * warp + lane;  // this thread's row (lanes 0-15)
+  const bool mine = kRows && lane < 16;
+  const int32_t tok = m / a.heads, head = m - tok * a.heads;
+  const uint32_t lane_base = tmem + (uint32_t(warp) << 21);
+  const uint32_t p_row = base + kOffPNarrow + m * 128;
+  const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0;
+  if (ms->stall) wait_for(ms, a, &ms->never, 0);
+  while (units.next(a, u)) {
+    const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
+    const bool live = mine && m < rows;
+    const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
+    float ref = -INFINITY, l = 0.f;
+    for (int32_t t = t0; t < t1; ++t, ++g) {
+      const uint32_t stage = g & 1;
+      wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
+      tc_fence_after();
+      float x[kTileKeys];
+      if constexpr (kRows) {
+#pragma unroll
+        for (int c = 0; c < kTileKeys; c += 16)
+          tmem_ld16(lane_base + kTmemS + 64 * stage + c, *reinterpret_cast<uint32_t(*)[16]>(x + c));
+      }
+      const uint2 flags = *reinterpret_cast<const uint2*>(&ms->flags[g & 3][0]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->s_empty[stage]);
+      bool move = false;
+      float use = 0.f;
+      if constexpr (kRows) {
+        if (a.scale_log2 <= 0.f) {
+          const float by = a.scale_log2 < 0.f ? -1.f : 0.f;
+#pragma unroll
+          for (int c = 0; c < kTileKeys; ++c) x[c] *= by;
+        }
+        const int32_t n = see - t * kTileKeys;
+        if (__any_sync(0xffffffffu, n < kTileKeys) || (flags.x | flags.y)) {
+          const uint32_t lo = ~flags.x & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+          const uint32_t hi = ~flags.y & (n >= 64 ? 0xffffffffu : n <= 32 ? 0u : (1u << (n - 32)) - 1u);
+#pragma unroll
+          for (int c = 0; c < kTileKeys; ++c) x[c] = ((c < 32 ? lo : hi) >> (c & 31)) & 1u ? x[c] : -INFINITY;
+        }
+        float tm = x[0];
+#pragma unroll
+        for (int c = 1; c < kTileKeys; ++c) tm = fmaxf(tm, x[c]);
+        tm *= scale;
+        move = live && tm > ref + kMoveMargin;
+        const float nref = move ? tm : ref;
+        use = nref == -INFINITY ? 0.f : nref;
+        const float alpha = move ? ex2(ref - use) : 1.f;
+        ref = nref;
+        l *= alpha;
+        if (mine) ms->alpha[stage][m] = alpha;
+      }
+      const bool moved = named_barrier_or(1, 128, move);
+      uint32_t p[kTileKeys / 2];
+      if constexpr (kRows) {
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kTileKeys / 2; ++c) {
+          float y0, y1;
+          fma2(x[2 * c], x[2 * c + 1], scale, -use, y0, y1);
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          add2(s0, s1, y0, y1, s0, s1);
+          p[c] = pack_bf16x2(y0, y1);
+        }
+        l += s0 + s1;
+      }
+      if (g > 0) wait_for(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
+      if (t > t0 && moved) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4 * kN; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(lane_base + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * ms->alpha[stage][(c & (kN - 1)) + i]);
+          tmem_st16(lane_base + c, o);
+        }
+        tmem_wait_st();
+      }
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          st_shared_v4(p_row + ((c ^ (m & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms->p_full);
+    }
+    const bool whole = t0 == 0 && t1 == u.tiles;
+    const int64_t part = 2 * int64_t(worker) + (t0 > 0 ? 0 : 1);
+    if (mine) {
+      float factor = 1.f;
+      if (whole) {
+        float lse;
+        finish_head_v(ref, l, a.sink != nullptr, a.sink != nullptr && live ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+        if (live && a.lse) a.lse[(int64_t(u.row0) + tok) * a.heads + head] = lse;
+      } else if (live) {
+        a.ml_part[(part * a.part_rows + m) * 2] = ref;
+        a.ml_part[(part * a.part_rows + m) * 2 + 1] = l;
+      }
+      ms->factor[m] = factor;
+    }
+    named_barrier(1, 128);
+    wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    tc_fence_after();
+    // a lane has dim 128 b + 32 warp + lane of every row
+    const int32_t dim = 32 * warp + lane;
+    int32_t r_tok = 0, r_head = 0;
+#pragma unroll 1
+    for (int c = 0; c < rows; c += 16) {
+      uint32_t o[4][16];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_ld16(lane_base + b * kN + c, o[b]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (c + i >= rows) break;
+        if (whole) {
+          const float f = ms->factor[c + i];
+          uint16_t* dst = a.out + (int64_t(u.row0) + r_tok) * a.o_row + int64_t(r_head) * a.o_head + dim;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            dst[128 * b] = uint16_t(pack_bf16x2(__uint_as_float(o[b][i]) * f, 0.f));
+        } else {
+          float* dst = a.o_part + (part * a.part_rows + c + i) * kLatent + dim;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) dst[128 * b] = __uint_as_float(o[b][i]);
+        }
+        if (++r_head == a.heads) r_head = 0, ++r_tok;
+      }
+    }
+    tc_fence_before();
+    if (!whole && t0 > 0 && t1 == u.tiles && threadIdx.x == 0) name_merge(a, ms, worker, u);
+  }
+}
+
+template <int kN>
+__global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  const uint32_t base = smem_u32(raw_smem);
+  const int32_t worker = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) a.merge[worker * 4] = 0;
+  if (base & 1023u) {
+    if (threadIdx.x == 0 && a.b.status) atomicOr(a.b.status, SMLA_STATUS_SMEM_LAYOUT);
+    return;
+  }
+  Misc* ms = reinterpret_cast<Misc*>(raw_smem + kOffMiscNarrow);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms->k_full[i], 2 * kLoaderWarps);
+      mbar_init(&ms->s_empty[i], 4);
+      mbar_init(&ms->qk_done[i], 1);
+      mbar_init(&ms->pv_done[i], 1);
+    }
+    mbar_init(&ms->q_full, 2 * kLoaderWarps);
+    mbar_init(&ms->p_full, 4);
+    mbar_init(&ms->drain, 2);
+    mbar_init(&ms->never, 1);
+    fence_mbar_init();
+    ms->dead = 0;
+    ms->wait_ns = g_paged_wait_ns ? g_paged_wait_ns : kWaitNs;
+    ms->stall = g_paged_stall;
+  }
+  if (warp == kNarrowQk) {
+    tmem_alloc(&ms->tmem, kTmemCols);
+    tc_fence_before();
+  }
+  find_range<kNarrowThreads>(a, ms, worker);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  if (warp < kFirstLoader) {
+    if (16 * warp < kN) narrow_softmax_role<kN, true>(a, ms, base, tmem, worker);
+    else narrow_softmax_role<kN, false>(a, ms, base, tmem, worker);
+  } else if (warp < kNarrowQk) {
+    loader_role<false>(a, ms, base, 0);
+  } else {
+    const bool qk = warp == kNarrowQk;
+    const uint64_t q0 = smem_desc(base + kOffQNarrow, 16, 1024, kSw128);
+    const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128);
+    const uint64_t v0 = smem_desc(base + kOffK, kTileKeys * 128, 1024, kSw128);
+    const uint64_t p0 = smem_desc(base + kOffPNarrow, 16, 1024, kSw128);
+    Units units;
+    units.start(a, ms);
+    Unit u;
+    uint32_t g = 0, n_units = 0;
+    bool ok = true;
+    while (ok && units.next(a, u)) {
+      const int32_t t0 = u.t0, t1 = u.t1;
+      if (qk) ok = warp_wait(ms, a, &ms->q_full, n_units++ & 1);
+      for (int32_t t = t0; ok && t < t1; ++t, ++g) {
+        const uint32_t stage = g & 1;
+        if (qk) {
+          ok = warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1) &&
+               (g < 2 || warp_wait(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t kd = k0 + uint64_t((stage * kStageNarrow) >> 4);
+#pragma unroll
+            for (int k = 0; k < kQK / 16; ++k)
+              mma_f16_ss(tmem + kTmemS + 64 * stage, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
+                         kd + uint64_t(((k >> 2) * (kTileKeys * 128) + (k & 3) * 32) >> 4),
+                         idesc_bf16(kCtaRows, kTileKeys, 0, 0), k > 0);
+            mma_commit(&ms->qk_done[stage]);
+          }
+        } else {
+          ok = warp_wait(ms, a, &ms->p_full, g & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint64_t vd = v0 + uint64_t((stage * kStageNarrow) >> 4);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+#pragma unroll
+              for (int k = 0; k < kTileKeys / 16; ++k)
+                mma_f16_ss(tmem + b * kN, vd + uint64_t((b * 2 * (kTileKeys * 128) + k * 2048) >> 4), p0 + uint64_t(k * 2),
+                           idesc_bf16(128, kN, 1, 0), (t == t0 && k == 0) ? 0u : 1u);
+            mma_commit(&ms->pv_done[stage]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+    if (lane == 0) {  // every MMA complete before the memory it reads goes away
+      mma_commit(&ms->drain);
+      if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kNarrowQk) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
 // Joins the partials of a row tile shared between pairs: with m = max_c m_c,
 //   l = sum_c l_c 2^(m_c - m),  O = sum_c O_c 2^(m_c - m),
 // and the sink enters once.  A warp per row, one block per 8 rows of a pair's
@@ -1076,7 +1379,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
   float mx = -INFINITY;
   for (int32_t c = first; c <= last; ++c) {
     const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
-    mx = fmaxf(mx, a.ml_part[(part * kPairRows + m) * 2]);
+    mx = fmaxf(mx, a.ml_part[(part * a.part_rows + m) * 2]);
   }
   const float use = mx == -INFINITY ? 0.f : mx;
   float l = 0.f, o[16];
@@ -1084,9 +1387,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
   for (int i = 0; i < 16; ++i) o[i] = 0.f;
   for (int32_t c = first; c <= last; ++c) {
     const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
-    const float wgt = ex2(a.ml_part[(part * kPairRows + m) * 2] - use);
-    l += a.ml_part[(part * kPairRows + m) * 2 + 1] * wgt;
-    const float4* src = reinterpret_cast<const float4*>(a.o_part + (part * kPairRows + m) * kLatent) + lane;
+    const float wgt = ex2(a.ml_part[(part * a.part_rows + m) * 2] - use);
+    l += a.ml_part[(part * a.part_rows + m) * 2 + 1] * wgt;
+    const float4* src = reinterpret_cast<const float4*>(a.o_part + (part * a.part_rows + m) * kLatent) + lane;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = src[32 * i];
@@ -1113,23 +1416,45 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __g
 
 }  // namespace
 
+// Rows of a narrow tile (16, 32, 64), or 0 for the pair kernel: by the mean number
+// of rows (tokens x heads) of a sequence, since the lengths themselves are on the
+// device.  Any split is computed correctly by either.
+static int narrow_rows(const smla_paged_attend_params& p) {
+  if (p.num_heads > kCtaRows) return 0;
+  const int64_t mean = (p.batch.n_rows * p.num_heads + p.batch.n_seqs - 1) / p.batch.n_seqs;
+  if (mean > kCtaRows) return 0;
+  const int64_t rows = mean > p.num_heads ? mean : p.num_heads;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
 AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
   AttendPlan plan{};
   const smla_paged_batch& b = p.batch;
   if (b.n_rows <= 0 || b.n_seqs <= 0) return plan;
-  const int64_t tokens = p.num_heads >= kPairRows ? 1 : kPairRows / p.num_heads;
+  plan.narrow = narrow_rows(p);
+  plan.part_rows = plan.narrow ? kCtaRows : kPairRows;
+  const int64_t tokens = (plan.narrow ? plan.narrow : kPairRows) / p.num_heads;
   const int64_t coverage = int64_t(b.max_pages) * b.page_size;
   const int64_t most_tiles = coverage > 0 ? (coverage + kTileKeys - 1) / kTileKeys : 1;
   const int64_t row_tiles = (b.n_rows + tokens - 1) / tokens + (b.n_rows < b.n_seqs ? b.n_rows : int64_t(b.n_seqs));
   const int64_t slots = row_tiles * (most_tiles + 1);
-  int64_t pairs = num_sms / 2;
-  if (slots / kMinPairSlots < pairs) pairs = slots / kMinPairSlots;
-  plan.pairs = int32_t(pairs < 1 ? 1 : pairs);
+  int64_t workers = plan.narrow ? num_sms : num_sms / 2;
+  if (slots / kMinWorkerSlots < workers) workers = slots / kMinWorkerSlots;
+  plan.workers = int32_t(workers < 1 ? 1 : workers);
   plan.merge_off = 0;
-  plan.ml_off = (int64_t(plan.pairs) * 16 + 255) & ~int64_t(255);
-  plan.o_off = plan.ml_off + ((int64_t(plan.pairs) * 2 * kPairRows * 8 + 255) & ~int64_t(255));
-  plan.total = plan.o_off + int64_t(plan.pairs) * 2 * kPairRows * kLatent * 4;
+  plan.ml_off = (int64_t(plan.workers) * 16 + 255) & ~int64_t(255);
+  plan.o_off = plan.ml_off + ((int64_t(plan.workers) * 2 * plan.part_rows * 8 + 255) & ~int64_t(255));
+  plan.total = plan.o_off + int64_t(plan.workers) * 2 * plan.part_rows * kLatent * 4;
   return plan;
+}
+
+template <int kN>
+static cudaError_t launch_narrow(const AttendArgs& a, cudaStream_t stream) {
+  const cudaError_t err =
+      cudaFuncSetAttribute(paged_attend_narrow_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+  if (err != cudaSuccess) return err;
+  paged_attend_narrow_kernel<kN><<<a.workers, kNarrowThreads, kNarrowSmem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendPlan& plan, void* workspace,
@@ -1146,21 +1471,31 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
   a.sink = p.sink;
   a.scale_log2 = p.sm_scale * kLog2e;
   a.heads = p.num_heads;
-  a.tokens = kPairRows / p.num_heads;
+  a.tokens = (plan.narrow ? plan.narrow : kPairRows) / p.num_heads;
   a.causal = p.causal != 0;
-  a.pairs = plan.pairs;
+  a.workers = plan.workers;
+  a.part_rows = plan.part_rows;
   a.coverage = p.batch.max_pages * p.batch.page_size;
   char* ws = static_cast<char*>(workspace);
   a.merge = reinterpret_cast<int32_t*>(ws + plan.merge_off);
   a.ml_part = reinterpret_cast<float*>(ws + plan.ml_off);
   a.o_part = reinterpret_cast<float*>(ws + plan.o_off);
-  cudaError_t err =
-      cudaFuncSetAttribute(paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
-  if (err != cudaSuccess) return err;
-  paged_attend_kernel<<<2 * plan.pairs, kAttendThreads, kAttendSmem, stream>>>(a);
-  err = cudaGetLastError();
-  if (err != cudaSuccess || plan.pairs == 1) return err;
-  paged_merge_kernel<<<dim3(unsigned(plan.pairs), kPairRows / kMergeWarps), 32 * kMergeWarps, 0, stream>>>(a);
+  cudaError_t err;
+  if (plan.narrow == 16) {
+    err = launch_narrow<16>(a, stream);
+  } else if (plan.narrow == 32) {
+    err = launch_narrow<32>(a, stream);
+  } else if (plan.narrow == 64) {
+    err = launch_narrow<64>(a, stream);
+  } else {
+    err = cudaFuncSetAttribute(paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
+    if (err != cudaSuccess) return err;
+    paged_attend_kernel<<<2 * plan.workers, kAttendThreads, kAttendSmem, stream>>>(a);
+    err = cudaGetLastError();
+  }
+  if (err != cudaSuccess || plan.workers == 1) return err;
+  paged_merge_kernel<<<dim3(unsigned(plan.workers), unsigned((plan.narrow ? plan.narrow : kPairRows) / kMergeWarps)),
+                       32 * kMergeWarps, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
