@@ -90,8 +90,9 @@ constexpr int kStageNarrow = 9 * kTileKeys * 128;
 constexpr int kOffQNarrow = 2 * kStageNarrow;
 constexpr int kOffPNarrow = kOffQNarrow + 9 * kQBlock;
 constexpr int kOffMiscNarrow = kOffPNarrow + kCtaRows * 128;
-constexpr int kNarrowThreads = 14 * 32;
-constexpr int kNarrowQk = 12;  // and 13: PV
+constexpr int kNarrowThreads = 16 * 32;
+constexpr int kNarrowQk = 12;  // and 13
+constexpr int kNarrowPv = 14;  // and 15
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;              // two S buffers of two accumulators of 32 columns behind O's 256
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
@@ -139,6 +140,14 @@ static_assert(sizeof(Misc) <= 3072, "shared memory");
 constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc));
 constexpr int kNarrowSmem = kOffMiscNarrow + int(sizeof(Misc));
 static_assert(kAttendSmem <= 232448 && kNarrowSmem <= 232448, "shared memory of a CTA");
+
+// ---- launch order ----
+
+// The merge kernel is launched as a dependent of the attend kernel: its blocks may
+// be placed as soon as those of the attend kernel leave, and wait there for all of
+// it to be complete.
+__device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- cluster helpers ----
 
@@ -549,12 +558,13 @@ __device__ __noinline__ Raw load_scattered(uint64_t rec) {
   return r;
 }
 
-// q of a unit's rows of this CTA, zeros behind them, by `warps` warps (w: which).
+// q of a unit's rows of this CTA, zeros behind them, `copies` times over the 64
+// rows, by `warps` warps (w: which).
 __device__ __noinline__ void load_q(const AttendArgs& a, uint32_t q_at, uint32_t rank, int w, int warps, int32_t row0,
-                                    int32_t rows) {
+                                    int32_t rows, int copies) {
   const int lane = threadIdx.x & 31;
   for (int i = w; i < kCtaRows; i += warps) {
-    const int32_t m = int32_t(rank) * kCtaRows + i;
+    const int32_t m = int32_t(rank) * kCtaRows + i % (kCtaRows / copies);
     const uint32_t dst = q_at + i * 128;
     const int32_t tok = m / a.heads;
     const uint16_t* src = a.q + int64_t(row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head;
@@ -572,46 +582,30 @@ __device__ __noinline__ void load_q(const AttendArgs& a, uint32_t q_at, uint32_t
 
 // ---- roles ----
 
-// kPair: two groups of four warps take turns at the tiles, a CTA loads 32 keys of
-// each.  Else (the narrow kernel) all eight warps load the 64 keys of every tile.
+// A loader warp's cursor over the pair's or CTA's tiles, `kStep` tiles at a time,
+// and the addresses of its 8 keys there.
 template <bool kPair>
-__device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
-  constexpr int kWarps = kPair ? kLoaderWarps : 2 * kLoaderWarps;
-  constexpr int kRowsK = kPair ? kOwnKeys : kTileKeys;  // keys in a 64-dim block of K
-  constexpr int kStage = kPair ? kStageK : kStageNarrow;
-  const int lane = threadIdx.x & 31, index = (threadIdx.x >> 5) - kFirstLoader;
-  const uint32_t group = kPair ? index / kLoaderWarps : 0;  // takes the tiles g with g % 2 == group
-  const int w = index % kWarps;                             // keys [8 w, 8 w + 8) of the CTA's
-  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0);
-  // where this lane's chunks go: row key = 8 w + j of block lane / 8, swizzled
-  // column (lane & 7) ^ j
-  const uint32_t k_at = base + kOffK + (lane >> 3) * (kRowsK * 128) + w * kKeysPerWarp * 128;
-  const uint32_t rope_at = base + kOffK + 8 * (kRowsK * 128) + w * kKeysPerWarp * 128;
-
-  // A cursor over the group's tiles: the records' addresses are looked up while
-  // the tile before is converted; their loads set out as soon as its registers are
-  // free and land while the other group works.
+struct Cursor {
   Units units;
-  units.start(a, ms);
   bool more;
   int32_t t, t0, t1, end, seq, row0, rows;  // of the cursor's unit
-  auto next_unit = [&]() {
+
+  __device__ __forceinline__ void next_unit(const AttendArgs& a) {
     Unit u;
     more = units.next(a, u);
     t = t0 = u.t0, t1 = u.t1, end = u.end, seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
-  };
-  next_unit();
-  auto step = [&]() {
-    if (more && ++t == t1) next_unit();
-  };
-  if (group == 1) step();
-
-  // Page id and offset at the cursor: lanes 0-7 this warp's keys, in a pair lanes
-  // 8-15 the peer warp's (both CTAs need to know which keys have no record).  The id is
-  // first looked at when the loads set out; in: a key before the end.
-  auto look_up = [&](int32_t& id, int32_t& offset, bool& in) {
+  }
+  __device__ __forceinline__ void step(const AttendArgs& a) {
+    if (more && ++t == t1) next_unit(a);
+  }
+  // Page id and offset at the cursor: lanes 0-7 the warp's keys, in a pair lanes
+  // 8-15 the peer warp's (both CTAs need to know which keys have no record).  The id
+  // is first looked at when the loads set out; in: a key before the end.
+  __device__ __forceinline__ void look_up(const AttendArgs& a, int32_t rank, int w, int32_t& id, int32_t& offset,
+                                          bool& in) const {
+    const int lane = threadIdx.x & 31;
     id = -1;
-    const int32_t owner = kPair ? int32_t(rank) ^ (lane >> 3) : 0;
+    const int32_t owner = kPair ? rank ^ (lane >> 3) : 0;
     const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 7);
     in = more && lane < (kPair ? 2 : 1) * kKeysPerWarp && pos < end;  // (the end lies within the table)
     if (in) {
@@ -619,21 +613,47 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
       offset = pos - int32_t(page) * a.b.page_size;
       id = int32_t(ldg_u32_now(a.b.table + int64_t(seq) * a.b.table_stride + page));
     }
-  };
-  auto address = [&](int32_t id, int32_t offset) -> uint64_t {
-    if (id < 0) return 0;
-    if (id >= a.b.n_pages) {
-      if (a.b.status) atomicOr(a.b.status, SMLA_STATUS_INDEX_OOB);
-      return 0;
-    }
-    return reinterpret_cast<uint64_t>(a.b.kv) + int64_t(id) * a.b.page_stride + int64_t(offset) * kRecordBytes;
-  };
+  }
+};
+
+__device__ __forceinline__ uint64_t record_address(const AttendArgs& a, int32_t id, int32_t offset) {
+  if (id < 0) return 0;
+  if (id >= a.b.n_pages) {
+    if (a.b.status) atomicOr(a.b.status, SMLA_STATUS_INDEX_OOB);
+    return 0;
+  }
+  return reinterpret_cast<uint64_t>(a.b.kv) + int64_t(id) * a.b.page_stride + int64_t(offset) * kRecordBytes;
+}
+
+// Whether the 8 records of lanes 0-7 lie in a row, as in pages of a multiple of 8.
+__device__ __forceinline__ bool records_in_a_row(uint64_t rec, uint64_t first) {
+  const int lane = threadIdx.x & 31;
+  return __all_sync(0xffffffffu, lane >= kKeysPerWarp || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
+}
+
+// The pair's loaders: two groups of four warps take turns at the tiles, of each of
+// which a CTA loads 32 keys.
+__device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t rank) {
+  const int lane = threadIdx.x & 31, index = (threadIdx.x >> 5) - kFirstLoader;
+  const uint32_t group = index / kLoaderWarps;  // takes the tiles g with g % 2 == group: the stage
+  const int w = index % kLoaderWarps;           // keys [8 w, 8 w + 8) of the CTA's 32
+  const uint32_t q_full = map_to(smem_u32(&ms->q_full), 0), k_full = map_to(smem_u32(ms->k_full), 0);
+  // where this lane's chunks go: row key = 8 w + j of block lane / 8, swizzled
+  // column (lane & 7) ^ j
+  const uint32_t k_at = base + kOffK + (lane >> 3) * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
+  const uint32_t rope_at = base + kOffK + 8 * (kOwnKeys * 128) + w * kKeysPerWarp * 128;
+
+  // The records' addresses are looked up while the tile before is converted; their
+  // loads set out as soon as its registers are free and land while the other group
+  // works.
+  Cursor<true> c;
+  c.units.start(a, ms);
+  c.next_unit(a);
+  if (group == 1) c.step(a);
   // rec: lane j's record (0: none)
   auto issue = [&](uint64_t rec, Raw& r) {
     const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
-    const uint32_t run = __ballot_sync(
-        0xffffffffu, lane >= kKeysPerWarp || (rec != 0 && rec == first + uint64_t(lane) * kRecordBytes));
-    if (run == 0xffffffffu) {  // all in a row, as in pages of a multiple of 8 records
+    if (records_in_a_row(rec, first)) {
       const uint8_t* p = reinterpret_cast<const uint8_t*>(first);
 #pragma unroll
       for (int j = 0; j < kKeysPerWarp; ++j) load_record(p + j * kRecordBytes, j, r);
@@ -648,25 +668,23 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   Raw raw;
   int32_t id, offset = 0;
   bool in;
-  look_up(id, offset, in);
-  for (uint32_t g = group; more; g += kPair ? 2 : 1) {
-    const uint32_t stage = kPair ? group : g & 1;
-    const uint64_t rec = address(id, offset);
+  c.look_up(a, int32_t(rank), w, id, offset, in);
+  for (uint32_t g = group; c.more; g += 2) {
+    const uint64_t rec = record_address(a, id, offset);
     const uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && in);
     issue(rec, raw);
-    if (t == t0) {
+    if (c.t == c.t0) {
       // q of the unit, once the last QK of the unit before is done.  (A parity tells
-      // a phase from its neighbours only, so QK(g - 3) has to be known as past: in a
-      // pair, where that is the other group's barrier, QK(g - 2) says so; else the
-      // wait for PV(g - 3) has.)
-      if (kPair && g >= 2 && !warp_wait(ms, a, &ms->qk_done[stage], ((g - 2) >> 1) & 1)) return;
-      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[stage ^ 1], ((g - 1) >> 1) & 1)) return;
-      load_q(a, base + (kPair ? kOffQ : kOffQNarrow), rank, w, kWarps, row0, rows);
+      // a phase from its neighbours only, so QK(g - 3) has to be known as past, which
+      // is on the other group's barrier: QK(g - 2) says so.)
+      if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
+      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
+      load_q(a, base + kOffQ, rank, w, kLoaderWarps, c.row0, c.rows, 1);
       if (lane == 0) arrive_at(q_full);
     }
-    step();
-    if (kPair) step();
-    look_up(id, offset, in);
+    c.step(a);
+    c.step(a);
+    c.look_up(a, int32_t(rank), w, id, offset, in);
     // convert the landed records
     uint32_t v[kKeysPerWarp][2][4];
     uint32_t odd = 0, top = 0;
@@ -703,29 +721,119 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     }
     if (g >= 2) {
       const uint32_t parity = ((g - 2) >> 1) & 1;
-      if (kPair ? !warp_wait(ms, a, &ms->qk_done[stage], parity) || !warp_wait(ms, a, &ms->v_full[stage], parity)
-                : !warp_wait(ms, a, &ms->pv_done[stage], parity))
-        return;
+      if (!warp_wait(ms, a, &ms->qk_done[group], parity) || !warp_wait(ms, a, &ms->v_full[group], parity)) return;
     }
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j) {
-      const uint32_t at = k_at + stage * kStage + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
+      const uint32_t at = k_at + group * kStageK + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
       st_shared_v4(at, v[j][0][0], v[j][0][1], v[j][0][2], v[j][0][3]);
-      st_shared_v4(at + 4 * (kRowsK * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
+      st_shared_v4(at + 4 * (kOwnKeys * 128), v[j][1][0], v[j][1][1], v[j][1][2], v[j][1][3]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t key = 4 * i + (lane >> 3);
       const uint4 r = raw.rope[i];
-      st_shared_v4(rope_at + stage * kStage + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
+      st_shared_v4(rope_at + group * kStageK + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
     }
-    if (lane < (kPair ? 2 : 1)) ms->flags[g & 3][(kPair ? rank ^ lane : 0) * kLoaderWarps + w] = uint8_t(holes >> (8 * lane));
+    if (lane < 2) ms->flags[g & 3][(rank ^ lane) * kLoaderWarps + w] = uint8_t(holes >> (8 * lane));
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (kPair) mbar_arrive(&ms->k_ready[stage]);
-      arrive_at(k_full + 8 * stage);
+      mbar_arrive(&ms->k_ready[group]);
+      arrive_at(k_full + 8 * group);
     }
+  }
+}
+
+// The narrow kernel's loaders: all eight warps load the 64 keys of every tile, a
+// warp 8 of them.  Record by record: convert, store, and send the same registers
+// off for the next tile's record, so that a warp's 8 records are in flight at
+// nearly all times (42 KB an SM: what HBM needs at ~1 us latency).
+__device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms, uint32_t base, int copies) {
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
+  const uint32_t k_at = base + kOffK + (lane >> 3) * (kTileKeys * 128) + w * kKeysPerWarp * 128;
+  const uint32_t rope_at = base + kOffK + 8 * (kTileKeys * 128) + w * kKeysPerWarp * 128;
+  Cursor<false> c;  // one tile ahead of the one that is converted
+  c.units.start(a, ms);
+  c.next_unit(a);
+  if (!c.more) return;
+  Raw raw;
+  int32_t id, offset = 0;
+  bool in;
+  c.look_up(a, 0, w, id, offset, in);
+  uint64_t rec = record_address(a, id, offset);
+  uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && in);
+  raw = load_scattered(rec);
+  bool starts = true, any = true;
+  int32_t row0 = c.row0, rows = c.rows;
+  c.step(a);
+  c.look_up(a, 0, w, id, offset, in);
+  for (uint32_t g = 0; any; ++g) {
+    const uint32_t stage = g & 1;
+    if (starts) {
+      // q of the unit, once the last QK of the unit before is done (QK(g - 3), on the
+      // same barrier, is past: this warp has waited for PV(g - 3))
+      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[stage ^ 1], ((g - 1) >> 1) & 1)) return;
+      load_q(a, base + kOffQNarrow, 0, w, 2 * kLoaderWarps, row0, rows, copies);
+      if (lane == 0) mbar_arrive(&ms->q_full);
+    }
+    rec = record_address(a, id, offset);
+    const uint32_t next_holes = __ballot_sync(0xffffffffu, rec == 0 && in);
+    const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
+    const bool run = records_in_a_row(rec, first);
+    if (g >= 2 && !warp_wait(ms, a, &ms->pv_done[stage], ((g - 2) >> 1) & 1)) return;
+    uint32_t odd = 0, top = 0;
+#pragma unroll
+    for (int j = 0; j < kKeysPerWarp; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) odd |= odd_scale(raw.scale[j][i]), top = nan_codes(raw.lat[j][i], top);
+    const bool plain = !__any_sync(0xffffffffu, odd != 0 || (top & 0x80808080u) != 0);
+    const uint32_t k = k_at + stage * kStageNarrow;
+    uint32_t bad_keys = 0;
+#pragma unroll
+    for (int j = 0; j < kKeysPerWarp; ++j) {
+      uint32_t v[2][4];
+      if (plain) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          dequant8(raw.lat[j][i], __byte_perm(raw.scale[j][i] + (120u << 23), 0, 0x3232), v[i]);
+      } else {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const Dequant8 d = dequant8_any(raw.lat[j][i].x, raw.lat[j][i].y, raw.scale[j][i]);
+          bad |= d.bad != 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[i][q] = d.v[q];
+        }
+        if (__any_sync(0xffffffffu, bad)) bad_keys |= 1u << j;
+      }
+      const uint32_t at = k + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
+      st_shared_v4(at, v[0][0], v[0][1], v[0][2], v[0][3]);
+      st_shared_v4(at + 4 * (kTileKeys * 128), v[1][0], v[1][1], v[1][2], v[1][3]);
+      if (run) load_record(reinterpret_cast<const uint8_t*>(first) + j * kRecordBytes, j, raw);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t key = 4 * i + (lane >> 3);
+      uint4 r = raw.rope[i];
+      // (NaN in the rope of a key whose latent is not finite, as in loader_role)
+      if ((lane & 7) == 0 && ((bad_keys >> key) & 1u)) r.x = 0x7FC07FC0u;
+      st_shared_v4(rope_at + stage * kStageNarrow + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
+      if (run)
+        raw.rope[i] = ldg_v4_now(reinterpret_cast<const uint8_t*>(first) + key * kRecordBytes + kRopeOffset + (lane & 7) * 16);
+    }
+    if (!run && c.more) raw = load_scattered(rec);
+    if (lane == 0) ms->flags[g & 3][w] = uint8_t(holes);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ms->k_full[stage]);
+    holes = next_holes;
+    any = c.more;
+    starts = c.t == c.t0;
+    row0 = c.row0, rows = c.rows;
+    c.step(a);
+    c.look_up(a, 0, w, id, offset, in);
   }
 }
 
@@ -1035,6 +1143,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1;
   const int warp = threadIdx.x >> 5;
+  let_dependents_launch();
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->k_ready[i], kLoaderWarps);
@@ -1069,7 +1178,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   if (warp < kFirstLoader) {
     softmax_role(a, ms, base, tmem, rank, pair);
   } else if (warp < kIssuerQk) {
-    loader_role<true>(a, ms, base, rank);
+    loader_role(a, ms, base, rank);
   } else if (warp == kCopier) {
     if ((threadIdx.x & 31) == 0) copier_role(a, ms, base, rank);
   } else if (rank == 0) {
@@ -1102,19 +1211,22 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // Up to kN = 16, 32 or 64 rows a tile (single tokens, a few drafted ones): no
 // pair, since half of its rows or more would be empty, and each CTA loads all 64
 // keys of a tile once for both products.
-//   S[64, 64] = Q K^T as above (M = 64: rows 16 w .. sit in lanes 32 w .. of TMEM);
+//   S[64, 64] = Q K^T as above (M = 64: rows 16 w .. sit in lanes 32 w .. of TMEM).
+// With kN < 64 the 64 rows hold 64 / kN copies of Q, so that every softmax warp
+// finds its rows in its own lanes and takes kN of the 64 keys.
 //   O^T[128 b .. + 128, kN] += V^T P^T, b = 0 .. 3: the four M = 128 blocks of
 // dims take 4 kN columns, and V^T is the K tile read MN-major, so nothing is copied.
-// A row's scores are one thread's; the factors of O's columns go through shared
-// memory.
+// Warps (16): 0-3 softmax, 4-11 loaders, 12-13 half of QK's K-steps each, 14-15
+// two blocks of PV each.
 
-// kRows: whether this warp has rows (with kN < 64 some only rescale and store O).
-template <int kN, bool kRows>
+template <int kN>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                     int32_t worker) {
+  constexpr int kCopies = kCtaRows / kN, kKeys = kN;  // a thread's keys of a tile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t m = 16 * warp + lane;  // this thread's row (lanes 0-15)
-  const bool mine = kRows && lane < 16;
+  const int32_t m = (16 * warp + (lane & 15)) % kN;   // this thread's row
+  const int slice = 16 * warp / kN;                   // and keys [kKeys slice, + kKeys)
+  const bool mine = lane < 16;
   const int32_t tok = m / a.heads, head = m - tok * a.heads;
   const uint32_t lane_base = tmem + (uint32_t(warp) << 21);
   const uint32_t p_row = base + kOffPNarrow + m * 128;
@@ -1133,59 +1245,66 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       const uint32_t stage = g & 1;
       wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
-      float x[kTileKeys];
-      if constexpr (kRows) {
+      float x[kKeys];
+      const uint32_t s_at = lane_base + kTmemS + 128 * stage + kKeys * slice;
 #pragma unroll
-        for (int c = 0; c < kTileKeys; c += 16)
-          tmem_ld16(lane_base + kTmemS + 64 * stage + c, *reinterpret_cast<uint32_t(*)[16]>(x + c));
+      for (int c = 0; c < kKeys; c += 16) {
+        uint32_t s0[16], s1[16];
+        tmem_ld16(s_at + c, s0);
+        tmem_ld16(s_at + 64 + c, s1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) add2(s0[i], s0[i + 1], s1[i], s1[i + 1], x[c + i], x[c + i + 1]);
       }
-      const uint2 flags = *reinterpret_cast<const uint2*>(&ms->flags[g & 3][0]);
-      tmem_wait_ld();
+      const uint64_t flags = *reinterpret_cast<const uint64_t*>(&ms->flags[g & 3][0]) >> (kKeys * slice);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms->s_empty[stage]);
-      bool move = false;
-      float use = 0.f;
-      if constexpr (kRows) {
-        if (a.scale_log2 <= 0.f) {
-          const float by = a.scale_log2 < 0.f ? -1.f : 0.f;
+      if (a.scale_log2 <= 0.f) {
+        const float by = a.scale_log2 < 0.f ? -1.f : 0.f;
 #pragma unroll
-          for (int c = 0; c < kTileKeys; ++c) x[c] *= by;
-        }
-        const int32_t n = see - t * kTileKeys;
-        if (__any_sync(0xffffffffu, n < kTileKeys) || (flags.x | flags.y)) {
-          const uint32_t lo = ~flags.x & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
-          const uint32_t hi = ~flags.y & (n >= 64 ? 0xffffffffu : n <= 32 ? 0u : (1u << (n - 32)) - 1u);
-#pragma unroll
-          for (int c = 0; c < kTileKeys; ++c) x[c] = ((c < 32 ? lo : hi) >> (c & 31)) & 1u ? x[c] : -INFINITY;
-        }
-        float tm = x[0];
-#pragma unroll
-        for (int c = 1; c < kTileKeys; ++c) tm = fmaxf(tm, x[c]);
-        tm *= scale;
-        move = live && tm > ref + kMoveMargin;
-        const float nref = move ? tm : ref;
-        use = nref == -INFINITY ? 0.f : nref;
-        const float alpha = move ? ex2(ref - use) : 1.f;
-        ref = nref;
-        l *= alpha;
-        if (mine) ms->alpha[stage][m] = alpha;
+        for (int c = 0; c < kKeys; ++c) x[c] *= by;
       }
-      const bool moved = named_barrier_or(1, 128, move);
-      uint32_t p[kTileKeys / 2];
-      if constexpr (kRows) {
-        float s0 = 0.f, s1 = 0.f;
+      const int32_t n = see - t * kTileKeys - kKeys * slice;
+      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0) {
+        const uint64_t seen = ~flags & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull);
 #pragma unroll
-        for (int c = 0; c < kTileKeys / 2; ++c) {
-          float y0, y1;
-          fma2(x[2 * c], x[2 * c + 1], scale, -use, y0, y1);
-          y0 = ex2(y0);
-          y1 = ex2(y1);
-          add2(s0, s1, y0, y1, s0, s1);
-          p[c] = pack_bf16x2(y0, y1);
-        }
-        l += s0 + s1;
+        for (int c = 0; c < kKeys; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
       }
+      float tm = x[0];
+#pragma unroll
+      for (int c = 1; c < kKeys; ++c) tm = fmaxf(tm, x[c]);
+      if (kCopies > 1) {
+        ms->tmax[stage][warp * 32 + lane] = tm;
+        named_barrier(1, 128);
+#pragma unroll
+        for (int k = 1; k < kCopies; ++k) tm = fmaxf(tm, ms->tmax[stage][(warp ^ (k * (kN / 16))) * 32 + lane]);
+      }
+      tm *= scale;
+      const bool move = live && tm > ref + kMoveMargin;
+      const float nref = move ? tm : ref;
+      const float use = nref == -INFINITY ? 0.f : nref;
+      const float alpha = move ? ex2(ref - use) : 1.f;
+      ref = nref;
+      bool moved;
+      if (kN == 16) {
+        moved = __any_sync(0xffffffffu, move);
+      } else {
+        if (mine && slice == 0) ms->alpha[stage][m] = alpha;
+        moved = named_barrier_or(1, 128, move);
+      }
+      uint32_t p[kKeys / 2];
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < kKeys / 2; ++c) {
+        float y0, y1;
+        fma2(x[2 * c], x[2 * c + 1], scale, -use, y0, y1);
+        y0 = ex2(y0);
+        y1 = ex2(y1);
+        add2(sum0, sum1, y0, y1, sum0, sum1);
+        p[c] = pack_bf16x2(y0, y1);
+      }
+      l = l * alpha + (sum0 + sum1);
       if (g > 0) wait_for(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
       if (t > t0 && moved) {
         tc_fence_after();
@@ -1195,16 +1314,19 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
           tmem_ld16(lane_base + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            o[i] = __float_as_uint(__uint_as_float(o[i]) * ms->alpha[stage][(c & (kN - 1)) + i]);
+          for (int i = 0; i < 16; ++i) {
+            const float f = kN == 16 ? __shfl_sync(0xffffffffu, alpha, i) : ms->alpha[stage][(c & (kN - 1)) + i];
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+          }
           tmem_st16(lane_base + c, o);
         }
         tmem_wait_st();
       }
       if (mine) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          st_shared_v4(p_row + ((c ^ (m & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+        for (int c = 0; c < kKeys / 8; ++c)
+          st_shared_v4(p_row + (((slice * (kKeys / 8) + c) ^ (m & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2],
+                       p[4 * c + 3]);
       }
       fence_proxy_async_smem();
       tc_fence_before();
@@ -1213,7 +1335,14 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
     }
     const bool whole = t0 == 0 && t1 == u.tiles;
     const int64_t part = 2 * int64_t(worker) + (t0 > 0 ? 0 : 1);
-    if (mine) {
+    if (kCopies > 1) {
+      ms->lsum[warp * 32 + lane] = l;
+      named_barrier(1, 128);
+      l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kCopies; ++k) l += ms->lsum[(warp ^ (k * (kN / 16))) * 32 + lane];
+    }
+    if (mine && slice == 0) {
       float factor = 1.f;
       if (whole) {
         float lse;
@@ -1244,8 +1373,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
           const float f = ms->factor[c + i];
           uint16_t* dst = a.out + (int64_t(u.row0) + r_tok) * a.o_row + int64_t(r_head) * a.o_head + dim;
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            dst[128 * b] = uint16_t(pack_bf16x2(__uint_as_float(o[b][i]) * f, 0.f));
+          for (int b = 0; b < 4; ++b) dst[128 * b] = uint16_t(pack_bf16x2(__uint_as_float(o[b][i]) * f, 0.f));
         } else {
           float* dst = a.o_part + (part * a.part_rows + c + i) * kLatent + dim;
 #pragma unroll
@@ -1259,12 +1387,70 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   }
 }
 
+// One thread each: K-steps which, which + 2, ... of every QK into an accumulator
+// of its own.
+__device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
+                                               uint32_t which) {
+  const uint64_t q0 = smem_desc(base + kOffQNarrow, 16, 1024, kSw128) + which * 2;
+  const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128) + which * 2;
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0, n_units = 0;
+  while (units.next(a, u)) {
+    const int32_t t0 = u.t0, t1 = u.t1;
+    if (!wait_for(ms, a, &ms->q_full, n_units++ & 1)) return;
+    for (int32_t t = t0; t < t1; ++t, ++g) {
+      const uint32_t stage = g & 1;
+      if (!wait_for(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
+      if (g >= 2 && !wait_for(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
+      tc_fence_after();
+      const uint64_t kd = k0 + uint64_t((stage * kStageNarrow) >> 4);
+#pragma unroll
+      for (int k = 0; k < kQK / 16; k += 2)
+        mma_f16_ss(tmem + kTmemS + 128 * stage + 64 * which, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
+                   kd + uint64_t(((k >> 2) * (kTileKeys * 128) + (k & 3) * 32) >> 4),
+                   idesc_bf16(kCtaRows, kTileKeys, 0, 0), k > 0);
+      mma_commit(&ms->qk_done[stage]);
+    }
+  }
+}
+
+// One thread each: blocks 2 which and 2 which + 1 of every O^T += V^T P^T.
+template <int kN>
+__device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
+                                               uint32_t which) {
+  const uint64_t v0 = smem_desc(base + kOffK + which * 4 * (kTileKeys * 128), kTileKeys * 128, 1024, kSw128);
+  const uint64_t p0 = smem_desc(base + kOffPNarrow, 16, 1024, kSw128);
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0;
+  while (units.next(a, u)) {
+    const int32_t t0 = u.t0, t1 = u.t1;
+    for (int32_t t = t0; t < t1; ++t, ++g) {
+      const uint32_t stage = g & 1;
+      if (!wait_for(ms, a, &ms->p_full, g & 1)) return;
+      tc_fence_after();
+      const uint64_t vd = v0 + uint64_t((stage * kStageNarrow) >> 4);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 16; ++k)
+          mma_f16_ss(tmem + (2 * which + b) * kN, vd + uint64_t((b * 2 * (kTileKeys * 128) + k * 2048) >> 4),
+                     p0 + uint64_t(k * 2), idesc_bf16(128, kN, 1, 0), (t == t0 && k == 0) ? 0u : 1u);
+      mma_commit(&ms->pv_done[stage]);
+    }
+  }
+}
+
 template <int kN>
 __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   const uint32_t base = smem_u32(raw_smem);
   const int32_t worker = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  let_dependents_launch();
   if (threadIdx.x == 0) a.merge[worker * 4] = 0;
   if (base & 1023u) {
     if (threadIdx.x == 0 && a.b.status) atomicOr(a.b.status, SMLA_STATUS_SMEM_LAYOUT);
@@ -1275,12 +1461,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->k_full[i], 2 * kLoaderWarps);
       mbar_init(&ms->s_empty[i], 4);
-      mbar_init(&ms->qk_done[i], 1);
-      mbar_init(&ms->pv_done[i], 1);
+      mbar_init(&ms->qk_done[i], 2);
+      mbar_init(&ms->pv_done[i], 2);
     }
     mbar_init(&ms->q_full, 2 * kLoaderWarps);
     mbar_init(&ms->p_full, 4);
-    mbar_init(&ms->drain, 2);
+    mbar_init(&ms->drain, 4);
     mbar_init(&ms->never, 1);
     fence_mbar_init();
     ms->dead = 0;
@@ -1296,63 +1482,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
   if (warp < kFirstLoader) {
-    if (16 * warp < kN) narrow_softmax_role<kN, true>(a, ms, base, tmem, worker);
-    else narrow_softmax_role<kN, false>(a, ms, base, tmem, worker);
+    narrow_softmax_role<kN>(a, ms, base, tmem, worker);
   } else if (warp < kNarrowQk) {
-    loader_role<false>(a, ms, base, 0);
-  } else {
-    const bool qk = warp == kNarrowQk;
-    const uint64_t q0 = smem_desc(base + kOffQNarrow, 16, 1024, kSw128);
-    const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128);
-    const uint64_t v0 = smem_desc(base + kOffK, kTileKeys * 128, 1024, kSw128);
-    const uint64_t p0 = smem_desc(base + kOffPNarrow, 16, 1024, kSw128);
-    Units units;
-    units.start(a, ms);
-    Unit u;
-    uint32_t g = 0, n_units = 0;
-    bool ok = true;
-    while (ok && units.next(a, u)) {
-      const int32_t t0 = u.t0, t1 = u.t1;
-      if (qk) ok = warp_wait(ms, a, &ms->q_full, n_units++ & 1);
-      for (int32_t t = t0; ok && t < t1; ++t, ++g) {
-        const uint32_t stage = g & 1;
-        if (qk) {
-          ok = warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1) &&
-               (g < 2 || warp_wait(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t kd = k0 + uint64_t((stage * kStageNarrow) >> 4);
-#pragma unroll
-            for (int k = 0; k < kQK / 16; ++k)
-              mma_f16_ss(tmem + kTmemS + 64 * stage, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
-                         kd + uint64_t(((k >> 2) * (kTileKeys * 128) + (k & 3) * 32) >> 4),
-                         idesc_bf16(kCtaRows, kTileKeys, 0, 0), k > 0);
-            mma_commit(&ms->qk_done[stage]);
-          }
-        } else {
-          ok = warp_wait(ms, a, &ms->p_full, g & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint64_t vd = v0 + uint64_t((stage * kStageNarrow) >> 4);
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-              for (int k = 0; k < kTileKeys / 16; ++k)
-                mma_f16_ss(tmem + b * kN, vd + uint64_t((b * 2 * (kTileKeys * 128) + k * 2048) >> 4), p0 + uint64_t(k * 2),
-                           idesc_bf16(128, kN, 1, 0), (t == t0 && k == 0) ? 0u : 1u);
-            mma_commit(&ms->pv_done[stage]);
-          }
-        }
-        __syncwarp();
-      }
-    }
-    __syncwarp();
-    if (lane == 0) {  // every MMA complete before the memory it reads goes away
-      mma_commit(&ms->drain);
-      if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
-    }
+    narrow_loader_role(a, ms, base, kCtaRows / kN);
+  } else if (lane == 0) {
+    if (warp < kNarrowPv) narrow_qk_role(a, ms, base, tmem, uint32_t(warp - kNarrowQk));
+    else narrow_pv_role<kN>(a, ms, base, tmem, uint32_t(warp - kNarrowPv));
+    // every MMA complete before the memory it reads goes away
+    mma_commit(&ms->drain);
+    if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
   }
   __syncwarp();
   tc_fence_before();
@@ -1364,54 +1502,63 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   }
 }
 
-// Joins the partials of a row tile shared between pairs: with m = max_c m_c,
+// Joins the partials of a row tile shared between workers: with m = max_c m_c,
 //   l = sum_c l_c 2^(m_c - m),  O = sum_c O_c 2^(m_c - m),
-// and the sink enters once.  A warp per row, one block per 8 rows of a pair's
-// merge job; the parts come from L2.
-constexpr int kMergeWarps = 8;
+// and the sink enters once.  The parts (up to one a worker) come from L2, whose
+// latency is the cost: a warp takes a quarter of a row's dims, so that a merge of
+// few rows and many parts is spread over many SMs, and keeps 8 parts' loads in
+// flight.
+constexpr int kMergeRows = 2;  // rows of a block of 8 warps
 
-__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const __grid_constant__ AttendArgs a) {
+__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ AttendArgs a) {
   const int32_t last = blockIdx.x;
-  const int lane = threadIdx.x & 31;
-  const int32_t m = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
-  if (m >= a.merge[last * 4]) return;
-  const int32_t row0 = a.merge[last * 4 + 1], first = a.merge[last * 4 + 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t m = blockIdx.y * kMergeRows + (warp >> 2);
+  wait_for_primary();
+  const int4 job = *reinterpret_cast<const int4*>(a.merge + last * 4);
+  if (m >= job.x) return;
+  const int32_t first = job.z;
+  auto part_of = [&](int32_t c) -> int64_t { return (2 * int64_t(c) + (c == first ? 1 : 0)) * a.part_rows + m; };
   float mx = -INFINITY;
-  for (int32_t c = first; c <= last; ++c) {
-    const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
-    mx = fmaxf(mx, a.ml_part[(part * a.part_rows + m) * 2]);
-  }
+  for (int32_t c = first + lane; c <= last; c += 32) mx = fmaxf(mx, a.ml_part[part_of(c) * 2]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float use = mx == -INFINITY ? 0.f : mx;
-  float l = 0.f, o[16];
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int32_t at = 128 * (warp & 3) + 4 * lane;
+  constexpr int kFlight = 8;
+  for (int32_t c0 = first; c0 <= last; c0 += 32) {
+    // lane i: weight and weighted sum of part c0 + i
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (c0 + lane <= last) ml = *reinterpret_cast<const float2*>(a.ml_part + part_of(c0 + lane) * 2);
+    const float wgt = ex2(ml.x - use);
+    l += ml.y * wgt;
+    const int32_t n = min(last - c0 + 1, 32);
+    for (int32_t i = 0; i < n; i += kFlight) {
+      float4 v[kFlight];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) o[i] = 0.f;
-  for (int32_t c = first; c <= last; ++c) {
-    const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
-    const float wgt = ex2(a.ml_part[(part * a.part_rows + m) * 2] - use);
-    l += a.ml_part[(part * a.part_rows + m) * 2 + 1] * wgt;
-    const float4* src = reinterpret_cast<const float4*>(a.o_part + (part * a.part_rows + m) * kLatent) + lane;
+      for (int k = 0; k < kFlight; ++k) {
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + k < n) v[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + part_of(c0 + i + k) * kLatent + at));
+      }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = src[32 * i];
-      o[4 * i] += v.x * wgt;
-      o[4 * i + 1] += v.y * wgt;
-      o[4 * i + 2] += v.z * wgt;
-      o[4 * i + 3] += v.w * wgt;
+      for (int k = 0; k < kFlight; ++k) {
+        const float f = __shfl_sync(0xffffffffu, wgt, (i + k) & 31);
+        if (i + k < n) o.x += v[k].x * f, o.y += v[k].y * f, o.z += v[k].z * f, o.w += v[k].w * f;
+      }
     }
   }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
   const int32_t tok = m / a.heads, head = m - tok * a.heads;
-  const int64_t tok_row = int64_t(row0) + tok;
+  const int64_t tok_row = int64_t(job.y) + tok;
   float factor, lse;
   finish_head_v(mx, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
-  if (lane == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
-  uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 4 * lane;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint2 v = make_uint2(pack_bf16x2(o[4 * i] * factor, o[4 * i + 1] * factor),
-                         pack_bf16x2(o[4 * i + 2] * factor, o[4 * i + 3] * factor));
-    if (l == 0.f) v = make_uint2(0, 0);
-    *reinterpret_cast<uint2*>(dst + 128 * i) = v;
-  }
+  if (lane == 0 && (warp & 3) == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
+  uint2 v = make_uint2(pack_bf16x2(o.x * factor, o.y * factor), pack_bf16x2(o.z * factor, o.w * factor));
+  if (l == 0.f) v = make_uint2(0, 0);
+  *reinterpret_cast<uint2*>(a.out + tok_row * a.o_row + int64_t(head) * a.o_head + at) = v;
 }
 
 }  // namespace
@@ -1494,9 +1641,16 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
     err = cudaGetLastError();
   }
   if (err != cudaSuccess || plan.workers == 1) return err;
-  paged_merge_kernel<<<dim3(unsigned(plan.workers), unsigned((plan.narrow ? plan.narrow : kPairRows) / kMergeWarps)),
-                       32 * kMergeWarps, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(unsigned(plan.workers), unsigned((plan.narrow ? plan.narrow : kPairRows) / kMergeRows));
+  config.blockDim = dim3(256);
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, paged_merge_kernel, a);
 }
 
 cudaError_t paged_set_wait_limit(uint64_t ns, int stall) {
