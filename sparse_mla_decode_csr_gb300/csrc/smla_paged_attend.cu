@@ -227,6 +227,19 @@ __device__ __forceinline__ void fma2(float x0, float x1, float m, float c, float
       : "f"(x0), "f"(x1), "f"(m), "f"(c));
 }
 
+// One lane of the converged warp.  What it runs alone stays uniform to the
+// compiler (unlike a branch on the thread index), so that an MMA's descriptors are
+// made in uniform registers: a thread then issues an MMA every 33 cycles, not 83.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
 // Arrives once on `bar` of both CTAs when the MMAs issued so far are complete.
 __device__ __forceinline__ void commit2(uint64_t* bar) {
   asm volatile(
@@ -922,7 +935,7 @@ __device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, ui
       tc_fence_after();
       const uint32_t d = tmem + kTmemS + 64 * stage + 32 * which;
       const uint64_t qd = q0 + which * 2, kd = k0 + uint64_t((stage * kStageK) >> 4) + which * 2;
-      if ((threadIdx.x & 31) == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kQK / 16; k += 2)
           mma2(d, qd + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
@@ -950,7 +963,7 @@ __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, ui
       if (!warp_wait(ms, a, &ms->p_full, g & 1)) return;
       tc_fence_after();
       const uint64_t vd = v0 + uint64_t((stage * kStageV) >> 4);
-      if ((threadIdx.x & 31) == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -1188,7 +1201,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
     // memory it reads go away (also after a wait that gave up); the odd CTA
     // learns of it at the cluster barrier
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
+    if (elect_one()) {  // (the lane that issued them: the same for the same mask)
       asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                        smem_u32(&ms->drain))
                    : "memory");
@@ -1387,7 +1400,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   }
 }
 
-// One thread each: K-steps which, which + 2, ... of every QK into an accumulator
+// A warp each: K-steps which, which + 2, ... of every QK into an accumulator
 // of its own.
 __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                uint32_t which) {
@@ -1399,24 +1412,27 @@ __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, ui
   uint32_t g = 0, n_units = 0;
   while (units.next(a, u)) {
     const int32_t t0 = u.t0, t1 = u.t1;
-    if (!wait_for(ms, a, &ms->q_full, n_units++ & 1)) return;
+    if (!warp_wait(ms, a, &ms->q_full, n_units++ & 1)) return;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      if (!wait_for(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
-      if (g >= 2 && !wait_for(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
+      if (!warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
+      if (g >= 2 && !warp_wait(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
       tc_fence_after();
       const uint64_t kd = k0 + uint64_t((stage * kStageNarrow) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int k = 0; k < kQK / 16; k += 2)
-        mma_f16_ss(tmem + kTmemS + 128 * stage + 64 * which, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
+        for (int k = 0; k < kQK / 16; k += 2)
+          mma_f16_ss(tmem + kTmemS + 128 * stage + 64 * which, q0 + uint64_t(((k >> 2) * kQBlock + (k & 3) * 32) >> 4),
                    kd + uint64_t(((k >> 2) * (kTileKeys * 128) + (k & 3) * 32) >> 4),
                    idesc_bf16(kCtaRows, kTileKeys, 0, 0), k > 0);
-      mma_commit(&ms->qk_done[stage]);
+        mma_commit(&ms->qk_done[stage]);
+      }
+      __syncwarp();
     }
   }
 }
 
-// One thread each: blocks 2 which and 2 which + 1 of every O^T += V^T P^T.
+// A warp each: blocks 2 which and 2 which + 1 of every O^T += V^T P^T.
 template <int kN>
 __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                uint32_t which) {
@@ -1430,16 +1446,19 @@ __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, ui
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      if (!wait_for(ms, a, &ms->p_full, g & 1)) return;
+      if (!warp_wait(ms, a, &ms->p_full, g & 1)) return;
       tc_fence_after();
       const uint64_t vd = v0 + uint64_t((stage * kStageNarrow) >> 4);
+      if (elect_one()) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          mma_f16_ss(tmem + (2 * which + b) * kN, vd + uint64_t((b * 2 * (kTileKeys * 128) + k * 2048) >> 4),
+          for (int k = 0; k < kTileKeys / 16; ++k)
+            mma_f16_ss(tmem + (2 * which + b) * kN, vd + uint64_t((b * 2 * (kTileKeys * 128) + k * 2048) >> 4),
                      p0 + uint64_t(k * 2), idesc_bf16(128, kN, 1, 0), (t == t0 && k == 0) ? 0u : 1u);
-      mma_commit(&ms->pv_done[stage]);
+        mma_commit(&ms->pv_done[stage]);
+      }
+      __syncwarp();
     }
   }
 }
@@ -1485,12 +1504,15 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
     narrow_softmax_role<kN>(a, ms, base, tmem, worker);
   } else if (warp < kNarrowQk) {
     narrow_loader_role(a, ms, base, kCtaRows / kN);
-  } else if (lane == 0) {
+  } else {
     if (warp < kNarrowPv) narrow_qk_role(a, ms, base, tmem, uint32_t(warp - kNarrowQk));
     else narrow_pv_role<kN>(a, ms, base, tmem, uint32_t(warp - kNarrowPv));
     // every MMA complete before the memory it reads goes away
-    mma_commit(&ms->drain);
-    if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
+    __syncwarp();
+    if (elect_one()) {  // (the lane that issued them: the same for the same mask)
+      mma_commit(&ms->drain);
+      if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
+    }
   }
   __syncwarp();
   tc_fence_before();
