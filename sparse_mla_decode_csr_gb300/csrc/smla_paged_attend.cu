@@ -99,7 +99,7 @@ constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(kPairRows, 256, 0, 1);
-constexpr int kMinWorkerSlots = 3;            // slots below which no further worker is used
+constexpr int kMinWorkerSlots = 1;            // slots below which no further worker is used
 
 struct AttendArgs {
   PagedArgs b;
@@ -343,6 +343,7 @@ __device__ __forceinline__ int32_t key_tiles(int32_t end) { return max((end + kT
 __device__ int64_t slots_before(const AttendArgs& a, const Seq& s, int32_t j) {
   if (j <= 0) return 0;
   if (!a.causal) return int64_t(j) * (1 + key_tiles(keys_end(a, s, 0)));
+  if (j == 1) return 1 + key_tiles(keys_end(a, s, 0));  // (single tokens: no division)
   int64_t sum = j;
   const int32_t n = min(j, s.tiles - 1);  // tiles that end at past + tokens (i + 1)
   if (j == s.tiles) sum += key_tiles(keys_end(a, s, j - 1));
@@ -383,7 +384,9 @@ struct Units {
   }
 
   // The next unit of this pair; false when there is none.
-  __device__ __noinline__ bool next(const AttendArgs& a, Unit& u) {
+  __device__ __noinline__ bool next(const AttendArgs& a, Unit& u) { return next_inline(a, u); }
+
+  __device__ __forceinline__ bool next_inline(const AttendArgs& a, Unit& u) {
     while (slot < end && seq < a.b.n_seqs) {
       if (j >= s.tiles) {
         j = 0;
@@ -605,7 +608,7 @@ struct Cursor {
 
   __device__ __forceinline__ void next_unit(const AttendArgs& a) {
     Unit u;
-    more = units.next(a, u);
+    more = kPair ? units.next(a, u) : units.next_inline(a, u);
     t = t0 = u.t0, t1 = u.t1, end = u.end, seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
   }
   __device__ __forceinline__ void step(const AttendArgs& a) {
@@ -1249,7 +1252,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   Unit u;
   uint32_t g = 0;
   if (ms->stall) wait_for(ms, a, &ms->never, 0);
-  while (units.next(a, u)) {
+  while (units.next_inline(a, u)) {
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const bool live = mine && m < rows;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
@@ -1410,7 +1413,7 @@ __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, ui
   units.start(a, ms);
   Unit u;
   uint32_t g = 0, n_units = 0;
-  while (units.next(a, u)) {
+  while (units.next_inline(a, u)) {
     const int32_t t0 = u.t0, t1 = u.t1;
     if (!warp_wait(ms, a, &ms->q_full, n_units++ & 1)) return;
     for (int32_t t = t0; t < t1; ++t, ++g) {
@@ -1442,7 +1445,7 @@ __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, ui
   units.start(a, ms);
   Unit u;
   uint32_t g = 0;
-  while (units.next(a, u)) {
+  while (units.next_inline(a, u)) {
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
