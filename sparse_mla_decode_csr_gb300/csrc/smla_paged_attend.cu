@@ -850,6 +850,9 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
     row0 = c.row0, rows = c.rows;
     c.step(a);
     c.look_up(a, 0, w, id, offset, in);
+    // the records of the tile after next set out for L2
+    if (in && lane == 0 && id >= 0 && id < a.b.n_pages && a.b.page_size % kKeysPerWarp == 0)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(record_address(a, id, offset)), kKeysPerWarp * kRecordBytes);
   }
 }
 
