@@ -555,7 +555,7 @@ __device__ __forceinline__ void load_record(const uint8_t* p, int j, Raw& r) {
 }
 
 // The loads of records anywhere (rec: lane j's, 0: none, read as zeros).
-__device__ __noinline__ Raw load_scattered(uint64_t rec) {
+__device__ __forceinline__ Raw load_scattered(uint64_t rec) {
   const int lane = threadIdx.x & 31;
   Raw r;
 #pragma unroll
@@ -573,6 +573,11 @@ __device__ __noinline__ Raw load_scattered(uint64_t rec) {
   }
   return r;
 }
+
+// The same out of line, for the pair's loaders, whose registers are all taken
+// (inline there: 248 -> 279 us at 7 chunks of 300; the call costs pages that are no
+// multiple of 8 records 313 us instead).
+__device__ __noinline__ Raw load_scattered_call(uint64_t rec) { return load_scattered(rec); }
 
 // q of a unit's rows of this CTA, zeros behind them, `copies` times over the 64
 // rows, by `warps` warps (w: which).
@@ -677,7 +682,7 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
       for (int i = 0; i < 2; ++i)
         r.rope[i] = ldg_v4_now(p + (4 * i + (lane >> 3)) * kRecordBytes + kRopeOffset + (lane & 7) * 16);
     } else {
-      r = load_scattered(rec);
+      r = load_scattered_call(rec);
     }
   };
 
