@@ -420,6 +420,8 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
   for (int32_t s = s0; s < s1; ++s) {
     const Seq q = seq_at(a, s);
     sum += slots_before(a, q, q.tiles);
+    if (worker == 0 && q.rows > 0 && q.past > a.coverage - q.rows && a.b.status)  // positions past the table
+      atomicOr(a.b.status, SMLA_STATUS_INDEX_OOB);
   }
   int64_t inc = sum;
 #pragma unroll

@@ -290,6 +290,100 @@ def test_attend_many_sequences():
     check(c, q, out, lse, 1 / 24, sk, True)
 
 
+@pytest.mark.parametrize("heads", [5, 16, 30, 64])
+@pytest.mark.parametrize("page", [1, 20, 64])
+def test_both_kernels_on_the_same_rows(heads, page):
+    # empty sequences lower the mean number of rows, which chooses the kernel: the
+    # same rows through tiles of 16, 32 or 64 rows and through pairs of CTAs
+    base = [(3, 200), (20, 150), (1, 64), (65 // heads + 1, 333)]
+    outs = []
+    for empty in (0, 60):
+        c = Batch(base + [(0, 0)] * empty, page)
+        q, sk, out, lse, st = attend(c, heads, sink=True)
+        check(c, q, out, lse, 1 / 24, sk, True)
+        outs.append((out.float(), lse))
+    # both within 2^-8 (p) + 2^-8 (result) of the exact value, of values up to ~2
+    assert (outs[0][0] - outs[1][0]).abs().max() <= 4 * 2.0 ** -8 * 2
+    assert (outs[0][1] - outs[1][1]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("heads,rows", [(16, 1), (64, 1), (128, 2), (16, 200)])
+def test_attend_a_very_long_sequence(heads, rows):
+    # 400,000 positions over 5 distinct pages (a prefix may repeat): the exact softmax
+    # weighs every slot by how often a row sees it
+    c = Batch([(5 * 64, 5 * 64)], 64, spare_pages=0)
+    n_pages, length = 6250, 400_000
+    pick = torch.randint(0, 5, (n_pages,), generator=gen(3))
+    table = c.table[0][pick].view(1, -1).contiguous()
+    q = torch.randn(rows, heads, 576, generator=gen(1)).to(torch.bfloat16)
+    out = torch.empty(rows, heads, 512, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(rows, heads, device=DEV)
+    smla.smla_paged_attend(q.to(DEV), c.cache(), table.to(DEV), torch.tensor([0, rows], dtype=torch.int32, device=DEV),
+                           torch.tensor([length], dtype=torch.int32, device=DEV), 1 / 24, None, out, lse)
+    lat, _, rope = unpack(c.rec)
+    keys = np.concatenate([lat, rope], 1)
+    ids = table[0].numpy()
+    for r in sorted({0, rows // 2, rows - 1}):
+        seen = length - rows + r + 1
+        count = np.bincount(ids[:seen // 64], minlength=5).repeat(64).astype(np.float64)
+        if seen % 64:
+            tail = int(ids[seen // 64]) * 64
+            count[tail:tail + seen % 64] += 1
+        s = q[r].double().numpy() @ keys.T / 24
+        m = s.max(1, keepdims=True)
+        w = np.exp(s - m) * count
+        ref_lse = (m[:, 0] + np.log(w.sum(1)))
+        ref = (w / w.sum(1, keepdims=True)) @ lat
+        spread = (w / w.sum(1, keepdims=True)) @ np.abs(lat)
+        # p and the result as bf16, scores in f32 (576 terms), an f32 sum of up to
+        # 6250 tiles' sums: 6250 * 2^-24 relative at most
+        ds = 2 * 576 * U32 * (np.abs(q[r].double().numpy()) @ np.abs(keys).T).max() / 24
+        tol = (2.0 ** -8 + 2 * ds + 6250 * U32) * spread + 2.0 ** -8 * np.abs(ref)
+        assert (np.abs(out[r].double().cpu().numpy() - ref) <= tol).all()
+        assert (np.abs(lse[r].double().cpu().numpy() - ref_lse) <= ds + 6250 * U32 + 2.0 ** -18 * (1 + np.abs(ref_lse))).all()
+
+
+def test_a_nan_query_row_stays_in_its_row():
+    c = Batch([(9, 100), (1, 300)], 16)
+    q, _, want, want_lse, _ = attend(c, 16)
+    q2 = q.clone()
+    q2[4, 3, 17], q2[4, 5, 570] = float("nan"), float("inf")
+    _, _, out, lse, _ = attend(c, 16, q=q2)
+    assert torch.isnan(out[4, 3].float()).all() and torch.isnan(lse[4, 3])
+    keep = torch.ones(c.rows, 16, dtype=torch.bool)
+    keep[4, 3] = keep[4, 5] = False
+    assert torch.equal(out.cpu()[keep], want.cpu()[keep]) and torch.equal(lse.cpu()[keep], want_lse.cpu()[keep])
+
+
+def test_row_boundaries_outside_the_tensors_are_clamped():
+    c = Batch([(4, 40), (3, 30)], 16)
+    kv, (table, cu, sl) = c.cache(), c.dev()
+    cu = torch.tensor([-5, 4, 1000], dtype=torch.int32, device=DEV)  # rows 0..3, 4..6
+    q, _, want, want_lse, _ = attend(c, 16)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    smla.smla_paged_attend(q.to(DEV), kv, table, cu, sl, 1 / 24, None, out, lse)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    # boundaries that decrease name rows twice or not at all: no access leaves the tensors
+    for bad in ([0, 6, 3], [7, 0, 0], [5, 5, 2]):
+        smla.smla_paged_attend(q.to(DEV), kv, table, torch.tensor(bad, dtype=torch.int32, device=DEV), sl, 1 / 24, None,
+                               out, lse)
+        lat, rope = torch.zeros(7, 512, device=DEV), torch.zeros(7, 64, device=DEV)
+        smla.smla_paged_read(kv, table, torch.tensor(bad, dtype=torch.int32, device=DEV), sl, lat, rope)
+    torch.cuda.synchronize()
+
+
+def test_attend_without_pages_or_table():
+    q = torch.randn(2, 16, 576, generator=gen(0)).to(torch.bfloat16).to(DEV)
+    cu, sl = torch.tensor([0, 2], dtype=torch.int32, device=DEV), torch.tensor([9], dtype=torch.int32, device=DEV)
+    for kv, table in ((torch.empty(0, 16, REC, dtype=torch.uint8, device=DEV), torch.zeros(1, 3, dtype=torch.int32, device=DEV)),
+                      (torch.zeros(2, 16, REC, dtype=torch.uint8, device=DEV), torch.zeros(1, 0, dtype=torch.int32, device=DEV))):
+        out, lse = torch.full((2, 16, 512), 7.0, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 16, device=DEV)
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        smla.smla_paged_attend(q, kv, table, cu, sl, 1 / 24, None, out, lse, status=status)
+        assert (out == 0).all() and torch.isneginf(lse).all()
+        assert int(status) == smla.STATUS_INDEX_OOB
+
+
 def test_attend_sharp_softmax_moves_the_reference():
     # scores of some hundreds: the running reference moves often
     c = Batch([(6, 700), (1, 1500)], 64, std=3.0)
@@ -326,6 +420,7 @@ def test_attend_bad_pages_are_masked_and_flagged():
     c.lens = [(3, 90)]
     q, sk, out, lse, st = attend(c, 16)
     check(c, q, out, lse, 1 / 24, sk, True)
+    assert st == smla.STATUS_INDEX_OOB
 
 
 def test_attend_strided_q_and_out():
@@ -340,7 +435,8 @@ def test_attend_strided_q_and_out():
     smla.smla_paged_attend(q, c.cache(), *c.dev(), 1 / 24, None, out, None)  # without an LSE
 
 
-def test_attend_returns_every_code_exactly():
+@pytest.mark.parametrize("heads", [16, 128])
+def test_attend_returns_every_code_exactly(heads):
     # one key: out is its latent, so every E4M3 code at scales over the fast path's
     # range (subnormal codes included) comes back as bf16(e4m3 * scale)
     c = Batch([(1, 1)] * 8, 1)
@@ -350,21 +446,22 @@ def test_attend_returns_every_code_exactly():
         s = c.slot(b, 0)
         c.rec[s, :512] = np.concatenate([codes, codes[::-1]])
         c.rec[s, 512:528] = np.full(4, scales[b], np.float32).view(np.uint8)
-    q, _, out, lse, _ = attend(c, 16, q=torch.zeros(8, 16, 576, dtype=torch.bfloat16))
+    q, _, out, lse, _ = attend(c, heads, q=torch.zeros(8, heads, 576, dtype=torch.bfloat16))
     lat = unpack(c.rec)[0]
     for b in range(8):
         assert (out[b].double().cpu().numpy() == lat[c.slot(b, 0)]).all(), scales[b]
     assert (lse == 0).all()
 
 
-def test_attend_foreign_scales_round_once():
+@pytest.mark.parametrize("heads", [16, 128])
+def test_attend_foreign_scales_round_once(heads):
     c = Batch([(3, 70)], 16)
     sc = torch.exp2(torch.rand(c.n_pages * 16, 4, generator=gen(4)) * 6 - 4).float().numpy()
     sc[::3] = np.ldexp(1.0, np.random.default_rng(0).integers(-130, 9, sc[::3].shape)).astype(np.float32)
     c.rec[:, 512:528] = sc.view(np.uint8)
-    q, sk, out, lse, _ = attend(c, 16)
-    # what enters the products is bf16(f32(e4m3 * scale)): the oracle on those values,
-    # packed with scale 1 codes impossible, so the bound gets k's and v's half step
+    q, sk, out, lse, _ = attend(c, heads)
+    # what enters the products is bf16(f32(e4m3 * scale)): the bound gets the half
+    # step of k and v
     rows, ref, ref_lse, (a_out, a_lse) = reference_operands(c, q)
     err = np.abs(out.double().cpu().numpy()[rows] - ref) - (a_out + 2.0 ** -8 * np.abs(ref))
     assert err.max() <= 0
@@ -383,11 +480,12 @@ def reference_operands(c, q):
     return rows, out, lse, allowance(qq, c.rec, idx, ptr, None, 1 / 24, None, operand_rel=2.0 ** -8)
 
 
-def test_what_a_row_may_not_see_never_reaches_it():
+@pytest.mark.parametrize("empty", [0, 20])
+def test_what_a_row_may_not_see_never_reaches_it(empty):
     # the chunk's later tokens and the slots past the end hold NaN codes, infinite
     # scales and infinite rope: rows before them are as if they were not there
-    c = Batch([(10, 75)], 16)
-    clean = c.rec.copy()
+    # (empty sequences choose the kernel of few rows)
+    c = Batch([(10, 75)] + [(0, 0)] * empty, 16)
     q, _, want, want_lse, _ = attend(c, 16)
     for p, kind in ((70, 0), (71, 1), (72, 2), (73, 3)):
         s = c.slot(0, p)
@@ -404,7 +502,6 @@ def test_what_a_row_may_not_see_never_reaches_it():
     _, _, out, lse, _ = attend(c, 16, q=q)
     assert torch.equal(out[:5], want[:5]) and torch.equal(lse[:5], want_lse[:5])
     assert torch.isnan(out[5:].float()).all() and torch.isnan(lse[5:]).all()
-    c.rec = clean
 
 
 def test_attend_agrees_with_the_sparse_decode_on_the_same_cache():
@@ -530,14 +627,15 @@ def test_empty_batches_do_nothing():
                           torch.zeros(1, dtype=torch.int32, device=DEV), z)
 
 
-def test_attend_wait_timeout_sets_the_status_and_leaves_the_context_usable():
+@pytest.mark.parametrize("heads", [16, 128])
+def test_attend_wait_timeout_sets_the_status_and_leaves_the_context_usable(heads):
     c = Batch([(1, 500), (4, 900)], 64)
     try:
         smla.smla_set_wait_limit(20_000_000, stall_first_wait=True)
-        *_, st = attend(c, 16)
+        *_, st = attend(c, heads)
         assert st & smla.STATUS_TIMEOUT
     finally:
         smla.smla_set_wait_limit(0)
-    q, sk, out, lse, st = attend(c, 16)
+    q, sk, out, lse, st = attend(c, heads)
     assert st == 0
     check(c, q, out, lse, 1 / 24, sk, True)
