@@ -67,6 +67,7 @@ cudaError_t launch_pack(const void* latent, int64_t latent_stride, const void* r
 // part_rows rows, and their O.
 struct AttendPlan {
   int32_t workers, part_rows;
+  int32_t start_slots, merge_tiles;  // slots of a row tile's start; row tiles that may be shared
   int32_t narrow;  // rows of a tile of the narrow kernel (16, 32, 64); 0: the pair kernel
   int64_t merge_off, ml_off, o_off, total;
 };

@@ -14,13 +14,16 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+bool sizes_fit(const smla_paged_batch& b) {
+  return b.n_rows >= 0 && b.n_rows <= (int64_t(1) << 30) && b.n_seqs >= 0 && b.n_seqs <= (1 << 24) &&
+         b.page_size >= 1 && b.max_pages >= 0 && int64_t(b.max_pages) * b.page_size <= (int64_t(1) << 30);
+}
+
 // Checks of the batch; *empty when there is no row to work on.
 int check_batch(const smla_paged_batch* b, bool* empty) {
   *empty = false;
   if (b == nullptr) return SMLA_ERR_NULL;
-  if (b->n_rows < 0 || b->n_rows > (int64_t(1) << 30) || b->n_seqs < 0 || b->n_seqs > (1 << 24)) return SMLA_ERR_SHAPE;
-  if (b->n_pages < 0 || b->n_pages > (int64_t(1) << 31) || b->page_size < 1 || b->max_pages < 0) return SMLA_ERR_SHAPE;
-  if (int64_t(b->max_pages) * b->page_size > (int64_t(1) << 30)) return SMLA_ERR_SHAPE;
+  if (!sizes_fit(*b) || b->n_pages < 0 || b->n_pages > (int64_t(1) << 31)) return SMLA_ERR_SHAPE;
   if (b->n_rows == 0 || b->n_seqs == 0) {
     *empty = true;
     return SMLA_OK;
@@ -119,16 +122,11 @@ int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_
 }
 
 size_t smla_paged_attend_workspace_size(const smla_paged_attend_params* params) {
-  bool empty = false;
   int sms = 0;
   if (params == nullptr || params->num_heads < 1 || params->num_heads > SMLA_PAGED_MAX_HEADS) return 0;
   const smla_paged_batch& b = params->batch;
   // (the sizes alone: pointers may still be unset here)
-  if (b.n_rows < 0 || b.n_seqs < 0 || b.page_size < 1 || b.max_pages < 0 ||
-      int64_t(b.max_pages) * b.page_size > (int64_t(1) << 30))
-    return 0;
-  empty = b.n_rows == 0 || b.n_seqs == 0;
-  if (empty || device_sms(&sms) != SMLA_OK) return 0;
+  if (!sizes_fit(b) || b.n_rows == 0 || b.n_seqs == 0 || device_sms(&sms) != SMLA_OK) return 0;
   return size_t(paged_attend_plan(*params, sms).total);
 }
 

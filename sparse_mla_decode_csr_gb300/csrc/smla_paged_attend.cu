@@ -95,11 +95,11 @@ constexpr int kNarrowQk = 12;  // and 13
 constexpr int kNarrowPv = 14;  // and 15
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;              // two S buffers of two accumulators of 32 columns behind O's 256
+constexpr int kPairStart = 8, kNarrowStart = 2;
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(kPairRows, 256, 0, 1);
-constexpr int kMinWorkerSlots = 1;            // slots below which no further worker is used
 
 struct AttendArgs {
   PagedArgs b;
@@ -114,6 +114,7 @@ struct AttendArgs {
   int32_t workers;                // pairs of CTAs, or CTAs of the narrow kernel
   int32_t part_rows;              // rows of a partial: 128, or 64
   int32_t coverage;               // positions the block table can hold
+  int32_t start_slots;            // slots of a row tile's start
   float* o_part;                  // [2 workers][part_rows][512]
   float* ml_part;                 // [2 workers][part_rows][2]
   int32_t* merge;                 // [workers][4]: rows to merge (0: none), first token row, first worker
@@ -136,7 +137,6 @@ struct Misc {
   // per tile: a byte per 8 keys, bit: a key before the end that has no record
   uint8_t flags[4][kTileKeys / 8];
 };
-static_assert(sizeof(Misc) <= 3072, "shared memory");
 constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc));
 constexpr int kNarrowSmem = kOffMiscNarrow + int(sizeof(Misc));
 static_assert(kAttendSmem <= 232448 && kNarrowSmem <= 232448, "shared memory of a CTA");
@@ -290,28 +290,23 @@ __device__ __forceinline__ bool warp_wait(Misc* ms, const AttendArgs& a, uint64_
 
 // ---- the schedule ----
 
-// sum_{i < n} floor((a i + b) / m) for a, b >= 0 (the lattice-point count, by
-// the Euclidean reduction of (a, m)).
-__device__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
-  int64_t ans = 0;
-  while (n > 0) {
-    if (a >= m) {
-      ans += (n - 1) * n / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
-    }
-    const int64_t y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const int64_t t = m;
-    m = a;
-    a = t;
+// sum_{i < n} floor((g i + b) / 64) for g, b >= 0: the plain sum less the residues
+// modulo 64, which repeat every 64 / gcd(g, 64) terms as b mod gcd, + gcd, ...
+__device__ __forceinline__ int64_t tile_sum(int32_t n, int32_t g, int32_t b) {
+  const int32_t gcd = min(g & -g, kTileKeys), shift = __popc(kTileKeys / gcd - 1), period = 1 << shift;
+  int64_t residues = int64_t(n >> shift) * (period * (b & (gcd - 1)) + gcd * (period * (period - 1) / 2));
+  int32_t r = b & (kTileKeys - 1), rest = 0;
+  for (int32_t i = n & (period - 1); i > 0; --i) {
+    rest += r;
+    r = (r + g) & (kTileKeys - 1);
   }
-  return ans;
+  return (int64_t(n) * b + int64_t(n) * (n - 1) / 2 * g - residues - rest) / kTileKeys;
+}
+
+// n / d for n >= 0, d > 0; most are of 32 bits, in a fraction of the time.
+__device__ __forceinline__ int64_t div_up_to_64(int64_t n, int64_t d) {
+  if (((n | d) >> 32) == 0) return int64_t(uint32_t(n) / uint32_t(d));
+  return n / d;
 }
 
 // What a sequence needs for its row tiles.
@@ -342,20 +337,18 @@ __device__ __forceinline__ int32_t key_tiles(int32_t end) { return max((end + kT
 // Slots of the sequence's first j row tiles.
 __device__ int64_t slots_before(const AttendArgs& a, const Seq& s, int32_t j) {
   if (j <= 0) return 0;
-  if (!a.causal) return int64_t(j) * (1 + key_tiles(keys_end(a, s, 0)));
-  if (j == 1) return 1 + key_tiles(keys_end(a, s, 0));  // (single tokens: no division)
-  int64_t sum = j;
+  if (!a.causal) return int64_t(j) * (a.start_slots + key_tiles(keys_end(a, s, 0)));
+  if (j == 1) return a.start_slots + key_tiles(keys_end(a, s, 0));
+  int64_t sum = int64_t(j) * a.start_slots;
   const int32_t n = min(j, s.tiles - 1);  // tiles that end at past + tokens (i + 1)
   if (j == s.tiles) sum += key_tiles(keys_end(a, s, j - 1));
   // tiles [0, lo) have one key tile, [lo, hi) follow the line, [hi, n) end at the table's end
-  const int64_t G = a.tokens, P = s.past, C = a.coverage;
-  int64_t lo = P <= kTileKeys ? (kTileKeys - P) / G : 0;
-  lo = min(lo, int64_t(n));
-  int64_t hi = C - P > 0 ? (C - P + G - 1) / G - 1 : 0;
-  hi = max(min(hi, int64_t(n)), lo);
+  const int32_t G = a.tokens, P = s.past, C = a.coverage;
+  int32_t lo = P <= kTileKeys ? min((kTileKeys - P) / G, n) : 0, hi = n;
+  if (P > C - s.rows) hi = P < C ? max(min(int32_t((uint32_t(C - P) + uint32_t(G - 1)) / uint32_t(G)) - 1, n), lo) : lo;
   sum += lo;
-  sum += floor_sum(hi - lo, kTileKeys, G, P + G * (lo + 1) + kTileKeys - 1);
-  sum += (n - hi) * int64_t(key_tiles(a.coverage));
+  if (hi > lo) sum += tile_sum(hi - lo, G, P + G * (lo + 1) + kTileKeys - 1);
+  sum += int64_t(n - hi) * key_tiles(C);
   return sum;
 }
 
@@ -365,7 +358,7 @@ struct Unit {
   int32_t pos0;               // position of that token
   int32_t end;                // end of its visible positions
   int32_t t0, t1, tiles;      // key tiles [t0, t1) of `tiles`
-  int64_t slot;               // first slot of the row tile
+  int64_t slot;               // that of key tile 0
 };
 
 struct Units {
@@ -399,10 +392,11 @@ struct Units {
       u.pos0 = s.past + j * a.tokens;
       u.end = keys_end(a, s, j);
       u.tiles = key_tiles(u.end);
+      slot += a.start_slots;
       u.slot = slot;
-      u.t0 = int32_t(max(beg - (slot + 1), int64_t(0)));
-      u.t1 = int32_t(min(end - (slot + 1), int64_t(u.tiles)));
-      slot += 1 + u.tiles;
+      u.t0 = int32_t(max(beg - slot, int64_t(0)));
+      u.t1 = int32_t(max(min(end - slot, int64_t(u.tiles)), int64_t(0)));
+      slot += u.tiles;
       ++j;
       if (u.t0 < u.t1) return true;
     }
@@ -438,8 +432,9 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
     if (w < warp) before += v;
     total += v;
   }
-  const int64_t G = max(min(int64_t(a.workers), total / kMinWorkerSlots), int64_t(1));
-  const int64_t beg = worker < G ? worker * total / G : total, end = worker < G ? (worker + 1) * total / G : total;
+  const int64_t G = max(min(int64_t(a.workers), total), int64_t(1));
+  const int64_t beg = worker < G ? div_up_to_64(worker * total, G) : total;
+  const int64_t end = worker < G ? div_up_to_64((worker + 1) * total, G) : total;
   if (tid == 0) {
     ms->beg = beg;
     ms->end = end;
@@ -456,15 +451,28 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
       q = seq_at(a, ++s);
       n = slots_before(a, q, q.tiles);
     }
-    int32_t lo = 0, hi = q.tiles - 1;  // the last row tile that starts at or before beg
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if (slot + slots_before(a, q, mid) <= beg) lo = mid;
-      else hi = mid - 1;
-    }
     ms->first_seq = s;
-    ms->first_j = lo;
-    ms->first_slot = slot + slots_before(a, q, lo);
+    ms->first_slot = slot;
+  }
+  __syncthreads();
+  // the last row tile of that sequence that starts at or before beg: each step looks
+  // at 32 of them
+  if (warp == 0 && beg < end) {
+    const Seq q = seq_at(a, ms->first_seq);
+    const int64_t at = beg - ms->first_slot;
+    int32_t lo = 0, n = q.tiles;
+    while (n > 1) {
+      const int32_t step = (n + 31) >> 5, off = lane * step;
+      const bool in = off < n && slots_before(a, q, lo + off) <= at;
+      const int32_t last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+      lo += last * step;
+      n = min(step, n - last * step);
+    }
+    __syncwarp();
+    if (lane == 0) {
+      ms->first_j = lo;
+      ms->first_slot += slots_before(a, q, lo);
+    }
   }
 }
 
@@ -581,23 +589,30 @@ __device__ __forceinline__ Raw load_scattered(uint64_t rec) {
 // multiple of 8 records 313 us instead).
 __device__ __noinline__ Raw load_scattered_call(uint64_t rec) { return load_scattered(rec); }
 
-// q of a unit's rows of this CTA, zeros behind them, `copies` times over the 64
-// rows, by `warps` warps (w: which).
+// Starts the copies of a unit's q rows of this CTA, zeros behind them, `copies`
+// times over the 64 rows, by `warps` warps (w: which).  Eight lanes take a row, one
+// of its 16-byte chunks in each of the nine blocks, so that all nine addresses are
+// one plus constants.
 __device__ __noinline__ void load_q(const AttendArgs& a, uint32_t q_at, uint32_t rank, int w, int warps, int32_t row0,
                                     int32_t rows, int copies) {
   const int lane = threadIdx.x & 31;
-  for (int i = w; i < kCtaRows; i += warps) {
+  for (int i = 4 * w + (lane >> 3); i < kCtaRows; i += 4 * warps) {
     const int32_t m = int32_t(rank) * kCtaRows + i % (kCtaRows / copies);
-    const uint32_t dst = q_at + i * 128;
-    const int32_t tok = m / a.heads;
-    const uint16_t* src = a.q + int64_t(row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head;
+    const uint32_t dst = q_at + i * 128 + (((lane ^ i) & 7) << 4);
+    if (m < rows) {
+      const int32_t tok = m / a.heads;
+      const uint16_t* src = a.q + int64_t(row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head + (lane & 7) * 8;
 #pragma unroll
-    for (int c = lane; c < kQK / 8; c += 32) {
-      const uint32_t at = dst + (c >> 3) * kQBlock + (((c & 7) ^ (i & 7)) << 4);
-      if (m < rows) cp_async16(at, src + c * 8);
-      else st_shared_v4(at, 0, 0, 0, 0);
+      for (int b = 0; b < kQK / 64; ++b) cp_async16(dst + b * kQBlock, src + b * 64);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kQK / 64; ++b) st_shared_v4(dst + b * kQBlock, 0, 0, 0, 0);
     }
   }
+}
+
+// The end of load_q's copies: the caller may announce them after it.
+__device__ __forceinline__ void finish_q() {
   cp_async_wait_all();
   fence_proxy_async_smem();
   __syncwarp();
@@ -703,6 +718,7 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
       if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
       if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
       load_q(a, base + kOffQ, rank, w, kLoaderWarps, c.row0, c.rows, 1);
+      finish_q();
       if (lane == 0) arrive_at(q_full);
     }
     c.step(a);
@@ -798,7 +814,6 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
       // same barrier, is past: this warp has waited for PV(g - 3))
       if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[stage ^ 1], ((g - 1) >> 1) & 1)) return;
       load_q(a, base + kOffQNarrow, 0, w, 2 * kLoaderWarps, row0, rows, copies);
-      if (lane == 0) mbar_arrive(&ms->q_full);
     }
     rec = record_address(a, id, offset);
     const uint32_t next_holes = __ballot_sync(0xffffffffu, rec == 0 && in);
@@ -847,6 +862,10 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
         raw.rope[i] = ldg_v4_now(reinterpret_cast<const uint8_t*>(first) + key * kRecordBytes + kRopeOffset + (lane & 7) * 16);
     }
     if (!run && c.more) raw = load_scattered(rec);
+    if (starts) {
+      finish_q();
+      if (lane == 0) mbar_arrive(&ms->q_full);
+    }
     if (lane == 0) ms->flags[g & 3][w] = uint8_t(holes);
     fence_proxy_async_smem();
     __syncwarp();
@@ -993,9 +1012,9 @@ __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, ui
 // The last part of a row tile: the merge kernel joins the parts from the worker
 // that holds its first key tile up to this one.
 __device__ __noinline__ void name_merge(const AttendArgs& a, const Misc* ms, int32_t worker, const Unit& u) {
-  const int64_t G = max(min(int64_t(a.workers), ms->total / kMinWorkerSlots), int64_t(1));
+  const int64_t G = max(min(int64_t(a.workers), ms->total), int64_t(1));
   a.merge[worker * 4 + 1] = u.row0;
-  a.merge[worker * 4 + 2] = int32_t(((u.slot + 2) * G - 1) / ms->total);
+  a.merge[worker * 4 + 2] = int32_t(((u.slot + 1) * G - 1) / ms->total);
   a.merge[worker * 4] = u.tokens * a.heads;
 }
 
@@ -1126,7 +1145,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       if (live && half == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
     }
     uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 256 * half;
-    float* pdst = a.o_part + (part * a.part_rows + m) * kLatent + 256 * half;
+    float* pdst = a.o_part + (part * kLatent + 256 * half) * kPairRows + m * 4;  // (see paged_merge_pair_kernel)
 #pragma unroll 1
     for (int c = 0; c < 256; c += 16) {
       uint32_t o[16];
@@ -1144,7 +1163,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       } else {
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<uint4*>(pdst + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          *reinterpret_cast<uint4*>(pdst + (c + i) * kPairRows) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
       }
     }
     tc_fence_before();
@@ -1537,19 +1556,52 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   }
 }
 
+// The worker whose job a block of a merge kernel takes: blockIdx.x, or in grids of as
+// many blocks as there may be jobs (kSearch) the blockIdx.x-th that named one.
+template <bool kSearch>
+__device__ __forceinline__ int32_t merge_job(const AttendArgs& a) {
+  if (!kSearch) return blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  int32_t last = -1;
+  for (int32_t base = 0, seen = 0; base < a.workers && last < 0; base += 256) {
+    int32_t named[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int32_t w = base + 32 * i + lane;
+      named[i] = w < a.workers ? a.merge[4 * w] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t mask = __ballot_sync(0xffffffffu, named[i] > 0);
+      const int32_t nth = int32_t(blockIdx.x) - seen;
+      if (nth >= 0 && nth < __popc(mask)) last = base + 32 * i + int32_t(__fns(mask, 0, nth + 1));
+      seen += __popc(mask);
+    }
+  }
+  return last;
+}
+
 // Joins the partials of a row tile shared between workers: with m = max_c m_c,
 //   l = sum_c l_c 2^(m_c - m),  O = sum_c O_c 2^(m_c - m),
 // and the sink enters once.  The parts (up to one a worker) come from L2, whose
 // latency is the cost: a warp takes a quarter of a row's dims, so that a merge of
 // few rows and many parts is spread over many SMs, and keeps 8 parts' loads in
 // flight.
-constexpr int kMergeRows = 2;  // rows of a block of 8 warps
-
-__global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ AttendArgs a) {
-  const int32_t last = blockIdx.x;
+//
+// kGroups > 1, for row tiles of many parts: that many warps share a quarter's parts
+// and meet in shared memory.
+template <int kGroups>
+__global__ void __launch_bounds__(kGroups == 1 ? 256 : 128 * kGroups) paged_merge_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kRows = kGroups == 1 ? 2 : 1;  // of a block
+  constexpr int kFlight = 8;
+  __shared__ float4 o_sum[kGroups][128];
+  __shared__ float l_sum[kGroups];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t m = blockIdx.y * kMergeRows + (warp >> 2);
+  const int quarter = warp & 3, group = kGroups == 1 ? 0 : warp >> 2;
+  const int32_t m = blockIdx.y * kRows + (kGroups == 1 ? warp >> 2 : 0);
   wait_for_primary();
+  const int32_t last = merge_job<(kGroups > 1)>(a);
+  if (last < 0) return;
   const int4 job = *reinterpret_cast<const int4*>(a.merge + last * 4);
   if (m >= job.x) return;
   const int32_t first = job.z;
@@ -1561,21 +1613,21 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   const float use = mx == -INFINITY ? 0.f : mx;
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int32_t at = 128 * (warp & 3) + 4 * lane;
-  constexpr int kFlight = 8;
-  for (int32_t c0 = first; c0 <= last; c0 += 32) {
-    // lane i: weight and weighted sum of part c0 + i
+  const int32_t at = 128 * quarter + 4 * lane;
+  for (int32_t c0 = first + group; c0 <= last; c0 += 32 * kGroups) {
+    // lane i: weight and weighted sum of part c0 + kGroups i
     float2 ml = make_float2(-INFINITY, 0.f);
-    if (c0 + lane <= last) ml = *reinterpret_cast<const float2*>(a.ml_part + part_of(c0 + lane) * 2);
+    if (c0 + kGroups * lane <= last) ml = *reinterpret_cast<const float2*>(a.ml_part + part_of(c0 + kGroups * lane) * 2);
     const float wgt = ex2(ml.x - use);
     l += ml.y * wgt;
-    const int32_t n = min(last - c0 + 1, 32);
+    const int32_t n = min((last - c0) / kGroups + 1, 32);
     for (int32_t i = 0; i < n; i += kFlight) {
       float4 v[kFlight];
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i + k < n) v[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + part_of(c0 + i + k) * kLatent + at));
+        if (i + k < n)
+          v[k] = __ldcg(reinterpret_cast<const float4*>(a.o_part + part_of(c0 + kGroups * (i + k)) * kLatent + at));
       }
 #pragma unroll
       for (int k = 0; k < kFlight; ++k) {
@@ -1586,14 +1638,115 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+  if constexpr (kGroups > 1) {
+    o_sum[group][32 * quarter + lane] = o;
+    if (quarter == 0 && lane == 0) l_sum[group] = l;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 v = o_sum[g][32 * quarter + lane];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+      l += l_sum[g];
+    }
+  }
   const int32_t tok = m / a.heads, head = m - tok * a.heads;
   const int64_t tok_row = int64_t(job.y) + tok;
   float factor, lse;
   finish_head_v(mx, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
-  if (lane == 0 && (warp & 3) == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
+  if (lane == 0 && quarter == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
   uint2 v = make_uint2(pack_bf16x2(o.x * factor, o.y * factor), pack_bf16x2(o.z * factor, o.w * factor));
   if (l == 0.f) v = make_uint2(0, 0);
   *reinterpret_cast<uint2*>(a.out + tok_row * a.o_row + int64_t(head) * a.o_head + at) = v;
+}
+
+// The same for the pair kernel's partials, which lie as its threads (one a row) write
+// them: O of a part as [512 / 4][128 rows][4].  A lane takes a row, a warp 16 dims of
+// 32 rows.  One pass: the sums are rescaled when the maximum moves.
+template <int kGroups>
+__global__ void __launch_bounds__(kGroups == 1 ? 256 : 128 * kGroups)
+paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
+  constexpr int kDimWarps = kGroups == 1 ? 8 : 4, kDims = 16, kSplit = kLatent / (kDims * kDimWarps);
+  constexpr int kFlight = 4;
+  __shared__ float4 o_sum[kGroups == 1 ? 1 : kGroups][kDims / 4][kDimWarps * 32];
+  __shared__ float2 ml_sum[kGroups][kDimWarps * 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int dim_warp = warp % kDimWarps, group = warp / kDimWarps;
+  const int32_t m0 = blockIdx.y / kSplit * 32, m = m0 + lane;
+  const int32_t at = kDims * (blockIdx.y % kSplit * kDimWarps + dim_warp);
+  wait_for_primary();
+  const int32_t last = merge_job<(kGroups > 1)>(a);
+  if (last < 0) return;
+  const int4 job = *reinterpret_cast<const int4*>(a.merge + last * 4);
+  if (m0 >= job.x) return;
+  const bool live = m < job.x;
+  const int32_t first = job.z;
+  float mx = -INFINITY, l = 0.f;
+  float4 o[kDims / 4];
+#pragma unroll
+  for (int i = 0; i < kDims / 4; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  // joins one more sum with its own maximum
+  auto add = [&](const float2& ml, const float4 (&v)[kDims / 4]) {
+    const float nm = fmaxf(mx, ml.x), use = nm == -INFINITY ? 0.f : nm;
+    const float f = ex2(mx - use), w = ex2(ml.x - use);
+    mx = nm;
+    l = l * f + ml.y * w;
+#pragma unroll
+    for (int i = 0; i < kDims / 4; ++i) {
+      o[i].x = o[i].x * f + v[i].x * w, o[i].y = o[i].y * f + v[i].y * w;
+      o[i].z = o[i].z * f + v[i].z * w, o[i].w = o[i].w * f + v[i].w * w;
+    }
+  };
+  for (int32_t c0 = first + group; c0 <= last; c0 += kGroups * kFlight) {
+    float2 ml[kFlight];
+    float4 v[kFlight][kDims / 4];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int32_t c = c0 + kGroups * k;
+      ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < kDims / 4; ++i) v[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c > last || !live) continue;  // (rows behind the last hold nothing)
+      const int64_t part = 2 * int64_t(c) + (c == first ? 1 : 0);
+      ml[k] = *reinterpret_cast<const float2*>(a.ml_part + (part * kPairRows + m) * 2);
+#pragma unroll
+      for (int i = 0; i < kDims / 4; ++i)
+        v[k][i] = __ldcg(reinterpret_cast<const float4*>(a.o_part + (part * kLatent + at + 4 * i) * kPairRows + m * 4));
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (c0 + kGroups * k <= last) add(ml[k], v[k]);
+  }
+  if constexpr (kGroups > 1) {
+    const int at_sum = dim_warp * 32 + lane;
+    ml_sum[group][at_sum] = make_float2(mx, l);
+#pragma unroll
+    for (int i = 0; i < kDims / 4; ++i) o_sum[group][i][at_sum] = o[i];
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      float4 v[kDims / 4];
+#pragma unroll
+      for (int i = 0; i < kDims / 4; ++i) v[i] = o_sum[g][i][at_sum];
+      add(ml_sum[g][at_sum], v);
+    }
+  }
+  if (!live) return;
+  const int32_t tok = m / a.heads, head = m - tok * a.heads;
+  const int64_t tok_row = int64_t(job.y) + tok;
+  float factor, lse;
+  finish_head_v(mx, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+  if (at == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
+  uint32_t v[kDims / 2];
+#pragma unroll
+  for (int i = 0; i < kDims / 4; ++i) {
+    v[2 * i] = l == 0.f ? 0u : pack_bf16x2(o[i].x * factor, o[i].y * factor);
+    v[2 * i + 1] = l == 0.f ? 0u : pack_bf16x2(o[i].z * factor, o[i].w * factor);
+  }
+  uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + at;
+  *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<uint4*>(dst + 8) = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
 }  // namespace
@@ -1619,10 +1772,12 @@ AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
   const int64_t coverage = int64_t(b.max_pages) * b.page_size;
   const int64_t most_tiles = coverage > 0 ? (coverage + kTileKeys - 1) / kTileKeys : 1;
   const int64_t row_tiles = (b.n_rows + tokens - 1) / tokens + (b.n_rows < b.n_seqs ? b.n_rows : int64_t(b.n_seqs));
-  const int64_t slots = row_tiles * (most_tiles + 1);
+  plan.start_slots = plan.narrow ? kNarrowStart : kPairStart;
+  const int64_t slots = row_tiles * (most_tiles + plan.start_slots);
   int64_t workers = plan.narrow ? num_sms : num_sms / 2;
-  if (slots / kMinWorkerSlots < workers) workers = slots / kMinWorkerSlots;
+  if (slots < workers) workers = slots;
   plan.workers = int32_t(workers < 1 ? 1 : workers);
+  plan.merge_tiles = int32_t(row_tiles < plan.workers ? row_tiles : plan.workers);
   plan.merge_off = 0;
   plan.ml_off = (int64_t(plan.workers) * 16 + 255) & ~int64_t(255);
   plan.o_off = plan.ml_off + ((int64_t(plan.workers) * 2 * plan.part_rows * 8 + 255) & ~int64_t(255));
@@ -1637,6 +1792,20 @@ static cudaError_t launch_narrow(const AttendArgs& a, cudaStream_t stream) {
   if (err != cudaSuccess) return err;
   paged_attend_narrow_kernel<kN><<<a.workers, kNarrowThreads, kNarrowSmem, stream>>>(a);
   return cudaGetLastError();
+}
+
+static cudaError_t launch_merge(void (*kernel)(AttendArgs), const AttendArgs& a, dim3 grid, int threads,
+                                cudaStream_t stream) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(unsigned(threads));
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, a);
 }
 
 cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendPlan& plan, void* workspace,
@@ -1657,6 +1826,7 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
   a.causal = p.causal != 0;
   a.workers = plan.workers;
   a.part_rows = plan.part_rows;
+  a.start_slots = plan.start_slots;
   a.coverage = p.batch.max_pages * p.batch.page_size;
   char* ws = static_cast<char*>(workspace);
   a.merge = reinterpret_cast<int32_t*>(ws + plan.merge_off);
@@ -1676,16 +1846,15 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
     err = cudaGetLastError();
   }
   if (err != cudaSuccess || plan.workers == 1) return err;
-  cudaLaunchConfig_t config{};
-  config.gridDim = dim3(unsigned(plan.workers), unsigned((plan.narrow ? plan.narrow : kPairRows) / kMergeRows));
-  config.blockDim = dim3(256);
-  config.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = attr;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, paged_merge_kernel, a);
+  // Row tiles of many parts (8 or more on average) get four warps to a row's quarter
+  const bool many = plan.workers >= 8 * plan.merge_tiles;
+  const unsigned jobs = unsigned(many ? plan.merge_tiles : plan.workers);
+  if (plan.narrow) {
+    if (many) return launch_merge(paged_merge_kernel<4>, a, dim3(jobs, unsigned(plan.narrow)), 512, stream);
+    return launch_merge(paged_merge_kernel<1>, a, dim3(jobs, unsigned(plan.narrow) / 2), 256, stream);
+  }
+  if (many) return launch_merge(paged_merge_pair_kernel<4>, a, dim3(jobs, 32), 512, stream);
+  return launch_merge(paged_merge_pair_kernel<1>, a, dim3(jobs, 16), 256, stream);
 }
 
 cudaError_t paged_set_wait_limit(uint64_t ns, int stall) {

@@ -3,14 +3,19 @@
 // Writer, per block of 128 latent values: scale = pow2ceil(max(amax, 1e-4) / 448),
 // code = E4M3(x / scale); 1 / scale is a power of two, so the quotient is exact
 // and each value is rounded once.  Reader: value = e4m3 * scale in f32, rounded
-// once to the output's type.  Both are bound by HBM at large sizes and by the
-// chain row -> sequence -> page -> record at small ones.
+// once to the output's type.
 //
-// A warp takes kRows consecutive token rows.  Lane l handles the 16-byte chunks
-// l, l + 32, ... of a row of the token tensor (8 values of a 16-bit type, 4 of
-// f32), so every access of a warp covers a contiguous range on both sides; a
-// scale block is 16 or all 32 lanes of one chunk step.  The rows' data is loaded
-// before the first of their records is located.
+// A warp takes a token row (in large 16-bit reads two).  Lane l handles the
+// 16-byte chunks l, l + 32, ... of a row of the token tensor (8 values of a 16-bit
+// type, 4 of f32), so every access of a warp covers a contiguous range on both
+// sides; a scale block is 16 or all 32 lanes of one chunk step.  The writer loads
+// its row before it looks for the record.
+//
+// What bounds them: at few rows the chain row -> sequence -> page -> record
+// (2.0 us for one row, 2.3 us for 64, graph replays), at many rows HBM: 131072
+// rows in pages of 64, bytes of both sides / time: write bf16 39.1 us = 6.1 TB/s,
+// write f32 58.4 us = 6.6 TB/s, read bf16 38.2 us = 6.2 TB/s, read f32 60.3 us =
+// 6.4 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -113,71 +118,62 @@ __device__ __forceinline__ uint8_t* locate(const PagedArgs& a, int32_t base, boo
   return record_at(a, b, seq_len_at(a, b) - (end - r));
 }
 
-template <int kRows, int kDtype>
+template <int kDtype>
 __global__ void __launch_bounds__(32 * kWarps)
 paged_write_kernel(const __grid_constant__ PagedArgs a, const uint8_t* __restrict__ latent, int64_t latent_stride,
                    const uint8_t* __restrict__ rope, int64_t rope_stride) {
   using E = Elem<kDtype>;
   const int lane = threadIdx.x & 31;
-  const int64_t base64 = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRows;
-  if (base64 >= a.n_rows) return;
-  const int32_t base = int32_t(base64);
-  uint4 lat[kRows][E::kSteps], rp[kRows];
+  const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (row >= a.n_rows) return;
+  const uint8_t* src = latent + row * latent_stride * E::kBytes + lane * 16;
+  uint4 lat[E::kSteps], rp;
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    if (base + j < a.n_rows) {
-      const uint8_t* src = latent + int64_t(base + j) * latent_stride * E::kBytes + lane * 16;
-#pragma unroll
-      for (int i = 0; i < E::kSteps; ++i) lat[j][i] = __ldcs(reinterpret_cast<const uint4*>(src + i * 512));
-      if (lane < E::kRopeLanes)
-        rp[j] = __ldcs(reinterpret_cast<const uint4*>(rope + int64_t(base + j) * rope_stride * E::kBytes + lane * 16));
-    }
-  }
+  for (int i = 0; i < E::kSteps; ++i) lat[i] = __ldcs(reinterpret_cast<const uint4*>(src + i * 512));
+  if (lane < E::kRopeLanes)
+    rp = __ldcs(reinterpret_cast<const uint4*>(rope + row * rope_stride * E::kBytes + lane * 16));
   bool has;
-  const uint64_t mine = reinterpret_cast<uint64_t>(locate<kRows>(a, base, &has));
+  const uint64_t mine = reinterpret_cast<uint64_t>(locate<1>(a, int32_t(row), &has));
+  uint8_t* rec = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, 0));
+  if (rec == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    uint8_t* rec = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, mine, j));
-    if (rec == nullptr) continue;  // (the same for the whole warp)
+  for (int i = 0; i < E::kSteps; ++i) {
+    float x[E::kPer];
+    unpack<kDtype>(lat[i], x);
+    float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < E::kSteps; ++i) {
-      float x[E::kPer];
-      unpack<kDtype>(lat[j][i], x);
-      float amax = 0.f;
+    for (int k = 0; k < E::kPer; ++k) amax = fmaxf(amax, fabsf(x[k]));
+    constexpr int kLanes = 128 / E::kPer;  // lanes of a scale block
 #pragma unroll
-      for (int k = 0; k < E::kPer; ++k) amax = fmaxf(amax, fabsf(x[k]));
-#pragma unroll
-      for (int o = 1; o < 128 / E::kPer; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float inv;
-      const float scale = block_scale(amax, &inv);
-      const uint32_t c0 = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-      const int chunk = lane + 32 * i;
-      if constexpr (E::kPer == 8) {
-        const uint32_t c1 = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
-        *reinterpret_cast<uint2*>(rec + chunk * 8) = make_uint2(c0, c1);
-      } else {
-        *reinterpret_cast<uint32_t*>(rec + chunk * 4) = c0;
-      }
-      constexpr int kLanes = 128 / E::kPer;  // lanes of a scale block
-      if ((lane & (kLanes - 1)) == 0) *reinterpret_cast<float*>(rec + kScaleOffset + 4 * (chunk / kLanes)) = scale;
+    for (int o = 1; o < kLanes; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    float inv;
+    const float scale = block_scale(amax, &inv);
+    const uint32_t c0 = e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    const int chunk = lane + 32 * i;
+    if constexpr (E::kPer == 8) {
+      const uint32_t c1 = e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv);
+      *reinterpret_cast<uint2*>(rec + chunk * 8) = make_uint2(c0, c1);
+    } else {
+      *reinterpret_cast<uint32_t*>(rec + chunk * 4) = c0;
     }
-    if (lane < E::kRopeLanes) {
-      if constexpr (kDtype == SMLA_DTYPE_BF16) {
-        *reinterpret_cast<uint4*>(rec + kRopeOffset + lane * 16) = rp[j];
-      } else {
-        float x[E::kPer];
-        unpack<kDtype>(rp[j], x);
-        uint32_t w[E::kPer / 2];
+    if ((lane & (kLanes - 1)) == 0) *reinterpret_cast<float*>(rec + kScaleOffset + 4 * (chunk / kLanes)) = scale;
+  }
+  if (lane < E::kRopeLanes) {
+    if constexpr (kDtype == SMLA_DTYPE_BF16) {
+      *reinterpret_cast<uint4*>(rec + kRopeOffset + lane * 16) = rp;
+    } else {
+      float x[E::kPer];
+      unpack<kDtype>(rp, x);
+      uint32_t w[E::kPer / 2];
 #pragma unroll
-        for (int k = 0; k < E::kPer / 2; ++k) {
-          const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
-          w[k] = *reinterpret_cast<const uint32_t*>(&v);
-        }
-        if constexpr (E::kPer == 8)
-          *reinterpret_cast<uint4*>(rec + kRopeOffset + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-        else
-          *reinterpret_cast<uint2*>(rec + kRopeOffset + lane * 8) = make_uint2(w[0], w[1]);
+      for (int k = 0; k < E::kPer / 2; ++k) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&v);
       }
+      if constexpr (E::kPer == 8)
+        *reinterpret_cast<uint4*>(rec + kRopeOffset + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      else
+        *reinterpret_cast<uint2*>(rec + kRopeOffset + lane * 8) = make_uint2(w[0], w[1]);
     }
   }
 }
@@ -257,30 +253,31 @@ paged_read_kernel(const __grid_constant__ PagedArgs a, uint8_t* __restrict__ lat
   }
 }
 
-// Rows per warp: enough warps to spread a small batch over the GPU, several
-// rows of loads in flight per warp for a large one.
-constexpr int kManyRows = 4;
-constexpr int64_t kFewRowsLimit = 152 * kWarps;
+// Rows of 16-bit reads above which a warp takes two, so that their loads fly
+// together (one row a warp / two, us: 1216 rows 2.58 / 2.72, 4864 rows 3.21 / 3.08,
+// 131072 rows 40.8 / 38.2).  Writes and f32 reads take one at every size (two:
+// bf16 write 39.1 -> 40.1 us, f32 write 58.4 -> 59.6, f32 read 60.4 -> 61.3 at
+// 131072 rows; four: 68.6 for the f32 write).
+constexpr int64_t kOneRowLimit = 2432;
 
-template <int kRows>
-unsigned grid_of(const PagedArgs& a) {
-  return unsigned((int64_t(a.n_rows) + kWarps * kRows - 1) / (kWarps * kRows));
+unsigned grid_of(const PagedArgs& a, int rows) {
+  return unsigned((int64_t(a.n_rows) + kWarps * rows - 1) / (kWarps * rows));
 }
 
 template <int kDtype>
 void write_typed(const PagedArgs& a, const uint8_t* lat, int64_t ls, const uint8_t* rope, int64_t rs, cudaStream_t st) {
-  if (a.n_rows <= kFewRowsLimit)
-    paged_write_kernel<1, kDtype><<<grid_of<1>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
-  else
-    paged_write_kernel<kManyRows, kDtype><<<grid_of<kManyRows>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+  paged_write_kernel<kDtype><<<grid_of(a, 1), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
 }
 
 template <int kDtype>
 void read_typed(const PagedArgs& a, uint8_t* lat, int64_t ls, uint8_t* rope, int64_t rs, cudaStream_t st) {
-  if (a.n_rows <= kFewRowsLimit)
-    paged_read_kernel<1, kDtype><<<grid_of<1>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
-  else
-    paged_read_kernel<kManyRows, kDtype><<<grid_of<kManyRows>(a), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+  if constexpr (kDtype != SMLA_DTYPE_F32) {
+    if (a.n_rows > kOneRowLimit) {
+      paged_read_kernel<2, kDtype><<<grid_of(a, 2), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+      return;
+    }
+  }
+  paged_read_kernel<1, kDtype><<<grid_of(a, 1), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
 }
 
 }  // namespace
