@@ -7,6 +7,10 @@
 // its keys, so (token, head) pairs are the rows of two matrix products:
 //   S[128, 64] = Q[128, 576] . K[64, 576]^T,   O[128, 512] += P[128, 64] . V[64, 512].
 //
+// Two kernels, by the mean number of rows of a sequence (narrow_rows): the pair
+// kernel described here for chunks and drafts, the narrow kernel (further down) for
+// up to 64 rows.
+//
 // Row tiles.  A row tile is floor(128 / heads) consecutive tokens of one
 // sequence with all their heads.  Its keys are the positions up to its last
 // token's, in tiles of 64.
@@ -15,33 +19,41 @@
 // of an SM, so a row tile belongs to a cluster of two CTAs and the products are
 // cta_group::2 instructions with M = 128: CTA c holds rows [64 c, 64 c + 64) of
 // Q, P, S and O (64 rows on 128 lanes: lanes 64.. hold the upper half of the
-// columns), which takes 256 columns for O and 32 per S buffer.  As B operands
-// each CTA supplies half of the N extent: its own 32 keys of the tile for QK
-// ("K": 32 x 576), and its own 256 value dims of all 64 keys for PV ("V": 64 x
-// 256, MN-major).  Every record is read and dequantised once, by the CTA that
-// owns the key, into K; bulk copies take K's latent blocks to the V of the CTA
-// that needs them, its own or its peer's (both are 128-byte-swizzled rows of 64
-// dims, so a 32-key block is one contiguous piece of 4 KB).
+// columns), which takes 256 columns for O and 64 per S buffer (the two issuers'
+// halves of the K-steps, 32 columns each).  As B operands each CTA supplies half
+// of the N extent: its own 32 keys of the tile for QK ("K": 32 x 576), and its own
+// 256 value dims of all 64 keys for PV ("V": 64 x 256, MN-major).  Every record is
+// read and dequantised once, by the CTA that owns the key, into K; bulk copies
+// take K's latent blocks to the V of the CTA that needs them, its own or its
+// peer's (both are 128-byte-swizzled rows of 64 dims, so a 32-key block is one
+// contiguous piece of 4 KB).
 //
-// Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 one thread each that
-// issues MMAs (even CTA only), 15 copier.  Per tile g (stage g & 1):
+// Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 issue MMAs (even CTA
+// only), 15 copier.  Per tile g (stage g & 1):
 //   loaders   two groups of four warps take turns at the tiles, a warp 8 of the
 //             CTA's 32 keys: records into registers, dequantised there, and as soon
 //             as QK(g - 2) and the copies out of its K are done, stored.  What a
 //             stage waits for after that is the stores alone
 //   copier    one thread: K -> V of both CTAs when PV(g - 2) is done
 //   issuers   12 and 13 the even and odd K-steps of QK into two accumulators, 14
-//             PV: a thread issues a cta_group::2 MMA at most every 48 cycles
-//             (measured), three times the time that a QK step takes
+//             PV: one thread's MMAs of N = 64 follow each other at 48 cycles or
+//             more, two threads' at half of that
 //   softmax   a row is two threads (32 keys each) that exchange their maxima;
 //             p = 2^(x - m_ref), the reference moves (and O is rescaled in TMEM)
 //             only when a score exceeds it by more than 8, so p <= 2^8
 //
-// Schedule.  A row tile takes one slot for its start and one per key tile; the
-// slots of all row tiles, in order, are split evenly over the pairs (pair c of
-// G takes [c W / G, (c + 1) W / G)).  A row tile inside one pair's range is
-// finished there; a shared one leaves f32 partials (O, m, l) that
-// paged_merge_kernel joins.
+// What bounds the pair kernel: shared memory.  A tile of 64 keys takes ~2420 cycles,
+// in which the operands' reads (1248), the loaders' and softmax warps' accesses (579)
+// and the bulk copies (512) keep its port busy for ~2340.  One chunk of 2048 tokens,
+// 64 heads, over 8192 positions: 2455 us = 1070 TFLOP/s, 56% of the measured bf16
+// peak; 7 chunks of 300 tokens, 16 heads, over up to 5000: 222 us.
+//
+// Schedule.  A row tile takes a few slots for its start (kPairStart, kNarrowStart: what
+// a unit's first tile and last store take, in key tiles) and one per key tile; the
+// slots of all row tiles, in order, are split evenly over the workers (worker c of
+// G takes [c W / G, (c + 1) W / G)).  A row tile inside one worker's range is
+// finished there; a shared one leaves f32 partials (O, m, l) that a merge kernel
+// joins.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -94,7 +106,10 @@ constexpr int kNarrowThreads = 16 * 32;
 constexpr int kNarrowQk = 12;  // and 13
 constexpr int kNarrowPv = 14;  // and 15
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemS = 256;              // two S buffers of two accumulators of 32 columns behind O's 256
+constexpr uint32_t kTmemS = 256;              // the S buffers, behind O's 256 columns
+// Slots of a row tile's start, by measurement (us): the pair kernel with 1 / 4 / 8 / 12
+// at 32 drafts of 5 tokens, 64 heads: 88 / 80 / 76 / 76; the narrow kernel with 1 / 2 / 4
+// at 4 x 64 heads: 43.7 / 42.2 / 41.3, at 64 x 16 heads over 4096: 72.9 / 73.1 / 75.2.
 constexpr int kPairStart = 8, kNarrowStart = 2;
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -229,7 +244,7 @@ __device__ __forceinline__ void fma2(float x0, float x1, float m, float c, float
 
 // One lane of the converged warp.  What it runs alone stays uniform to the
 // compiler (unlike a branch on the thread index), so that an MMA's descriptors are
-// made in uniform registers: a thread then issues an MMA every 33 cycles, not 83.
+// made in uniform registers: issuing one then takes 33 cycles, not 83.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
@@ -352,7 +367,7 @@ __device__ int64_t slots_before(const AttendArgs& a, const Seq& s, int32_t j) {
   return sum;
 }
 
-// A row tile's part that this pair works on.
+// A row tile's part that this worker works on.
 struct Unit {
   int32_t seq, row0, tokens;  // its first token row and number of tokens
   int32_t pos0;               // position of that token
@@ -376,7 +391,7 @@ struct Units {
     if (slot < end && seq < a.b.n_seqs) s = seq_at(a, seq);
   }
 
-  // The next unit of this pair; false when there is none.
+  // The next unit of this worker; false when there is none.
   __device__ __noinline__ bool next(const AttendArgs& a, Unit& u) { return next_inline(a, u); }
 
   __device__ __forceinline__ bool next_inline(const AttendArgs& a, Unit& u) {
@@ -585,8 +600,8 @@ __device__ __forceinline__ Raw load_scattered(uint64_t rec) {
 }
 
 // The same out of line, for the pair's loaders, whose registers are all taken
-// (inline there: 248 -> 279 us at 7 chunks of 300; the call costs pages that are no
-// multiple of 8 records 313 us instead).
+// (inline there: 248 -> 279 us at 7 chunks of 300; the call costs pages of one record
+// 288 us where pages of a multiple of 8 take 222).
 __device__ __noinline__ Raw load_scattered_call(uint64_t rec) { return load_scattered(rec); }
 
 // Starts the copies of a unit's q rows of this CTA, zeros behind them, `copies`
@@ -946,8 +961,7 @@ __device__ __forceinline__ void copier_role(const AttendArgs& a, Misc* ms, uint3
 }
 
 // A warp of the even CTA each: K-steps which, which + 2, ... of every QK.  (The
-// whole warp runs the loop and lane 0 issues, so that descriptors stay in uniform
-// registers.)
+// whole warp runs the loop, see elect_one.)
 __device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                uint32_t which) {
   const uint64_t q0 = smem_desc(base + kOffQ, 16, 1024, kSw128);
@@ -1263,6 +1277,12 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // dims take 4 kN columns, and V^T is the K tile read MN-major, so nothing is copied.
 // Warps (16): 0-3 softmax, 4-11 loaders, 12-13 half of QK's K-steps each, 14-15
 // two blocks of PV each.
+//
+// What bounds it: a tile's two chains, record loads and conversion (~4000 cycles) and
+// QK, softmax, PV (~3300), which alternate over the two stages that shared memory
+// holds, and for short rows the ~10 us until the first scores.  64 x 16 heads over up
+// to 4096 positions: 60 us (131 MB of records: 2.2 TB/s); 4 x 64 heads over up to 16384:
+// 36 us; one token, 16 heads, 500 positions: 14 us.
 
 template <int kN>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
@@ -1586,10 +1606,8 @@ __device__ __forceinline__ int32_t merge_job(const AttendArgs& a) {
 // and the sink enters once.  The parts (up to one a worker) come from L2, whose
 // latency is the cost: a warp takes a quarter of a row's dims, so that a merge of
 // few rows and many parts is spread over many SMs, and keeps 8 parts' loads in
-// flight.
-//
-// kGroups > 1, for row tiles of many parts: that many warps share a quarter's parts
-// and meet in shared memory.
+// flight.  With kGroups = 2, for row tiles of many parts, two warps share a quarter's
+// parts and meet in shared memory.
 template <int kGroups>
 __global__ void __launch_bounds__(kGroups == 1 ? 256 : 128 * kGroups) paged_merge_kernel(const __grid_constant__ AttendArgs a) {
   constexpr int kRows = kGroups == 1 ? 2 : 1;  // of a block
@@ -1753,7 +1771,10 @@ paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
 
 // Rows of a narrow tile (16, 32, 64), or 0 for the pair kernel: by the mean number
 // of rows (tokens x heads) of a sequence, since the lengths themselves are on the
-// device.  Any split is computed correctly by either.
+// device.  Any split is computed correctly by either.  Measured at 64 sequences of
+// 4096 positions (us): 64 rows 86 in a narrow tile of 64, 102 in the pair kernel; 96
+// rows 148 and 104; 128 rows 152 and 107; 16 rows 71, 73 and 77 in tiles of 16, 32 and
+// 64, 97 in the pair kernel.
 static int narrow_rows(const smla_paged_attend_params& p) {
   if (p.num_heads > kCtaRows) return 0;
   const int64_t mean = (p.batch.n_rows * p.num_heads + p.batch.n_seqs - 1) / p.batch.n_seqs;
@@ -1846,11 +1867,15 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
     err = cudaGetLastError();
   }
   if (err != cudaSuccess || plan.workers == 1) return err;
-  // Row tiles of many parts (8 or more on average) get four warps to a row's quarter
+  // Row tiles of 8 parts or more on average: several warps share a row's parts, and the
+  // grid is as large as the row tiles, not as the workers (4 x 64 heads, 38 parts: 42.9 us
+  // with the other form, 36.3 with this; four groups: 40.3; 2 x 2 x 64 heads in the pair
+  // kernel: 23.0, 20.1, with two groups 21.5).  With fewer parts a search of the job
+  // costs more than it saves (64 x 16 heads: 60 -> 64 us)
   const bool many = plan.workers >= 8 * plan.merge_tiles;
   const unsigned jobs = unsigned(many ? plan.merge_tiles : plan.workers);
   if (plan.narrow) {
-    if (many) return launch_merge(paged_merge_kernel<4>, a, dim3(jobs, unsigned(plan.narrow)), 512, stream);
+    if (many) return launch_merge(paged_merge_kernel<2>, a, dim3(jobs, unsigned(plan.narrow)), 256, stream);
     return launch_merge(paged_merge_kernel<1>, a, dim3(jobs, unsigned(plan.narrow) / 2), 256, stream);
   }
   if (many) return launch_merge(paged_merge_pair_kernel<4>, a, dim3(jobs, 32), 512, stream);
