@@ -45,8 +45,8 @@
 // What bounds the pair kernel: shared memory.  A tile of 64 keys takes ~2420 cycles,
 // in which the operands' reads (1248), the loaders' and softmax warps' accesses (579)
 // and the bulk copies (512) keep its port busy for ~2340.  One chunk of 2048 tokens,
-// 64 heads, over 8192 positions: 2455 us = 1070 TFLOP/s, 56% of the measured bf16
-// peak; 7 chunks of 300 tokens, 16 heads, over up to 5000: 222 us.
+// 64 heads, after 8192 earlier positions: 2455 us = 1070 TFLOP/s, 56% of the measured
+// bf16 peak; 7 chunks of up to 300 tokens, 16 heads, up to 4927 positions: 222 us.
 //
 // Schedule.  A row tile takes a few slots for its start (kPairStart, kNarrowStart: what
 // a unit's first tile and last store take, in key tiles) and one per key tile; the
