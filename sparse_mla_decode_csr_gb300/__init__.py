@@ -485,6 +485,8 @@ def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
         _fail(SMLA_ERR_SHAPE, what, "sink is f32 [heads]")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()):
         _fail(SMLA_ERR_SHAPE, what, "lse is contiguous f32 [rows, heads]")
+    if workspace_tensor is not None and not workspace_tensor.is_contiguous():
+        _fail(SMLA_ERR_STRIDE, what, "workspace_tensor is contiguous")
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
     device = _current_device(what, (q, out, sink, lse, kv_cache, block_table, cu_rows, seq_lens, status,
                                     workspace_tensor))

@@ -110,7 +110,7 @@ def call_read(t):
 
 def call_attend(t):
     smla.smla_paged_attend(t["q"], t["kv"], t["table"], t["cu"], t["sl"], 0.05, t["sink"], t["out"], t["lse"],
-                           status=t["status"])
+                           status=t["status"], workspace_tensor=t.get("ws"))
 
 
 SHARED = [
@@ -149,9 +149,17 @@ def test_the_binding_checks_write_and_read(call, kw, why):
     (dict(out=torch.zeros(5, 4, 512)), "shape"), (dict(out=torch.zeros(5, 3, 512, dtype=torch.bfloat16)), "shape"),
     (dict(q=torch.zeros(5, 4, 1152, dtype=torch.bfloat16)[..., ::2]), "stride"),
     (dict(sink=torch.zeros(3)), "shape"), (dict(sink=torch.zeros(4, dtype=torch.bfloat16)), "shape"),
+    (dict(ws=torch.zeros(1, dtype=torch.uint8).expand(1 << 30)), "stride"),
     (dict(lse=torch.zeros(4, 5)), "shape"), (dict(lse=torch.zeros(5, 8)[:, ::2]), "shape"),
 ])
 def test_the_binding_checks_attend(kw, why):
     with pytest.raises(smla.SmlaError) as e:
         call_attend({**tensors(), **kw})
     assert e.value.code == BAD[why]
+
+
+@pytest.mark.parametrize("kw", [dict(n_rows=(1 << 30) + 1), dict(n_seqs=(1 << 24) + 1), dict(page_size=0),
+                                dict(page_size=1 << 16, max_pages=1 << 15), dict(num_heads=0), dict(num_heads=129)])
+def test_the_workspace_of_invalid_sizes_is_zero(kw):
+    sizes = dict(dict(n_rows=4, num_heads=16, n_seqs=2, page_size=16, max_pages=4), **kw)
+    assert smla.smla_paged_attend_workspace_size(**sizes) == 0

@@ -93,6 +93,7 @@ COPY_CASES = [
     ([(5, 9), (0, 4), (1, 70), (33, 33)], 16, 32, 2, 3),
     ([(3, 100)] * 70, 48, 0, 0, 1),
     ([(700, 1000), (999, 999)], 64, 16, 1, 40),
+    ([(2601, 2605)], 100, 0, 0, 1),  # 16-bit reads of two rows a warp, the last one alone
 ]
 
 
@@ -639,3 +640,32 @@ def test_attend_wait_timeout_sets_the_status_and_leaves_the_context_usable(heads
     q, sk, out, lse, st = attend(c, heads)
     assert st == 0
     check(c, q, out, lse, 1 / 24, sk, True)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_attend_batches_drawn_at_random(seed):
+    # every head count, odd row tiles, more rows than positions, tables that end
+    # before the sequence does, pages without a record
+    r = np.random.default_rng(100 + seed)
+    heads = int(r.choice([1, 3, 7, 16, 18, 33, 40, 64, 90, 128]))
+    page = int(r.choice([1, 5, 16, 24, 64, 100]))
+    most = 2400 // heads
+    lens = [(int(r.integers(0, most)), int(r.integers(0, 700))) for _ in range(int(r.integers(1, 7)))]
+    lens.append((1 + most // 3, 400))
+    c = Batch(lens, page, seed=seed, front=int(r.integers(0, 3)), behind=int(r.integers(0, 3)), page_pad=48)
+    if seed % 2:
+        c.table = c.table[:, :max(1, c.table.shape[1] * 2 // 3)].contiguous()
+    c.table[torch.rand(c.table.shape, generator=gen(seed)) < 0.08] = -1
+    causal, sink = bool(r.integers(0, 4)), bool(r.integers(0, 2))
+    q, sk, out, lse, _ = attend(c, heads, causal=causal, sink=sink)
+    check(c, q, out, lse, 1 / 24, sk, causal)
+
+
+def test_sequences_that_share_their_first_pages():
+    c = Batch([(3, 200), (1, 170), (20, 100)], 16)
+    c.table[1, :8] = c.table[0, :8]
+    c.table[2, :4] = c.table[0, :4]
+    c.table[2, 4] = c.table[2, 3]  # the same page twice in one history
+    q, sk, out, lse, st = attend(c, 16)
+    check(c, q, out, lse, 1 / 24, sk, True)
+    assert st == 0
