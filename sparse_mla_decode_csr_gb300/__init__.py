@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -343,7 +344,25 @@ def smla_pack_records(latent: torch.Tensor, rope: torch.Tensor, kv_out: torch.Te
 # ---- the paged cache ----
 #
 # These calls can take less time on the GPU than their checks do here, so the
-# checks read each tensor's properties once and the messages are made on failure.
+# checks read each tensor's properties once, the messages are made on failure, and
+# the C structs (PagedBatch, PagedAttendParams) are packed as bytes.
+
+_BATCH_FORMAT = "PqqiiPqPPqi4xP"
+_pack_batch = struct.Struct(_BATCH_FORMAT).pack
+_pack_attend = struct.Struct(_BATCH_FORMAT + "iiPqqf4xPPqqP").pack
+
+
+def _packed(name: str, restype, *argtypes):
+    f = lib[name]  # a function object of its own, beside the typed one
+    f.restype, f.argtypes = restype, (ctypes.c_void_p, *argtypes)
+    return f
+
+
+_copy_args = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p)
+_write_packed = _packed("smla_paged_write", ctypes.c_int, *_copy_args)
+_read_packed = _packed("smla_paged_read", ctypes.c_int, *_copy_args)
+_workspace_packed = _packed("smla_paged_attend_workspace_size", ctypes.c_size_t)
+_attend_packed = _packed("smla_paged_attend", ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)
 
 
 def _fail(code: int, what: str, why: str):
@@ -374,6 +393,8 @@ def _paged_batch(what: str, kv_cache: torch.Tensor, block_table: torch.Tensor, c
     if kv_cache.dtype != torch.uint8 or kv_cache.dim() != 3 or kv_cache.shape[2] != RECORD_BYTES:
         _fail(SMLA_ERR_SHAPE, what, f"kv_cache is uint8 [n_pages, page_size, {RECORD_BYTES}]")
     n_pages, page_size, _ = kv_cache.shape
+    if page_size >> 30:
+        _fail(SMLA_ERR_SHAPE, what, "a page has at most 2^30 records")
     page_stride, record_stride, byte_stride = kv_cache.stride()
     # (a dimension of one element, or an empty cache, may carry any stride)
     if n_pages and page_size and (byte_stride != 1 or (page_size > 1 and record_stride != RECORD_BYTES)):
@@ -393,7 +414,7 @@ def _paged_batch(what: str, kv_cache: torch.Tensor, block_table: torch.Tensor, c
         _fail(SMLA_ERR_SHAPE, what, "status is int32 [1]")
     return (kv_cache.data_ptr(), n_pages, page_stride if n_pages > 1 else page_size * RECORD_BYTES, page_size, max_pages,
             block_table.data_ptr(), table_stride if n_seqs > 1 else max_pages, cu_rows.data_ptr(), seq_lens.data_ptr(),
-            n_rows, n_seqs, None if status is None else status.data_ptr())
+            n_rows, n_seqs, 0 if status is None else status.data_ptr())
 
 
 def _paged_copy(what, call, kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status) -> None:
@@ -413,7 +434,7 @@ def _paged_copy(what, call, kv_cache, block_table, cu_rows, seq_lens, latent, ro
         ls, rs = LATENT_DIM, ROPE_DIM
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
     device = _current_device(what, (latent, rope, kv_cache, block_table, cu_rows, seq_lens, status))
-    rc = call(PagedBatch(*batch), latent.data_ptr(), ls, rope.data_ptr(), rs, dtype, _launch_stream(stream, device))
+    rc = call(_pack_batch(*batch), latent.data_ptr(), ls, rope.data_ptr(), rs, dtype, _launch_stream(stream, device))
     if rc != 0:
         raise SmlaError(rc, what)
 
@@ -430,7 +451,7 @@ def smla_paged_write(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.T
     is negative are skipped; ids >= n_pages and positions past the table are
     skipped and set STATUS_INDEX_OOB.  The rows' positions must lie in different
     slots.  See include/smla.h."""
-    _paged_copy("smla_paged_write", lib.smla_paged_write, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
+    _paged_copy("smla_paged_write", _write_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
 
 
@@ -441,7 +462,7 @@ def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: 
     [rows, 64] (bf16, f16 or f32).  Batch as smla_paged_write: row r of sequence
     b gets position seq_lens[b] - (cu_rows[b + 1] - r); masked positions give
     zeros, rows of no sequence are left as they were.  See include/smla.h."""
-    _paged_copy("smla_paged_read", lib.smla_paged_read, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
+    _paged_copy("smla_paged_read", _read_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
 
 
@@ -490,25 +511,28 @@ def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
     device = _current_device(what, (q, out, sink, lse, kv_cache, block_table, cu_rows, seq_lens, status,
                                     workspace_tensor))
-    p = PagedAttendParams(PagedBatch(*batch), heads, 1 if causal else 0, q.data_ptr(), q_row, q_head, float(sm_scale),
-                          None if sink is None else sink.data_ptr(), out.data_ptr(), o_row, o_head,
-                          None if lse is None else lse.data_ptr())
+    try:
+        p = _pack_attend(*batch, heads, 1 if causal else 0, q.data_ptr(), q_row, q_head, sm_scale,
+                         0 if sink is None else sink.data_ptr(), out.data_ptr(), o_row, o_head,
+                         0 if lse is None else lse.data_ptr())
+    except OverflowError:
+        _fail(SMLA_ERR_SHAPE, what, "sm_scale is no finite f32")
     s = _launch_stream(stream, device)
     ws = workspace_tensor
     if ws is None:
-        nbytes = lib.smla_paged_attend_workspace_size(p)
+        nbytes = _workspace_packed(p)
         if nbytes:
             # a block of this call's own, on its stream: calls on other streams and
             # other captured graphs never share it
             if stream is None:
-                ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+                ws = kv_cache.new_empty(nbytes)
             else:
                 if not isinstance(stream, torch.cuda.Stream):
                     stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
                 with torch.cuda.stream(stream):
-                    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    rc = lib.smla_paged_attend(p, None if ws is None else ws.data_ptr(),
-                               0 if ws is None else ws.numel() * ws.element_size(), s)
+                    ws = kv_cache.new_empty(nbytes)
+    rc = _attend_packed(p, None if ws is None else ws.data_ptr(),
+                               0 if ws is None else ws.nbytes, s)
     if rc != 0:
         raise SmlaError(rc, what)
 

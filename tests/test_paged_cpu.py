@@ -117,6 +117,7 @@ SHARED = [
     (dict(kv=torch.zeros(6, 16, 655, dtype=torch.uint8)), "shape"),
     (dict(kv=torch.zeros(6, 16, 656, dtype=torch.int8)), "shape"),
     (dict(kv=torch.zeros(96, 656, dtype=torch.uint8)), "shape"),
+    (dict(kv=torch.zeros(0, 1 << 31, 656, dtype=torch.uint8)), "shape"),
     (dict(kv=torch.zeros(6, 16, 1312, dtype=torch.uint8)[..., ::2]), "stride"),
     (dict(kv=torch.zeros(6, 16, 672, dtype=torch.uint8)[..., :656]), "stride"),
     (dict(table=torch.zeros(2, 3, dtype=torch.int64)), "shape"),
@@ -163,3 +164,11 @@ def test_the_binding_checks_attend(kw, why):
 def test_the_workspace_of_invalid_sizes_is_zero(kw):
     sizes = dict(dict(n_rows=4, num_heads=16, n_seqs=2, page_size=16, max_pages=4), **kw)
     assert smla.smla_paged_attend_workspace_size(**sizes) == 0
+
+
+def test_packed_structs_have_the_c_layout():
+    # every field with a value of its own, through the formats that the calls use
+    values = list(range(101, 113))
+    assert bytes(smla.PagedBatch(*values)) == smla._pack_batch(*values)
+    rest = [201, 1, 203, 204, 205, 0.25, 207, 208, 209, 210, 211]
+    assert bytes(smla.PagedAttendParams(smla.PagedBatch(*values), *rest)) == smla._pack_attend(*values, *rest)

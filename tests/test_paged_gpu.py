@@ -669,3 +669,11 @@ def test_sequences_that_share_their_first_pages():
     q, sk, out, lse, st = attend(c, 16)
     check(c, q, out, lse, 1 / 24, sk, True)
     assert st == 0
+
+
+def test_attend_refuses_a_scale_that_is_no_finite_f32():
+    c = Batch([(1, 20)], 16)
+    for scale in (1e40, float("inf"), float("nan")):
+        with pytest.raises(smla.SmlaError) as e:
+            attend(c, 16, sm_scale=scale)
+        assert e.value.code == smla.SMLA_ERR_SHAPE
