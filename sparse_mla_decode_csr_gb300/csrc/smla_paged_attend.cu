@@ -1278,9 +1278,10 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // Warps (16): 0-3 softmax, 4-11 loaders, 12-13 half of QK's K-steps each, 14-15
 // two blocks of PV each.
 //
-// What bounds it: a tile's two chains, record loads and conversion (~4000 cycles) and
-// QK, softmax, PV (~3300), which alternate over the two stages that shared memory
-// holds, and for short rows the ~10 us until the first scores.  64 x 16 heads over up
+// What bounds it: the loaders' conversion (~1.85 us a tile of 64 records by eight warps
+// at the register limit; with a third stage behind them, and Q in tensor memory to make
+// room for it, 64 x 16 took 62 us instead of 60), and for short rows the ~10 us until
+// the first scores and the partials' way through L2.  64 x 16 heads over up
 // to 4096 positions: 60 us (131 MB of records: 2.2 TB/s); 4 x 64 heads over up to 16384:
 // 36 us; one token, 16 heads, 500 positions: 14 us.
 
