@@ -677,3 +677,25 @@ def test_attend_refuses_a_scale_that_is_no_finite_f32():
         with pytest.raises(smla.SmlaError) as e:
             attend(c, 16, sm_scale=scale)
         assert e.value.code == smla.SMLA_ERR_SHAPE
+
+
+def test_attend_a_chunk_of_over_a_thousand_row_tiles():
+    # 128 heads: a row tile is one token, and the schedule looks for a worker's first
+    # one among 1100 in two steps; a sample of the rows is compared
+    c = Batch([(2, 40), (1100, 1130), (1, 3)], 64)
+    q, sk, out, lse, st = attend(c, 128, sink=True)
+    assert st == 0 and torch.isfinite(out.float()).all()
+    picked = [x for x in c.positions()][::37]
+    idx, ptr = [], [0]
+    for _, b, p in picked:
+        idx += [c.slot(b, t) for t in range(p + 1)]
+        ptr.append(len(idx))
+    rows = [r for r, _, _ in picked]
+    idx, ptr = np.array(idx, np.int32), np.array(ptr, np.int32)
+    qq, s = q.double().numpy()[rows], sk.double().numpy()
+    ref, ref_lse, _ = oracle.sparse_mla_decode(qq, c.rec, idx, ptr, None, 1 / 24, s)
+    a_out, a_lse = allowance(qq, c.rec, idx, ptr, None, 1 / 24, s)
+    err = np.abs(out.double().cpu().numpy()[rows] - ref) - (a_out + 2.0 ** -8 * np.abs(ref) + 1e-30)
+    assert err.max() <= 0
+    e = np.abs(lse.double().cpu().numpy()[rows] - ref_lse) - (a_lse + 2.0 ** -18 * (1 + np.abs(ref_lse).max()))
+    assert e.max() <= 0
