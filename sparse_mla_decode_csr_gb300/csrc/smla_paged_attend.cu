@@ -97,11 +97,21 @@ constexpr int kOffQ = kOffV + 2 * kStageV;
 constexpr int kQBlock = kCtaRows * 128;
 constexpr int kOffP = kOffQ + 9 * kQBlock;
 constexpr int kOffMisc = kOffP + kCtaRows * 128;
-// narrow kernel: K of all 64 keys, in two stages; V is the same memory
-constexpr int kStageNarrow = 9 * kTileKeys * 128;
-constexpr int kOffQNarrow = 2 * kStageNarrow;
-constexpr int kOffPNarrow = kOffQNarrow + 9 * kQBlock;
-constexpr int kOffMiscNarrow = kOffPNarrow + kCtaRows * 128;
+// narrow and few-row kernel: K of all keys of a tile, in two stages; V is the same
+// memory.  The few-row kernel keeps Q in tensor memory and takes tiles of 96 keys.
+constexpr int kQRowPitch = kQK * 2 / 3 + 16;
+template <int kN>
+struct Narrow {
+  static constexpr bool kFew = kN == 16;
+  static constexpr int kKeys = kFew ? 96 : kTileKeys;  // of a tile
+  static constexpr int kLoaders = kKeys / 8;
+  static constexpr int kBlock = kKeys * 128;           // a 64-dim block of a tile
+  static constexpr int kStage = 9 * kBlock;
+  static constexpr int kOffQ = 2 * kStage;
+  static constexpr int kOffP = kOffQ + (kFew ? 0 : 9 * kQBlock);
+  static constexpr int kOffMisc = kOffP + (kFew ? 16 * kQRowPitch + 256 : kN * 128);  // (P of 4 KB, q on its way)
+};
+constexpr uint32_t kTmemQFew = 64, kTmemSFew = kTmemQFew + kQK / 2;  // behind O's 64 columns
 constexpr int kNarrowThreads = 16 * 32;
 constexpr int kNarrowQk = 12;  // and 13
 constexpr int kNarrowPv = 14;  // and 15
@@ -151,10 +161,12 @@ struct Misc {
   float alpha[2][kCtaRows], factor[kCtaRows];  // narrow kernel: per row
   // per tile: a byte per 8 keys, bit: a key before the end that has no record
   uint8_t flags[4][kTileKeys / 8];
+  uint8_t flags_few[4][16];  // few-row kernel: 12 are used
 };
 constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc));
-constexpr int kNarrowSmem = kOffMiscNarrow + int(sizeof(Misc));
-static_assert(kAttendSmem <= 232448 && kNarrowSmem <= 232448, "shared memory of a CTA");
+template <int kN>
+constexpr int kNarrowSmem = Narrow<kN>::kOffMisc + int(sizeof(Misc));
+static_assert(kAttendSmem <= 232448 && kNarrowSmem<16> <= 232448 && kNarrowSmem<64> <= 232448, "shared memory of a CTA");
 
 // ---- launch order ----
 
@@ -221,6 +233,16 @@ __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// A from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -633,6 +655,48 @@ __device__ __forceinline__ void finish_q() {
   __syncwarp();
 }
 
+// q of a unit's up to 16 rows into tensor memory, 32 lanes by each of four warps: lane
+// l gets row l % 16, so that S has all rows wherever a softmax warp looks for them.
+// The rows are loaded whole by the 128 threads together and change hands in shared
+// memory, a third at a time (each lane loading its own row took 4 us).
+__device__ __noinline__ void load_q_tmem(const AttendArgs& a, uint32_t buf, uint32_t at, int32_t row0, int32_t rows) {
+  constexpr int kThird = kQK / 8 / 3, kEach = 16 * kThird / 128;  // 16-byte chunks of a row's third, of a thread
+  uint4 v[3][kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int32_t j = threadIdx.x + 128 * i, m = j / kThird, tok = m / a.heads;
+    const uint16_t* src = a.q + int64_t(row0 + tok) * a.q_row + int64_t(m - tok * a.heads) * a.q_head + (j - m * kThird) * 8;
+#pragma unroll
+    for (int third = 0; third < 3; ++third) {
+      v[third][i] = make_uint4(0, 0, 0, 0);
+      if (m < rows) v[third][i] = ldg_v4_now(src + third * kThird * 8);
+    }
+  }
+  const uint32_t mine = buf + (threadIdx.x & 15) * kQRowPitch;
+#pragma unroll
+  for (int third = 0; third < 3; ++third) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int32_t j = threadIdx.x + 128 * i, m = j / kThird;
+      st_shared_v4(buf + m * kQRowPitch + (j - m * kThird) * 16, v[third][i].x, v[third][i].y, v[third][i].z, v[third][i].w);
+    }
+    named_barrier(1, 128);
+#pragma unroll 1
+    for (int c = 0; c < kThird; c += 4) {
+      uint32_t x[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = ld_shared_v4(mine + (c + i) * 16);
+        x[4 * i] = w.x, x[4 * i + 1] = w.y, x[4 * i + 2] = w.z, x[4 * i + 3] = w.w;
+      }
+      tmem_st16(at + 4 * (third * kThird + c), x);
+    }
+    named_barrier(1, 128);
+  }
+  tmem_wait_st();
+  tc_fence_before();
+}
+
 // ---- roles ----
 
 // A loader warp's cursor over the pair's or CTA's tiles, `kStep` tiles at a time,
@@ -661,6 +725,36 @@ struct Cursor {
     const int32_t owner = kPair ? rank ^ (lane >> 3) : 0;
     const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 7);
     in = more && lane < (kPair ? 2 : 1) * kKeysPerWarp && pos < end;  // (the end lies within the table)
+    if (in) {
+      const uint32_t page = page_of(a.b, uint32_t(pos));
+      offset = pos - int32_t(page) * a.b.page_size;
+      id = int32_t(ldg_u32_now(a.b.table + int64_t(seq) * a.b.table_stride + page));
+    }
+  }
+};
+
+// The narrow kernels' cursor: tiles of kKeys keys of the unit's keys [key0, stop), and
+// a warp's 8 records there by lanes 0-7.
+template <int kKeys>
+struct KeyCursor {
+  Units units;
+  bool more;
+  int32_t key, key0, stop, end, seq, row0, rows;
+
+  __device__ __forceinline__ void next_unit(const AttendArgs& a) {
+    Unit u;
+    more = units.next_inline(a, u);
+    key = key0 = u.t0 * kTileKeys, stop = u.t1 * kTileKeys, end = min(u.end, stop);
+    seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
+  }
+  __device__ __forceinline__ void step(const AttendArgs& a) {
+    if (more && (key += kKeys) >= stop) next_unit(a);
+  }
+  __device__ __forceinline__ void look_up(const AttendArgs& a, int w, int32_t& id, int32_t& offset, bool& in) const {
+    const int lane = threadIdx.x & 31;
+    id = -1;
+    const int32_t pos = key + w * kKeysPerWarp + (lane & 7);
+    in = more && lane < kKeysPerWarp && pos < end;
     if (in) {
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
@@ -799,36 +893,38 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   }
 }
 
-// The narrow kernel's loaders: all eight warps load the 64 keys of every tile, a
-// warp 8 of them.  Record by record: convert, store, and send the same registers
+// The narrow and few-row kernel's loaders: all eight or twelve warps load every tile, a
+// warp 8 of its keys.  Record by record: convert, store, and send the same registers
 // off for the next tile's record, so that a warp's 8 records are in flight at
 // nearly all times (42 KB an SM: what HBM needs at ~1 us latency).
-__device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms, uint32_t base, int copies) {
+template <int kN>
+__device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms, uint32_t base) {
+  using L = Narrow<kN>;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - kFirstLoader;
-  const uint32_t k_at = base + kOffK + (lane >> 3) * (kTileKeys * 128) + w * kKeysPerWarp * 128;
-  const uint32_t rope_at = base + kOffK + 8 * (kTileKeys * 128) + w * kKeysPerWarp * 128;
-  Cursor<false> c;  // one tile ahead of the one that is converted
+  const uint32_t k_at = base + kOffK + (lane >> 3) * L::kBlock + w * kKeysPerWarp * 128;
+  const uint32_t rope_at = base + kOffK + 8 * L::kBlock + w * kKeysPerWarp * 128;
+  KeyCursor<L::kKeys> c;  // one tile ahead of the one that is converted
   c.units.start(a, ms);
   c.next_unit(a);
   if (!c.more) return;
   Raw raw;
   int32_t id, offset = 0;
   bool in;
-  c.look_up(a, 0, w, id, offset, in);
+  c.look_up(a, w, id, offset, in);
   uint64_t rec = record_address(a, id, offset);
   uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && in);
   raw = load_scattered(rec);
   bool starts = true, any = true;
   int32_t row0 = c.row0, rows = c.rows;
   c.step(a);
-  c.look_up(a, 0, w, id, offset, in);
+  c.look_up(a, w, id, offset, in);
   for (uint32_t g = 0; any; ++g) {
     const uint32_t stage = g & 1;
-    if (starts) {
+    if (!L::kFew && starts) {
       // q of the unit, once the last QK of the unit before is done (QK(g - 3), on the
       // same barrier, is past: this warp has waited for PV(g - 3))
       if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[stage ^ 1], ((g - 1) >> 1) & 1)) return;
-      load_q(a, base + kOffQNarrow, 0, w, 2 * kLoaderWarps, row0, rows, copies);
+      load_q(a, base + L::kOffQ, 0, w, L::kLoaders, row0, rows, kCtaRows / kN);
     }
     rec = record_address(a, id, offset);
     const uint32_t next_holes = __ballot_sync(0xffffffffu, rec == 0 && in);
@@ -841,7 +937,7 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
 #pragma unroll
       for (int i = 0; i < 2; ++i) odd |= odd_scale(raw.scale[j][i]), top = nan_codes(raw.lat[j][i], top);
     const bool plain = !__any_sync(0xffffffffu, odd != 0 || (top & 0x80808080u) != 0);
-    const uint32_t k = k_at + stage * kStageNarrow;
+    const uint32_t k = k_at + stage * L::kStage;
     uint32_t bad_keys = 0;
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j) {
@@ -863,7 +959,7 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
       }
       const uint32_t at = k + j * 128 + ((uint32_t(lane & 7) ^ j) << 4);
       st_shared_v4(at, v[0][0], v[0][1], v[0][2], v[0][3]);
-      st_shared_v4(at + 4 * (kTileKeys * 128), v[1][0], v[1][1], v[1][2], v[1][3]);
+      st_shared_v4(at + 4 * L::kBlock, v[1][0], v[1][1], v[1][2], v[1][3]);
       if (run) load_record(reinterpret_cast<const uint8_t*>(first) + j * kRecordBytes, j, raw);
     }
 #pragma unroll
@@ -872,25 +968,25 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
       uint4 r = raw.rope[i];
       // (NaN in the rope of a key whose latent is not finite, as in loader_role)
       if ((lane & 7) == 0 && ((bad_keys >> key) & 1u)) r.x = 0x7FC07FC0u;
-      st_shared_v4(rope_at + stage * kStageNarrow + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
+      st_shared_v4(rope_at + stage * L::kStage + key * 128 + ((uint32_t(lane & 7) ^ key) << 4), r.x, r.y, r.z, r.w);
       if (run)
         raw.rope[i] = ldg_v4_now(reinterpret_cast<const uint8_t*>(first) + key * kRecordBytes + kRopeOffset + (lane & 7) * 16);
     }
     if (!run && c.more) raw = load_scattered(rec);
-    if (starts) {
+    if (!L::kFew && starts) {
       finish_q();
       if (lane == 0) mbar_arrive(&ms->q_full);
     }
-    if (lane == 0) ms->flags[g & 3][w] = uint8_t(holes);
+    if (lane == 0) (L::kFew ? ms->flags_few[g & 3] : ms->flags[g & 3])[w] = uint8_t(holes);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(&ms->k_full[stage]);
     holes = next_holes;
     any = c.more;
-    starts = c.t == c.t0;
+    starts = c.key == c.key0;
     row0 = c.row0, rows = c.rows;
     c.step(a);
-    c.look_up(a, 0, w, id, offset, in);
+    c.look_up(a, w, id, offset, in);
     // the records of the tile after next set out for L2
     if (in && lane == 0 && id >= 0 && id < a.b.n_pages && a.b.page_size % kKeysPerWarp == 0)
       prefetch_l2(reinterpret_cast<const uint8_t*>(record_address(a, id, offset)), kKeysPerWarp * kRecordBytes);
@@ -1288,6 +1384,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 template <int kN>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                     int32_t worker) {
+  using L = Narrow<kN>;
   constexpr int kCopies = kCtaRows / kN, kKeys = kN;  // a thread's keys of a tile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t m = (16 * warp + (lane & 15)) % kN;   // this thread's row
@@ -1295,7 +1392,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   const bool mine = lane < 16;
   const int32_t tok = m / a.heads, head = m - tok * a.heads;
   const uint32_t lane_base = tmem + (uint32_t(warp) << 21);
-  const uint32_t p_row = base + kOffPNarrow + m * 128;
+  const uint32_t p_row = base + L::kOffP + m * 128;
   const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
   Units units;
   units.start(a, ms);
@@ -1352,13 +1449,8 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       const float use = nref == -INFINITY ? 0.f : nref;
       const float alpha = move ? ex2(ref - use) : 1.f;
       ref = nref;
-      bool moved;
-      if (kN == 16) {
-        moved = __any_sync(0xffffffffu, move);
-      } else {
-        if (mine && slice == 0) ms->alpha[stage][m] = alpha;
-        moved = named_barrier_or(1, 128, move);
-      }
+      if (mine && slice == 0) ms->alpha[stage][m] = alpha;
+      const bool moved = named_barrier_or(1, 128, move);
       uint32_t p[kKeys / 2];
       float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
@@ -1381,8 +1473,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float f = kN == 16 ? __shfl_sync(0xffffffffu, alpha, i) : ms->alpha[stage][(c & (kN - 1)) + i];
-            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * ms->alpha[stage][(c & (kN - 1)) + i]);
           }
           tmem_st16(lane_base + c, o);
         }
@@ -1457,7 +1548,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
 // of its own.
 __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                uint32_t which) {
-  const uint64_t q0 = smem_desc(base + kOffQNarrow, 16, 1024, kSw128) + which * 2;
+  const uint64_t q0 = smem_desc(base + Narrow<64>::kOffQ, 16, 1024, kSw128) + which * 2;
   const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128) + which * 2;
   Units units;
   units.start(a, ms);
@@ -1471,7 +1562,7 @@ __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, ui
       if (!warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
       if (g >= 2 && !warp_wait(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
       tc_fence_after();
-      const uint64_t kd = k0 + uint64_t((stage * kStageNarrow) >> 4);
+      const uint64_t kd = k0 + uint64_t((stage * Narrow<64>::kStage) >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kQK / 16; k += 2)
@@ -1489,8 +1580,9 @@ __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, ui
 template <int kN>
 __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                uint32_t which) {
+  using L = Narrow<kN>;
   const uint64_t v0 = smem_desc(base + kOffK + which * 4 * (kTileKeys * 128), kTileKeys * 128, 1024, kSw128);
-  const uint64_t p0 = smem_desc(base + kOffPNarrow, 16, 1024, kSw128);
+  const uint64_t p0 = smem_desc(base + L::kOffP, 16, 1024, kSw128);
   Units units;
   units.start(a, ms);
   Unit u;
@@ -1501,7 +1593,7 @@ __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, ui
       const uint32_t stage = g & 1;
       if (!warp_wait(ms, a, &ms->p_full, g & 1)) return;
       tc_fence_after();
-      const uint64_t vd = v0 + uint64_t((stage * kStageNarrow) >> 4);
+      const uint64_t vd = v0 + uint64_t((stage * Narrow<64>::kStage) >> 4);
       if (elect_one()) {
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -1521,14 +1613,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   const uint32_t base = smem_u32(raw_smem);
   const int32_t worker = blockIdx.x;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   let_dependents_launch();
   if (threadIdx.x == 0) a.merge[worker * 4] = 0;
   if (base & 1023u) {
     if (threadIdx.x == 0 && a.b.status) atomicOr(a.b.status, SMLA_STATUS_SMEM_LAYOUT);
     return;
   }
-  Misc* ms = reinterpret_cast<Misc*>(raw_smem + kOffMiscNarrow);
+  Misc* ms = reinterpret_cast<Misc*>(raw_smem + Narrow<kN>::kOffMisc);
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ms->k_full[i], 2 * kLoaderWarps);
@@ -1556,7 +1648,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   if (warp < kFirstLoader) {
     narrow_softmax_role<kN>(a, ms, base, tmem, worker);
   } else if (warp < kNarrowQk) {
-    narrow_loader_role(a, ms, base, kCtaRows / kN);
+    narrow_loader_role<kN>(a, ms, base);
   } else {
     if (warp < kNarrowPv) narrow_qk_role(a, ms, base, tmem, uint32_t(warp - kNarrowQk));
     else narrow_pv_role<kN>(a, ms, base, tmem, uint32_t(warp - kNarrowPv));
@@ -1572,6 +1664,270 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   __syncthreads();
   tc_fence_after();
   if (warp == kNarrowQk) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---- the few-row kernel ----
+//
+// Up to 16 rows a tile: the loaders' conversion bounds the time, so twelve of the 16
+// warps load, in tiles of 96 keys, and warps 0-3 do the rest.  Q lies in tensor memory
+// (288 columns, the A operand of S[64, 96] = Q K^T), which leaves shared memory to two
+// stages of 96 keys.  S holds four copies of the 16 rows, one in each warp's lanes; a
+// warp takes 24 of the keys.  Per tile: S read, maxima exchanged, P stored, then warp 0
+// issues the next QK, warps 1 and 2 two blocks of O^T += V^T P^T each.
+
+// QK of tile g, by warp 0.
+__device__ __forceinline__ void few_issue_qk(const AttendArgs& a, Misc* ms, uint64_t k0, uint32_t tmem, uint32_t g) {
+  using L = Narrow<16>;
+  const uint32_t stage = g & 1;
+  if (warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1)) {
+    tc_fence_after();
+    const uint64_t kd = k0 + uint64_t((stage * L::kStage) >> 4);
+    if (elect_one()) {
+#pragma unroll
+      for (int k = 0; k < kQK / 16; ++k)
+        mma_ts(tmem + kTmemSFew, tmem + kTmemQFew + 8 * k, kd + uint64_t(((k >> 2) * L::kBlock + (k & 3) * 32) >> 4),
+               idesc_bf16(kCtaRows, L::kKeys, 0, 0), k > 0);
+      mma_commit(&ms->qk_done[stage]);
+    }
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
+                                                 int32_t worker) {
+  using L = Narrow<16>;
+  constexpr int kN = 16, kKeys = 24;  // rows; a thread's keys of a tile
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t m = lane & 15;
+  const int slice = warp;
+  const bool mine = lane < 16;
+  const int32_t tok = m / a.heads, head = m - tok * a.heads;
+  const uint32_t lane_base = tmem + (uint32_t(warp) << 21);
+  const uint32_t p_row = base + L::kOffP + m * 128;
+  const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
+  const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128);
+  const uint32_t pv = uint32_t(warp) - 1;  // warps 1 and 2: blocks 2 pv and 2 pv + 1
+  const uint64_t v0 = smem_desc(base + kOffK + (pv & 1) * 4 * L::kBlock, L::kBlock, 1024, kSw128);
+  const uint64_t p0 = smem_desc(base + L::kOffP, 16, 1024, kSw128);
+  Units units;
+  units.start(a, ms);
+  Unit u;
+  uint32_t g = 0;
+  // (a wait that gives up does not end this role: its warps meet at named barriers)
+  if (ms->stall) wait_for(ms, a, &ms->never, 0);
+  while (units.next_inline(a, u)) {
+    const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
+    const int32_t key0 = t0 * kTileKeys, stop = t1 * kTileKeys, end = min(u.end, stop);
+    const bool live = mine && m < rows;
+    const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, end), 0) : end;
+    float ref = -INFINITY, l = 0.f;
+    // q (every warp has seen the last QK and PV of the unit before done)
+    load_q_tmem(a, base + L::kOffP, lane_base + kTmemQFew, u.row0, rows);
+    named_barrier(1, 128);
+    if (warp == 0) few_issue_qk(a, ms, k0, tmem, g);
+    for (int32_t key = key0; key < stop; key += L::kKeys, ++g) {
+      const uint32_t stage = g & 1;
+      wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
+      __syncwarp();
+      tc_fence_after();
+      float x[kKeys];
+      {
+        uint32_t s0[16], s1[8];
+        tmem_ld16(lane_base + kTmemSFew + kKeys * slice, s0);
+        tmem_ld8(lane_base + kTmemSFew + kKeys * slice + 16, s1);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(s0[c]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[16 + c] = __uint_as_float(s1[c]);
+      }
+      const uint8_t* f = &ms->flags_few[g & 3][3 * slice];
+      const uint32_t flags = f[0] | uint32_t(f[1]) << 8 | uint32_t(f[2]) << 16;
+      if (a.scale_log2 <= 0.f) {
+        const float by = a.scale_log2 < 0.f ? -1.f : 0.f;
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) x[c] *= by;
+      }
+      const int32_t n = see - key - kKeys * slice;
+      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0) {
+        const uint32_t seen = ~flags & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
+      }
+      float tm = x[0];
+#pragma unroll
+      for (int c = 1; c < kKeys; ++c) tm = fmaxf(tm, x[c]);
+      ms->tmax[stage][warp * 32 + lane] = tm;
+      named_barrier(1, 128);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) tm = fmaxf(tm, ms->tmax[stage][(warp ^ k) * 32 + lane]);
+      tm *= scale;
+      const bool move = live && tm > ref + kMoveMargin;
+      const float nref = move ? tm : ref;
+      const float use = nref == -INFINITY ? 0.f : nref;
+      const float alpha = move ? ex2(ref - use) : 1.f;
+      ref = nref;
+      uint32_t p[kKeys / 2];
+      float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+      for (int c = 0; c < kKeys / 2; ++c) {
+        float y0, y1;
+        fma2(x[2 * c], x[2 * c + 1], scale, -use, y0, y1);
+        y0 = ex2(y0);
+        y1 = ex2(y1);
+        add2(sum0, sum1, y0, y1, sum0, sum1);
+        p[c] = pack_bf16x2(y0, y1);
+      }
+      l = l * alpha + (sum0 + sum1);
+      if (g > 0) wait_for(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
+      __syncwarp();
+      if (key > key0 && __any_sync(0xffffffffu, move)) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 4 * kN; c += 16) {
+          uint32_t o[16];
+          tmem_ld16(lane_base + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * __shfl_sync(0xffffffffu, alpha, i));
+          tmem_st16(lane_base + c, o);
+        }
+        tmem_wait_st();
+      }
+      if (mine) {  // P: two blocks of 64 and 32 keys
+#pragma unroll
+        for (int i = 0; i < kKeys / 8; ++i) {
+          const int c = slice * (kKeys / 8) + i;
+          st_shared_v4(p_row + (c >> 3) * (kN * 128) + (((c & 7) ^ (m & 7)) << 4), p[4 * i], p[4 * i + 1], p[4 * i + 2],
+                       p[4 * i + 3]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      named_barrier(2, 128);  // P is stored, S read
+      if (warp == 0) {
+        if (key + L::kKeys < stop) few_issue_qk(a, ms, k0, tmem, g + 1);
+      } else if (warp < 3) {
+        tc_fence_after();
+        const uint64_t vd = v0 + uint64_t((stage * L::kStage) >> 4);
+        if (elect_one()) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < L::kKeys / 16; ++k)
+              mma_f16_ss(tmem + (2 * pv + b) * kN, vd + uint64_t((b * 2 * L::kBlock + k * 2048) >> 4),
+                         p0 + uint64_t(((k >> 2) * (kN * 128) + (k & 3) * 32) >> 4), idesc_bf16(128, kN, 1, 0),
+                         (key == key0 && k == 0) ? 0u : 1u);
+          mma_commit(&ms->pv_done[stage]);
+        }
+        __syncwarp();
+      }
+    }
+    const bool whole = t0 == 0 && t1 == u.tiles;
+    const int64_t part = 2 * int64_t(worker) + (t0 > 0 ? 0 : 1);
+    ms->lsum[warp * 32 + lane] = l;
+    named_barrier(1, 128);
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) l += ms->lsum[(warp ^ k) * 32 + lane];
+    if (mine && slice == 0) {
+      float factor = 1.f;
+      if (whole) {
+        float lse;
+        finish_head_v(ref, l, a.sink != nullptr, a.sink != nullptr && live ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+        if (live && a.lse) a.lse[(int64_t(u.row0) + tok) * a.heads + head] = lse;
+      } else if (live) {
+        a.ml_part[(part * a.part_rows + m) * 2] = ref;
+        a.ml_part[(part * a.part_rows + m) * 2 + 1] = l;
+      }
+      ms->factor[m] = factor;
+    }
+    named_barrier(1, 128);
+    wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    tc_fence_after();
+    // a lane has dim 128 b + 32 warp + lane of every row
+    const int32_t dim = 32 * warp + lane;
+    int32_t r_tok = 0, r_head = 0;
+#pragma unroll 1
+    for (int c = 0; c < rows; c += 16) {
+      uint32_t o[4][16];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) tmem_ld16(lane_base + b * kN + c, o[b]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (c + i >= rows) break;
+        if (whole) {
+          const float f = ms->factor[c + i];
+          uint16_t* dst = a.out + (int64_t(u.row0) + r_tok) * a.o_row + int64_t(r_head) * a.o_head + dim;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) dst[128 * b] = uint16_t(pack_bf16x2(__uint_as_float(o[b][i]) * f, 0.f));
+        } else {
+          float* dst = a.o_part + (part * a.part_rows + c + i) * kLatent + dim;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) dst[128 * b] = __uint_as_float(o[b][i]);
+        }
+        if (++r_head == a.heads) r_head = 0, ++r_tok;
+      }
+    }
+    tc_fence_before();
+    if (!whole && t0 > 0 && t1 == u.tiles && threadIdx.x == 0) name_merge(a, ms, worker, u);
+  }
+}
+
+__global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_few_kernel(const __grid_constant__ AttendArgs a) {
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  const uint32_t base = smem_u32(raw_smem);
+  const int32_t worker = blockIdx.x;
+  const int warp = threadIdx.x >> 5;
+  let_dependents_launch();
+  if (threadIdx.x == 0) a.merge[worker * 4] = 0;
+  if (base & 1023u) {
+    if (threadIdx.x == 0 && a.b.status) atomicOr(a.b.status, SMLA_STATUS_SMEM_LAYOUT);
+    return;
+  }
+  Misc* ms = reinterpret_cast<Misc*>(raw_smem + Narrow<16>::kOffMisc);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms->k_full[i], Narrow<16>::kLoaders);
+      mbar_init(&ms->qk_done[i], 1);
+      mbar_init(&ms->pv_done[i], 2);
+    }
+    mbar_init(&ms->drain, 3);
+    mbar_init(&ms->never, 1);
+    fence_mbar_init();
+    ms->dead = 0;
+    ms->wait_ns = g_paged_wait_ns ? g_paged_wait_ns : kWaitNs;
+    ms->stall = g_paged_stall;
+  }
+  if (warp == 3) {
+    tmem_alloc(&ms->tmem, kTmemCols);
+    tc_fence_before();
+  }
+  find_range<kNarrowThreads>(a, ms, worker);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ms->tmem;
+  if (warp < kFirstLoader) {
+    few_compute_role(a, ms, base, tmem, worker);
+    // every MMA complete before the memory it reads goes away
+    __syncwarp();
+    if (warp < 3 && elect_one()) {  // (the lane that issued them: the same for the same mask)
+      mma_commit(&ms->drain);
+      if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
+    }
+  } else {
+    narrow_loader_role<16>(a, ms, base);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 3) {
     tmem_relinquish();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -1807,12 +2163,10 @@ AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
   return plan;
 }
 
-template <int kN>
-static cudaError_t launch_narrow(const AttendArgs& a, cudaStream_t stream) {
-  const cudaError_t err =
-      cudaFuncSetAttribute(paged_attend_narrow_kernel<kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem);
+static cudaError_t launch_narrow(void (*kernel)(AttendArgs), int smem, const AttendArgs& a, cudaStream_t stream) {
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  paged_attend_narrow_kernel<kN><<<a.workers, kNarrowThreads, kNarrowSmem, stream>>>(a);
+  kernel<<<a.workers, kNarrowThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -1856,11 +2210,11 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
   a.o_part = reinterpret_cast<float*>(ws + plan.o_off);
   cudaError_t err;
   if (plan.narrow == 16) {
-    err = launch_narrow<16>(a, stream);
+    err = launch_narrow(paged_attend_few_kernel, kNarrowSmem<16>, a, stream);
   } else if (plan.narrow == 32) {
-    err = launch_narrow<32>(a, stream);
+    err = launch_narrow(paged_attend_narrow_kernel<32>, kNarrowSmem<32>, a, stream);
   } else if (plan.narrow == 64) {
-    err = launch_narrow<64>(a, stream);
+    err = launch_narrow(paged_attend_narrow_kernel<64>, kNarrowSmem<64>, a, stream);
   } else {
     err = cudaFuncSetAttribute(paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
     if (err != cudaSuccess) return err;
