@@ -63,12 +63,12 @@ cudaError_t launch_pack(const void* latent, int64_t latent_stride, const void* r
                         int64_t rope_stride, int64_t n, void* kv_out, cudaStream_t stream);
 
 // The paged cache.  Workspace of one attend call: per worker (a pair of CTAs, or a
-// CTA of the narrow kernel) a merge job (16 bytes), two partials' (m, l) of
+// CTA of the other kernels) a merge job (16 bytes), two partials' (m, l) of
 // part_rows rows, and their O.
 struct AttendPlan {
   int32_t workers, part_rows;
   int32_t start_slots, merge_tiles;  // slots of a row tile's start; row tiles that may be shared
-  int32_t narrow;  // rows of a tile of the narrow kernel (16, 32, 64); 0: the pair kernel
+  int32_t narrow;  // rows of a tile: 16 few-row kernel, 32 and 64 narrow kernel; 0: the pair kernel
   int64_t merge_off, ml_off, o_off, total;
 };
 AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms);

@@ -7,9 +7,9 @@
 // its keys, so (token, head) pairs are the rows of two matrix products:
 //   S[128, 64] = Q[128, 576] . K[64, 576]^T,   O[128, 512] += P[128, 64] . V[64, 512].
 //
-// Two kernels, by the mean number of rows of a sequence (narrow_rows): the pair
-// kernel described here for chunks and drafts, the narrow kernel (further down) for
-// up to 64 rows.
+// Three kernels, by the mean number of rows of a sequence (narrow_rows): the pair
+// kernel described here for chunks and drafts, further down the narrow kernel for up to
+// 64 rows and the few-row kernel for up to 16.
 //
 // Row tiles.  A row tile is floor(128 / heads) consecutive tokens of one
 // sequence with all their heads.  Its keys are the positions up to its last
@@ -48,7 +48,7 @@
 // 64 heads, after 8192 earlier positions: 2455 us = 1070 TFLOP/s, 56% of the measured
 // bf16 peak; 7 chunks of up to 300 tokens, 16 heads, up to 4927 positions: 222 us.
 //
-// Schedule.  A row tile takes a few slots for its start (kPairStart, kNarrowStart: what
+// Schedule.  A row tile takes a few slots for its start (kPairStart and so on: what
 // a unit's first tile and last store take, in key tiles) and one per key tile; the
 // slots of all row tiles, in order, are split evenly over the workers (worker c of
 // G takes [c W / G, (c + 1) W / G)).  A row tile inside one worker's range is
@@ -119,8 +119,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;              // the S buffers, behind O's 256 columns
 // Slots of a row tile's start, by measurement (us): the pair kernel with 1 / 4 / 8 / 12
 // at 32 drafts of 5 tokens, 64 heads: 88 / 80 / 76 / 76; the narrow kernel with 1 / 2 / 4
-// at 4 x 64 heads: 43.7 / 42.2 / 41.3, at 64 x 16 heads over 4096: 72.9 / 73.1 / 75.2.
-constexpr int kPairStart = 8, kNarrowStart = 2;
+// at 4 x 64 heads: 43.7 / 42.2 / 41.3, at 64 x 64 heads over 4096: 88.2 / 86.4 / 87.9; the
+// few-row kernel with 1 / 2 / 4 at 64 x 16 heads: 53.5 / 53.2 / 51.8.
+constexpr int kPairStart = 8, kNarrowStart = 2, kFewStart = 4;
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
@@ -136,7 +137,7 @@ struct AttendArgs {
   const float* sink;
   float scale_log2;
   int32_t heads, tokens, causal;  // tokens: of a row tile
-  int32_t workers;                // pairs of CTAs, or CTAs of the narrow kernel
+  int32_t workers;                // pairs of CTAs, or CTAs of the other kernels
   int32_t part_rows;              // rows of a partial: 128, or 64
   int32_t coverage;               // positions the block table can hold
   int32_t start_slots;            // slots of a row tile's start
@@ -699,9 +700,7 @@ __device__ __noinline__ void load_q_tmem(const AttendArgs& a, uint32_t buf, uint
 
 // ---- roles ----
 
-// A loader warp's cursor over the pair's or CTA's tiles, `kStep` tiles at a time,
-// and the addresses of its 8 keys there.
-template <bool kPair>
+// A loader warp's cursor over the pair's tiles and the addresses of its 8 keys there.
 struct Cursor {
   Units units;
   bool more;
@@ -709,22 +708,22 @@ struct Cursor {
 
   __device__ __forceinline__ void next_unit(const AttendArgs& a) {
     Unit u;
-    more = kPair ? units.next(a, u) : units.next_inline(a, u);
+    more = units.next(a, u);
     t = t0 = u.t0, t1 = u.t1, end = u.end, seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
   }
   __device__ __forceinline__ void step(const AttendArgs& a) {
     if (more && ++t == t1) next_unit(a);
   }
-  // Page id and offset at the cursor: lanes 0-7 the warp's keys, in a pair lanes
-  // 8-15 the peer warp's (both CTAs need to know which keys have no record).  The id
+  // Page id and offset at the cursor: lanes 0-7 the warp's keys, lanes 8-15 the peer
+  // warp's (both CTAs need to know which keys have no record).  The id
   // is first looked at when the loads set out; in: a key before the end.
   __device__ __forceinline__ void look_up(const AttendArgs& a, int32_t rank, int w, int32_t& id, int32_t& offset,
                                           bool& in) const {
     const int lane = threadIdx.x & 31;
     id = -1;
-    const int32_t owner = kPair ? rank ^ (lane >> 3) : 0;
+    const int32_t owner = rank ^ (lane >> 3);
     const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 7);
-    in = more && lane < (kPair ? 2 : 1) * kKeysPerWarp && pos < end;  // (the end lies within the table)
+    in = more && lane < 2 * kKeysPerWarp && pos < end;  // (the end lies within the table)
     if (in) {
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
@@ -733,7 +732,7 @@ struct Cursor {
   }
 };
 
-// The narrow kernels' cursor: tiles of kKeys keys of the unit's keys [key0, stop), and
+// The narrow and the few-row kernel's cursor: tiles of kKeys keys of the unit's keys [key0, stop), and
 // a warp's 8 records there by lanes 0-7.
 template <int kKeys>
 struct KeyCursor {
@@ -793,7 +792,7 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   // The records' addresses are looked up while the tile before is converted; their
   // loads set out as soon as its registers are free and land while the other group
   // works.
-  Cursor<true> c;
+  Cursor c;
   c.units.start(a, ms);
   c.next_unit(a);
   if (group == 1) c.step(a);
@@ -987,9 +986,12 @@ __device__ __forceinline__ void narrow_loader_role(const AttendArgs& a, Misc* ms
     row0 = c.row0, rows = c.rows;
     c.step(a);
     c.look_up(a, w, id, offset, in);
-    // the records of the tile after next set out for L2
-    if (in && lane == 0 && id >= 0 && id < a.b.n_pages && a.b.page_size % kKeysPerWarp == 0)
-      prefetch_l2(reinterpret_cast<const uint8_t*>(record_address(a, id, offset)), kKeysPerWarp * kRecordBytes);
+    // the records of the tile after next set out for L2 (64 x 16: 52 us, without 58; one
+    // by one in pages that split a warp's eight: 67 us with pages of one record, without 72)
+    const bool rows_of_8 = a.b.page_size % kKeysPerWarp == 0;
+    if (in && (lane == 0 || !rows_of_8) && id >= 0 && id < a.b.n_pages)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(record_address(a, id, offset)),
+                  (rows_of_8 ? kKeysPerWarp : 1) * kRecordBytes);
   }
 }
 
@@ -1363,23 +1365,21 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 
 // ---- the narrow kernel ----
 //
-// Up to kN = 16, 32 or 64 rows a tile (single tokens, a few drafted ones): no
+// Up to kN = 32 or 64 rows a tile (single tokens, a few drafted ones): no
 // pair, since half of its rows or more would be empty, and each CTA loads all 64
 // keys of a tile once for both products.
 //   S[64, 64] = Q K^T as above (M = 64: rows 16 w .. sit in lanes 32 w .. of TMEM).
-// With kN < 64 the 64 rows hold 64 / kN copies of Q, so that every softmax warp
-// finds its rows in its own lanes and takes kN of the 64 keys.
+// With kN = 32 the 64 rows hold two copies of Q, so that every softmax warp finds
+// its rows in its own lanes and takes kN of the 64 keys.
 //   O^T[128 b .. + 128, kN] += V^T P^T, b = 0 .. 3: the four M = 128 blocks of
 // dims take 4 kN columns, and V^T is the K tile read MN-major, so nothing is copied.
 // Warps (16): 0-3 softmax, 4-11 loaders, 12-13 half of QK's K-steps each, 14-15
 // two blocks of PV each.
 //
 // What bounds it: the loaders' conversion (~1.85 us a tile of 64 records by eight warps
-// at the register limit; with a third stage behind them, and Q in tensor memory to make
-// room for it, 64 x 16 took 62 us instead of 60), and for short rows the ~10 us until
-// the first scores and the partials' way through L2.  64 x 16 heads over up
-// to 4096 positions: 60 us (131 MB of records: 2.2 TB/s); 4 x 64 heads over up to 16384:
-// 36 us; one token, 16 heads, 500 positions: 14 us.
+// at the register limit), and for short rows the ~10 us until the first scores and the
+// partials' way through L2.  4 x 64 heads over up to 16384 positions: 36 us; 64 x 64
+// heads over 4096: 87 us.
 
 template <int kN>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
@@ -1671,12 +1671,18 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
 
 // ---- the few-row kernel ----
 //
-// Up to 16 rows a tile: the loaders' conversion bounds the time, so twelve of the 16
-// warps load, in tiles of 96 keys, and warps 0-3 do the rest.  Q lies in tensor memory
+// Up to 16 rows a tile: the loaders' conversion bounds the narrow kernel, so here twelve
+// of the 16 warps load, in tiles of 96 keys, and warps 0-3 do the rest.  Q lies in tensor memory
 // (288 columns, the A operand of S[64, 96] = Q K^T), which leaves shared memory to two
 // stages of 96 keys.  S holds four copies of the 16 rows, one in each warp's lanes; a
 // warp takes 24 of the keys.  Per tile: S read, maxima exchanged, P stored, then warp 0
 // issues the next QK, warps 1 and 2 two blocks of O^T += V^T P^T each.
+//
+// 64 x 16 heads over up to 4096 positions: 52 us (131 MB of records: 2.5 TB/s; 60 us with
+// eight loaders, tiles of 64 keys and Q in shared memory, 62 us with Q in tensor memory
+// and a third stage instead of more loaders); one token, 16 heads, 500 positions: 14 us.
+// Bound: ~2.4 us a tile of 96 keys, still the loaders, and ~18 us of start, partials and
+// merge.
 
 // QK of tile g, by warp 0.
 __device__ __forceinline__ void few_issue_qk(const AttendArgs& a, Misc* ms, uint64_t k0, uint32_t tmem, uint32_t g) {
@@ -2130,8 +2136,8 @@ paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
 // of rows (tokens x heads) of a sequence, since the lengths themselves are on the
 // device.  Any split is computed correctly by either.  Measured at 64 sequences of
 // 4096 positions (us): 64 rows 86 in a narrow tile of 64, 102 in the pair kernel; 96
-// rows 148 and 104; 128 rows 152 and 107; 16 rows 71, 73 and 77 in tiles of 16, 32 and
-// 64, 97 in the pair kernel.
+// rows 148 and 104; 128 rows 152 and 107; 16 rows 62 in the few-row kernel, 73 and 77 in
+// narrow tiles of 32 and 64, 97 in the pair kernel.
 static int narrow_rows(const smla_paged_attend_params& p) {
   if (p.num_heads > kCtaRows) return 0;
   const int64_t mean = (p.batch.n_rows * p.num_heads + p.batch.n_seqs - 1) / p.batch.n_seqs;
@@ -2150,7 +2156,7 @@ AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
   const int64_t coverage = int64_t(b.max_pages) * b.page_size;
   const int64_t most_tiles = coverage > 0 ? (coverage + kTileKeys - 1) / kTileKeys : 1;
   const int64_t row_tiles = (b.n_rows + tokens - 1) / tokens + (b.n_rows < b.n_seqs ? b.n_rows : int64_t(b.n_seqs));
-  plan.start_slots = plan.narrow ? kNarrowStart : kPairStart;
+  plan.start_slots = plan.narrow == 16 ? kFewStart : plan.narrow ? kNarrowStart : kPairStart;
   const int64_t slots = row_tiles * (most_tiles + plan.start_slots);
   int64_t workers = plan.narrow ? num_sms : num_sms / 2;
   if (slots < workers) workers = slots;
