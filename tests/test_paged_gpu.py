@@ -699,3 +699,76 @@ def test_attend_a_chunk_of_over_a_thousand_row_tiles():
     assert err.max() <= 0
     e = np.abs(lse.double().cpu().numpy()[rows] - ref_lse) - (a_lse + 2.0 ** -18 * (1 + np.abs(ref_lse).max()))
     assert e.max() <= 0
+
+
+# ---- tiles of few rows: empty sequences keep the mean number of rows at 16 or less ----
+
+EMPTY = [(0, 0)] * 60
+
+
+@pytest.mark.parametrize("page", [1, 20, 64])
+@pytest.mark.parametrize("heads,lens", [
+    (16, [(1, 95), (1, 96), (1, 97), (2, 192), (1, 1), (5, 3), (1, 700)]), (5, [(7, 1000), (3, 64), (1, 65), (40, 260)]),
+    (1, [(33, 33), (16, 500), (17, 1200)]), (16, [(1, 20000)]), (8, [(2, 129), (9, 4000)])])
+def test_few_rows(heads, lens, page):
+    c = Batch(lens + EMPTY, page, front=2, behind=1, page_pad=32)
+    c.table[torch.rand(c.table.shape, generator=gen(1)) < 0.05] = -1
+    for causal in (True, False):
+        q, sk, out, lse, st = attend(c, heads, causal=causal, sink=causal)
+        check(c, q, out, lse, 1 / 24, sk, causal)
+        assert st == 0
+
+
+def test_few_rows_sharp_softmax_and_odd_scales():
+    c = Batch([(3, 700), (1, 1500)] + EMPTY, 64, std=3.0)
+    for scale in (1.0, -0.3, 0.0):
+        q, sk, out, lse, _ = attend(c, 16, sm_scale=scale, sink=True)
+        check(c, q, out, lse, scale, sk, True)
+
+
+def test_few_rows_foreign_scales_round_once():
+    c = Batch([(3, 270), (1, 100)] + EMPTY, 16)
+    sc = torch.exp2(torch.rand(c.n_pages * 16, 4, generator=gen(4)) * 6 - 4).float().numpy()
+    c.rec[:, 512:528] = sc.view(np.uint8)
+    q, sk, out, lse, _ = attend(c, 16)
+    rows, ref, ref_lse, (a_out, a_lse) = reference_operands(c, q)
+    err = np.abs(out.double().cpu().numpy()[rows] - ref) - (a_out + 2.0 ** -8 * np.abs(ref))
+    assert err.max() <= 0
+    assert (np.abs(lse.double().cpu().numpy()[rows] - ref_lse) <= a_lse + 2.0 ** -18 * (1 + np.abs(ref_lse).max())).all()
+
+
+def test_few_rows_a_nan_query_row_stays_in_its_row():
+    c = Batch([(2, 100), (1, 300)] + EMPTY, 16)
+    q, _, want, want_lse, _ = attend(c, 16)
+    q2 = q.clone()
+    q2[1, 3, 17], q2[1, 5, 570] = float("nan"), float("inf")
+    _, _, out, lse, _ = attend(c, 16, q=q2)
+    assert torch.isnan(out[1, 3].float()).all() and torch.isnan(lse[1, 3])
+    keep = torch.ones(c.rows, 16, dtype=torch.bool)
+    keep[1, 3] = keep[1, 5] = False
+    assert torch.equal(out.cpu()[keep], want.cpu()[keep]) and torch.equal(lse.cpu()[keep], want_lse.cpu()[keep])
+
+
+def test_few_rows_many_launches_give_the_same_bits():
+    c = Batch([(1, 900), (2, 3000), (1, 50)] + EMPTY, 64)
+    q, _, want, want_lse, _ = attend(c, 16)
+    kv, q = c.cache(), q.to(DEV)
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    for _ in range(24):
+        flush.fill_(1)
+        out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+        smla.smla_paged_attend(q, kv, *c.dev(), 1 / 24, None, out, lse)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_few_rows_wait_timeout_sets_the_status_and_leaves_the_context_usable():
+    c = Batch([(1, 500), (2, 900)] + EMPTY, 64)
+    try:
+        smla.smla_set_wait_limit(20_000_000, stall_first_wait=True)
+        *_, st = attend(c, 16)
+        assert st & smla.STATUS_TIMEOUT
+    finally:
+        smla.smla_set_wait_limit(0)
+    q, sk, out, lse, st = attend(c, 16)
+    assert st == 0
+    check(c, q, out, lse, 1 / 24, sk, True)
