@@ -1659,6 +1659,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
       if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
     }
   }
+  cp_async_wait_all();  // (a loader whose wait gave up may have q on its way)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
