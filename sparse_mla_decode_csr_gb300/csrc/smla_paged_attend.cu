@@ -326,6 +326,21 @@ __device__ __forceinline__ bool warp_wait(Misc* ms, const AttendArgs& a, uint64_
   return __all_sync(0xffffffffu, wait_for(ms, a, bar, parity));
 }
 
+// The same for a warp that goes on in any case (its role ends with the last tile, also
+// after a wait that gave up).  Lanes may leave the wait's loop at different turns, and
+// what follows are accesses of tensor memory by the whole warp, so they meet here.
+__device__ __forceinline__ void meet_after(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
+  wait_for(ms, a, bar, parity);
+  __syncwarp();
+}
+
+// A barrier of some of the block's warps, which lanes may reach from branches of
+// their own: the instruction itself wants the warp converged.
+__device__ __forceinline__ void group_barrier(uint32_t id, uint32_t threads) {
+  __syncwarp();
+  named_barrier(id, threads);
+}
+
 // ---- the schedule ----
 
 // sum_{i < n} floor((g i + b) / 64) for g, b >= 0: the plain sum less the residues
@@ -681,7 +696,7 @@ __device__ __noinline__ void load_q_tmem(const AttendArgs& a, uint32_t buf, uint
       const int32_t j = threadIdx.x + 128 * i, m = j / kThird;
       st_shared_v4(buf + m * kQRowPitch + (j - m * kThird) * 16, v[third][i].x, v[third][i].y, v[third][i].z, v[third][i].w);
     }
-    named_barrier(1, 128);
+    group_barrier(1, 128);
 #pragma unroll 1
     for (int c = 0; c < kThird; c += 4) {
       uint32_t x[16];
@@ -692,7 +707,7 @@ __device__ __noinline__ void load_q_tmem(const AttendArgs& a, uint32_t buf, uint
       }
       tmem_st16(at + 4 * (third * kThird + c), x);
     }
-    named_barrier(1, 128);
+    group_barrier(1, 128);
   }
   tmem_wait_st();
   tc_fence_before();
@@ -1148,7 +1163,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   uint32_t g = 0;
   // (a wait that gives up does not end this role: its warps meet at named
   // barriers, so all of them run through every tile)
-  if (ms->stall) wait_for(ms, a, &ms->never, 0);
+  if (ms->stall) meet_after(ms, a, &ms->never, 0);
   while (units.next(a, u)) {
     const bool live = m < u.tokens * a.heads;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
@@ -1156,7 +1171,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
+      meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       uint32_t s[64];  // the two accumulators' 32 columns
       {
@@ -1194,7 +1209,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
 #pragma unroll
       for (int c = 1; c < 32; ++c) tm = fmaxf(tm, x[c]);
       ms->tmax[stage][warp * 32 + lane] = tm;
-      named_barrier(1 + (warp & 1), 64);
+      group_barrier(1 + (warp & 1), 64);
       tm = fmaxf(tm, ms->tmax[stage][(warp ^ 2) * 32 + lane]) * scale;
       const bool move = tm > ref + kMoveMargin;
       const float nref = move ? tm : ref;
@@ -1213,7 +1228,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
         p[c] = pack_bf16x2(y0, y1);  // P as the product's bf16 operand; the sum keeps f32
       }
       l = l * alpha + (sum0 + sum1);
-      if (g > 0) wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      if (g > 0) meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
       if (t > t0 && __any_sync(0xffffffffu, move)) {
         tc_fence_after();
 #pragma unroll 1
@@ -1237,9 +1252,9 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
     }
     // the unit's end: row sums of the two halves, then O
     ms->lsum[warp * 32 + lane] = l;
-    named_barrier(1 + (warp & 1), 64);
+    group_barrier(1 + (warp & 1), 64);
     l += ms->lsum[(warp ^ 2) * 32 + lane];
-    wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
     const bool whole = u.t0 == 0 && u.t1 == u.tiles;
     const int64_t part = 2 * int64_t(pair) + (u.t0 > 0 ? 0 : 1);
@@ -1261,10 +1276,10 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
 #pragma unroll 1
     for (int c = 0; c < 256; c += 16) {
       uint32_t o[16];
+      __syncwarp();  // (dead lanes skip the stores, and the load is the whole warp's)
       tmem_ld16(lane_base + c, o);
       tmem_wait_ld();
-      if (!live) continue;
-      if (whole) {
+      if (live && whole) {
         uint32_t v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -1272,7 +1287,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
                           : pack_bf16x2(__uint_as_float(o[2 * i]) * factor, __uint_as_float(o[2 * i + 1]) * factor);
         *reinterpret_cast<uint4*>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
         *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-      } else {
+      } else if (live) {
 #pragma unroll
         for (int i = 0; i < 16; i += 4)
           *reinterpret_cast<uint4*>(pdst + (c + i) * kPairRows) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -1398,7 +1413,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   units.start(a, ms);
   Unit u;
   uint32_t g = 0;
-  if (ms->stall) wait_for(ms, a, &ms->never, 0);
+  if (ms->stall) meet_after(ms, a, &ms->never, 0);
   while (units.next_inline(a, u)) {
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const bool live = mine && m < rows;
@@ -1406,7 +1421,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
     float ref = -INFINITY, l = 0.f;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
+      meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       float x[kKeys];
       const uint32_t s_at = lane_base + kTmemS + 128 * stage + kKeys * slice;
@@ -1439,7 +1454,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       for (int c = 1; c < kKeys; ++c) tm = fmaxf(tm, x[c]);
       if (kCopies > 1) {
         ms->tmax[stage][warp * 32 + lane] = tm;
-        named_barrier(1, 128);
+        group_barrier(1, 128);
 #pragma unroll
         for (int k = 1; k < kCopies; ++k) tm = fmaxf(tm, ms->tmax[stage][(warp ^ (k * (kN / 16))) * 32 + lane]);
       }
@@ -1450,6 +1465,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       const float alpha = move ? ex2(ref - use) : 1.f;
       ref = nref;
       if (mine && slice == 0) ms->alpha[stage][m] = alpha;
+      __syncwarp();
       const bool moved = named_barrier_or(1, 128, move);
       uint32_t p[kKeys / 2];
       float sum0 = 0.f, sum1 = 0.f;
@@ -1463,7 +1479,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
         p[c] = pack_bf16x2(y0, y1);
       }
       l = l * alpha + (sum0 + sum1);
-      if (g > 0) wait_for(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
+      if (g > 0) meet_after(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
       if (t > t0 && moved) {
         tc_fence_after();
 #pragma unroll 1
@@ -1494,7 +1510,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
     const int64_t part = 2 * int64_t(worker) + (t0 > 0 ? 0 : 1);
     if (kCopies > 1) {
       ms->lsum[warp * 32 + lane] = l;
-      named_barrier(1, 128);
+      group_barrier(1, 128);
       l = 0.f;
 #pragma unroll
       for (int k = 0; k < kCopies; ++k) l += ms->lsum[(warp ^ (k * (kN / 16))) * 32 + lane];
@@ -1511,8 +1527,8 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       }
       ms->factor[m] = factor;
     }
-    named_barrier(1, 128);
-    wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    group_barrier(1, 128);
+    meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
     // a lane has dim 128 b + 32 warp + lane of every row
     const int32_t dim = 32 * warp + lane;
@@ -1724,7 +1740,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
   Unit u;
   uint32_t g = 0;
   // (a wait that gives up does not end this role: its warps meet at named barriers)
-  if (ms->stall) wait_for(ms, a, &ms->never, 0);
+  if (ms->stall) meet_after(ms, a, &ms->never, 0);
   while (units.next_inline(a, u)) {
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const int32_t key0 = t0 * kTileKeys, stop = t1 * kTileKeys, end = min(u.end, stop);
@@ -1733,12 +1749,11 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
     float ref = -INFINITY, l = 0.f;
     // q (every warp has seen the last QK and PV of the unit before done)
     load_q_tmem(a, base + L::kOffP, lane_base + kTmemQFew, u.row0, rows);
-    named_barrier(1, 128);
+    group_barrier(1, 128);
     if (warp == 0) few_issue_qk(a, ms, k0, tmem, g);
     for (int32_t key = key0; key < stop; key += L::kKeys, ++g) {
       const uint32_t stage = g & 1;
-      wait_for(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
-      __syncwarp();
+      meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       float x[kKeys];
       {
@@ -1768,7 +1783,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
 #pragma unroll
       for (int c = 1; c < kKeys; ++c) tm = fmaxf(tm, x[c]);
       ms->tmax[stage][warp * 32 + lane] = tm;
-      named_barrier(1, 128);
+      group_barrier(1, 128);
 #pragma unroll
       for (int k = 1; k < 4; ++k) tm = fmaxf(tm, ms->tmax[stage][(warp ^ k) * 32 + lane]);
       tm *= scale;
@@ -1789,8 +1804,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
         p[c] = pack_bf16x2(y0, y1);
       }
       l = l * alpha + (sum0 + sum1);
-      if (g > 0) wait_for(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
-      __syncwarp();
+      if (g > 0) meet_after(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
       if (key > key0 && __any_sync(0xffffffffu, move)) {
         tc_fence_after();
 #pragma unroll 1
@@ -1815,7 +1829,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
       }
       fence_proxy_async_smem();
       tc_fence_before();
-      named_barrier(2, 128);  // P is stored, S read
+      group_barrier(2, 128);  // P is stored, S read
       if (warp == 0) {
         if (key + L::kKeys < stop) few_issue_qk(a, ms, k0, tmem, g + 1);
       } else if (warp < 3) {
@@ -1837,7 +1851,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
     const bool whole = t0 == 0 && t1 == u.tiles;
     const int64_t part = 2 * int64_t(worker) + (t0 > 0 ? 0 : 1);
     ms->lsum[warp * 32 + lane] = l;
-    named_barrier(1, 128);
+    group_barrier(1, 128);
     l = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) l += ms->lsum[(warp ^ k) * 32 + lane];
@@ -1853,8 +1867,8 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
       }
       ms->factor[m] = factor;
     }
-    named_barrier(1, 128);
-    wait_for(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    group_barrier(1, 128);
+    meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
     // a lane has dim 128 b + 32 warp + lane of every row
     const int32_t dim = 32 * warp + lane;
