@@ -394,8 +394,10 @@ typedef struct smla_paged_attend_params {
 
 /* Workspace bytes of smla_paged_attend for these params on the current device
  * (0 for invalid params and empty batches).  It depends on the sizes alone
- * (num_heads, n_rows, n_seqs, page_size, max_pages), needs no initial contents
- * and is 256-byte aligned.  Calls that may overlap on the GPU need workspaces
+ * (num_heads, n_rows, n_seqs, page_size, max_pages) and never grows when n_rows,
+ * n_seqs, page_size or max_pages shrinks: a workspace for a server's largest batch
+ * serves all of its calls of as many heads.  It needs no initial contents and is
+ * 256-byte aligned.  Calls that may overlap on the GPU need workspaces
  * of their own. */
 size_t smla_paged_attend_workspace_size(const smla_paged_attend_params* params);
 

@@ -467,7 +467,8 @@ def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: 
 
 
 def smla_paged_attend_workspace_size(n_rows: int, num_heads: int, n_seqs: int, page_size: int, max_pages: int) -> int:
-    """Workspace bytes of smla_paged_attend for these sizes on the current device."""
+    """Workspace bytes of smla_paged_attend for these sizes on the current device.
+    They never grow when n_rows, n_seqs, page_size or max_pages shrinks."""
     p = PagedAttendParams()
     p.num_heads = int(num_heads)
     p.batch.n_rows, p.batch.n_seqs = int(n_rows), int(n_seqs)

@@ -2161,11 +2161,11 @@ static int narrow_rows(const smla_paged_attend_params& p) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
+// The plan of one kernel (narrow as in AttendPlan).
+static AttendPlan plan_of_kernel(const smla_paged_attend_params& p, int num_sms, int narrow) {
   AttendPlan plan{};
   const smla_paged_batch& b = p.batch;
-  if (b.n_rows <= 0 || b.n_seqs <= 0) return plan;
-  plan.narrow = narrow_rows(p);
+  plan.narrow = narrow;
   plan.part_rows = plan.narrow ? kCtaRows : kPairRows;
   const int64_t tokens = (plan.narrow ? plan.narrow : kPairRows) / p.num_heads;
   const int64_t coverage = int64_t(b.max_pages) * b.page_size;
@@ -2181,6 +2181,20 @@ AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
   plan.ml_off = (int64_t(plan.workers) * 16 + 255) & ~int64_t(255);
   plan.o_off = plan.ml_off + ((int64_t(plan.workers) * 2 * plan.part_rows * 8 + 255) & ~int64_t(255));
   plan.total = plan.o_off + int64_t(plan.workers) * 2 * plan.part_rows * kLatent * 4;
+  return plan;
+}
+
+// The workspace is as large as the largest that any kernel would take for these sizes.
+// Each kernel's grows with the rows, sequences and pages, so theirs does too, and a
+// workspace for a batch serves every smaller one, whichever kernel that gets.
+AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
+  if (p.batch.n_rows <= 0 || p.batch.n_seqs <= 0) return AttendPlan{};
+  AttendPlan plan = plan_of_kernel(p, num_sms, narrow_rows(p));
+  for (const int narrow : {0, 16, 32, 64}) {
+    if (narrow != 0 && narrow < p.num_heads) continue;
+    const int64_t total = plan_of_kernel(p, num_sms, narrow).total;
+    if (total > plan.total) plan.total = total;
+  }
   return plan;
 }
 

@@ -1,0 +1,49 @@
+"""Edges of the paged cache's calls on the GPU: workspaces of other batches, infinite
+sinks, queries and latents, empty sequences in between, and what hidden keys and bad
+queries do in each of the attend kernels."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import sparse_mla_decode_csr_gb300 as smla
+from smla_testlib import bits
+from test_paged_gpu import DEV, REC, Batch, attend, check, expect_records, gen, reference_operands, unpack
+
+pytestmark = pytest.mark.gpu
+
+# heads of single tokens that take each kernel: the few-row kernel, narrow tiles of 32
+# and 64 rows, pairs of CTAs
+KERNELS = {"few": 16, "narrow32": 32, "narrow64": 64, "pair": 128}
+
+
+# ---- workspaces ----
+
+
+@pytest.mark.parametrize("heads", [1, 16, 40, 128])
+def test_the_workspace_never_grows_when_a_size_shrinks(heads):
+    base = dict(n_rows=4096, n_seqs=64, page_size=64, max_pages=128)
+    for name, sizes in (("n_rows", [1, 2, 3, 31, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300, 512, 1000, 2048, 4096, 9999]),
+                        ("n_seqs", [1, 2, 3, 16, 63, 64, 65, 100, 1000, 4096, 9000]),
+                        ("max_pages", [0, 1, 2, 5, 100, 5000]), ("page_size", [1, 3, 64, 100])):
+        for rows in (1, 30, 4096):
+            got = [smla.smla_paged_attend_workspace_size(**{**base, "n_rows": rows, "num_heads": heads, name: n})
+                   for n in sizes]
+            assert got == sorted(got) and got[0] > 0, (name, rows)
+
+
+@pytest.mark.parametrize("heads", [16, 64])
+def test_a_step_runs_in_the_workspace_of_the_longest_chunk(heads):
+    # a server's workspace: sized once for 2048 rows of 64 sequences
+    n = smla.smla_paged_attend_workspace_size(2048, heads, 64, 64, 128)
+    ws = torch.full((n + 4096,), 0xAB, dtype=torch.uint8, device=DEV)
+    for lens in ([(1, 70 + 9 * b) for b in range(64)], [(2, 64 + b) for b in range(40)], [(1, 5000)], [(90, 90)] * 3):
+        c = Batch(lens, 64)
+        c.table = torch.nn.functional.pad(c.table, (0, 128 - c.table.shape[1]), value=-1)
+        q = torch.randn(c.rows, heads, 576, generator=gen(1)).to(torch.bfloat16)
+        out = torch.empty(c.rows, heads, 512, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(c.rows, heads, device=DEV)
+        smla.smla_paged_attend(q.to(DEV), c.cache(), *c.dev(), 1 / 24, None, out, lse, workspace_tensor=ws[:n])
+        check(c, q, out, lse, 1 / 24, None, True)
+    assert (ws[n:] == 0xAB).all()
