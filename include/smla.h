@@ -340,10 +340,12 @@ typedef struct smla_paged_batch {
 } smla_paged_batch;
 
 /* Writes every token row's record at its position: the rule of
- * smla_pack_records (bit for bit for bf16 inputs) for latent and rope of type
- * dtype, values in f32 and rope rounded to bf16 (nearest even).  A block's
- * largest finite magnitude bounds its scale (an infinity is stored as +-448
- * times the scale of the largest f32); a NaN latent is stored as the NaN code.
+ * smla_pack_records (bit for bit for finite bf16 inputs) for latent and rope of
+ * type dtype, values in f32 and rope rounded to bf16 (nearest even).  A NaN
+ * latent is stored as the NaN code and does not enter its block's scale.  An
+ * infinity counts as the largest f32 there: the block's scale becomes 2^120,
+ * the infinity is stored as +-448 times that (and read back as +-inf), and the
+ * block's values up to 2^110 become zeros of their sign.
  * latent [n_rows][latent_stride] (512 used), rope [n_rows][rope_stride] (64
  * used), 16-byte aligned, strides multiples of 16 bytes.  The rows' positions
  * have to lie in different slots: of two rows that a block table sends to one

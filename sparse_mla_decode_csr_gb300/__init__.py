@@ -450,7 +450,8 @@ def smla_paged_write(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.T
     position p lives in page block_table[b, p // page_size].  Rows whose page id
     is negative are skipped; ids >= n_pages and positions past the table are
     skipped and set STATUS_INDEX_OOB.  The rows' positions must lie in different
-    slots.  See include/smla.h."""
+    slots.  An infinite latent takes its whole block of 128 values to the scale
+    2^120, where ordinary values become zero.  See include/smla.h."""
     _paged_copy("smla_paged_write", _write_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
 

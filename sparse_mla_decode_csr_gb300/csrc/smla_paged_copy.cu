@@ -78,7 +78,8 @@ __device__ __forceinline__ uint4 pack(const float (&x)[Elem<kDtype>::kPer]) {
 }
 
 // Scale of a block with largest magnitude amax, and its reciprocal: the
-// smallest power of two that is not below max(amax, 1e-4) / 448.
+// smallest power of two that is not below max(amax, 1e-4) / 448.  (An infinite amax
+// counts as the largest f32, so that the reciprocal stays a normal power of two.)
 __device__ __forceinline__ float block_scale(float amax, float* inv) {
   const uint32_t b = __float_as_uint(fminf(fmaxf(amax, 1e-4f), FLT_MAX) / 448.0f);
   const uint32_t e = (b >> 23) + ((b & 0x7FFFFFu) ? 1u : 0u);

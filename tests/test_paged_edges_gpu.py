@@ -47,3 +47,46 @@ def test_a_step_runs_in_the_workspace_of_the_longest_chunk(heads):
         smla.smla_paged_attend(q.to(DEV), c.cache(), *c.dev(), 1 / 24, None, out, lse, workspace_tensor=ws[:n])
         check(c, q, out, lse, 1 / 24, None, True)
     assert (ws[n:] == 0xAB).all()
+
+
+# ---- latents that are not finite ----
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_an_infinite_latent_takes_its_blocks_scale_and_no_other(dtype):
+    # scale 2^120: +-inf saturates at +-448 (read back: beyond the largest f32), values up
+    # to 2^110 (half the least code 2^-9) become zeros of their sign, larger ones are codes
+    kind = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[dtype]
+    lat = (torch.randn(4, 512, generator=gen(3)) * 8).to(kind)
+    lat[1, 130], lat[1, 131] = float("inf"), -float("inf")
+    lat[2, 300] = float("inf")
+    lat[3, 17] = float("nan")
+    if dtype != "f16":
+        lat[1, 140], lat[1, 141] = 2.0 ** 127, -(2.0 ** 112)
+    block = lat[1, 128:256].float()
+    kv = torch.zeros(1, 4, REC, dtype=torch.uint8, device=DEV)
+    table, cu = torch.zeros(1, 1, dtype=torch.int32, device=DEV), torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    sl = torch.tensor([4], dtype=torch.int32, device=DEV)
+    smla.smla_paged_write(lat.to(DEV), torch.zeros(4, 64, dtype=kind, device=DEV), kv, table, cu, sl)
+    rec = kv.cpu().numpy()[0]
+    scale = rec[:, 512:528].copy().view(np.float32)
+    assert scale[1, 1] == 2.0 ** 120 and scale[2, 2] == 2.0 ** 120
+    codes = oracle.e4m3_table()[rec[1, 128:256]]
+    expect = oracle.e4m3_table()[np.asarray(oracle.e4m3_encode_rne(
+        torch.where(torch.isinf(block), torch.zeros(()), block).double().numpy() / 2.0 ** 120), np.uint8)]
+    expect[2], expect[3] = 448.0, -448.0
+    assert np.array_equal(codes, expect) and np.count_nonzero(codes) == (2 if dtype == "f16" else 4)
+    zero = codes == 0
+    assert np.array_equal(rec[1, 128:256][zero] >> 7, (block.numpy()[zero] < 0).astype(np.uint8))
+    assert rec[3, 17] & 0x7F == 0x7F
+    # every other block is as if nothing had been there
+    want = expect_records(torch.where(torch.isfinite(lat), lat, 0.0), torch.zeros(4, 64))
+    for r in range(4):
+        for i in range(4):
+            if (r, i) not in ((1, 1), (2, 2)):
+                keep = [d for d in range(128 * i, 128 * i + 128) if (r, d) != (3, 17)]
+                assert np.array_equal(rec[r, keep], want[r, keep])
+                assert np.array_equal(rec[r, 512 + 4 * i:516 + 4 * i], want[r, 512 + 4 * i:516 + 4 * i])
+    back, rope = torch.empty(4, 512, device=DEV), torch.empty(4, 64, device=DEV)
+    smla.smla_paged_read(kv, table, cu, sl, back, rope)
+    assert back[1, 130] == float("inf") and back[1, 131] == -float("inf") and torch.isnan(back[3, 17])
