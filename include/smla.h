@@ -367,7 +367,8 @@ int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_
  * sequence b at position p, the visible keys are the unmasked positions
  * t <= p (causal = 1) or t < seq_lens[b] (causal = 0); with k_t, s_t, the sink,
  * out and lse as in smla_decode.  A row without a visible key gives out = 0 and
- * lse = -inf.  A visible record whose latent holds a value that is not finite
+ * lse = -inf.  A sink of +inf gives out = 0 (unless the row is NaN), one of -inf
+ * changes nothing.  A visible record whose latent holds a value that is not finite
  * (a NaN code, a scale that is not finite) makes the row's out and lse NaN;
  * what a row may not see never reaches it.
  *

@@ -1136,6 +1136,14 @@ __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, ui
   }
 }
 
+// Output factor and LSE of a row (finish_head_v) with the sink of its head.  A sink of
+// +inf holds all of the weight: out = 0, where inf - inf would give NaN.
+__device__ __forceinline__ void finish_row(const AttendArgs& a, int32_t head, float m, float l, float* factor, float* lse) {
+  const float sink = a.sink != nullptr ? __ldg(a.sink + head) : 0.f;
+  finish_head_v(m, l, a.sink != nullptr, sink, factor, lse);
+  if (sink == INFINITY && l >= 0.f) *factor = 0.f;
+}
+
 // The last part of a row tile: the merge kernel joins the parts from the worker
 // that holds its first key tile up to this one.
 __device__ __noinline__ void name_merge(const AttendArgs& a, const Misc* ms, int32_t worker, const Unit& u) {
@@ -1268,7 +1276,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
     }
     if (whole) {
       float lse;
-      finish_head_v(ref, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+      finish_row(a, head, ref, l, &factor, &lse);
       if (live && half == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
     }
     uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 256 * half;
@@ -1519,7 +1527,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       float factor = 1.f;
       if (whole) {
         float lse;
-        finish_head_v(ref, l, a.sink != nullptr, a.sink != nullptr && live ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+        finish_row(a, head, ref, l, &factor, &lse);
         if (live && a.lse) a.lse[(int64_t(u.row0) + tok) * a.heads + head] = lse;
       } else if (live) {
         a.ml_part[(part * a.part_rows + m) * 2] = ref;
@@ -1859,7 +1867,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
       float factor = 1.f;
       if (whole) {
         float lse;
-        finish_head_v(ref, l, a.sink != nullptr, a.sink != nullptr && live ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+        finish_row(a, head, ref, l, &factor, &lse);
         if (live && a.lse) a.lse[(int64_t(u.row0) + tok) * a.heads + head] = lse;
       } else if (live) {
         a.ml_part[(part * a.part_rows + m) * 2] = ref;
@@ -2049,7 +2057,7 @@ __global__ void __launch_bounds__(kGroups == 1 ? 256 : 128 * kGroups) paged_merg
   const int32_t tok = m / a.heads, head = m - tok * a.heads;
   const int64_t tok_row = int64_t(job.y) + tok;
   float factor, lse;
-  finish_head_v(mx, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+  finish_row(a, head, mx, l, &factor, &lse);
   if (lane == 0 && quarter == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
   uint2 v = make_uint2(pack_bf16x2(o.x * factor, o.y * factor), pack_bf16x2(o.z * factor, o.w * factor));
   if (l == 0.f) v = make_uint2(0, 0);
@@ -2132,7 +2140,7 @@ paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
   const int32_t tok = m / a.heads, head = m - tok * a.heads;
   const int64_t tok_row = int64_t(job.y) + tok;
   float factor, lse;
-  finish_head_v(mx, l, a.sink != nullptr, a.sink != nullptr ? __ldg(a.sink + head) : 0.f, &factor, &lse);
+  finish_row(a, head, mx, l, &factor, &lse);
   if (at == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
   uint32_t v[kDims / 2];
 #pragma unroll

@@ -90,3 +90,33 @@ def test_an_infinite_latent_takes_its_blocks_scale_and_no_other(dtype):
     back, rope = torch.empty(4, 512, device=DEV), torch.empty(4, 64, device=DEV)
     smla.smla_paged_read(kv, table, cu, sl, back, rope)
     assert back[1, 130] == float("inf") and back[1, 131] == -float("inf") and torch.isnan(back[3, 17])
+
+
+# ---- sinks, queries and scores that are not finite ----
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_sinks_that_are_not_finite(name):
+    # one row shared between workers, one finished by its own, one without a key
+    heads = KERNELS[name]
+    c = Batch([(1, 3000), (1, 40), (1, 0)], 64)
+    q = torch.randn(c.rows, heads, 576, generator=gen(5)).to(torch.bfloat16)
+    sink = torch.randn(heads, generator=gen(6))
+    sink[1], sink[3], sink[5] = float("inf"), -float("inf"), float("nan")
+    kv, dev = c.cache(), c.dev()
+    got = []
+    for sk in (sink, torch.where(torch.isfinite(sink), sink, -1e30), None):
+        out = torch.empty(c.rows, heads, 512, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(c.rows, heads, device=DEV)
+        smla.smla_paged_attend(q.to(DEV), kv, *dev, 1 / 24, None if sk is None else sk.to(DEV), out, lse)
+        got.append((out.cpu(), lse.cpu()))
+    (out, lse), (fine, fine_lse), (plain, _) = got
+    assert torch.equal(lse, fine_lse)  # no sink enters the LSE
+    assert (out[:, 1] == 0).all()
+    # a sink of -inf is a weight of zero: as without one, each rounded once to bf16
+    assert torch.equal(out[:, 3], fine[:, 3])
+    assert ((out[:2, 3].float() - plain[:2, 3].float()).abs() <= 2 * 2.0 ** -8 * plain[:2, 3].float().abs()).all()
+    assert torch.isnan(out[:2, 5].float()).all()
+    assert (out[2, [0, 1, 2, 3, 4]] == 0).all() and torch.isneginf(lse[2]).all()
+    rest = [h for h in range(heads) if h not in (1, 3, 5)]
+    assert torch.equal(out[:, rest], fine[:, rest])
