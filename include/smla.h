@@ -367,10 +367,13 @@ int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_
  * sequence b at position p, the visible keys are the unmasked positions
  * t <= p (causal = 1) or t < seq_lens[b] (causal = 0); with k_t, s_t, the sink,
  * out and lse as in smla_decode.  A row without a visible key gives out = 0 and
- * lse = -inf.  A sink of +inf gives out = 0 (unless the row is NaN), one of -inf
- * changes nothing.  A visible record whose latent holds a value that is not finite
- * (a NaN code, a scale that is not finite) makes the row's out and lse NaN;
- * what a row may not see never reaches it.
+ * lse = -inf.  A visible score of -inf (q or a key's rope infinite) weighs
+ * nothing: a row that has no other ends like a row without a visible key.  A
+ * score of +inf or NaN makes the row's out and lse NaN.  A sink of +inf gives
+ * out = 0 (unless the row is NaN), one of -inf changes nothing.  A visible
+ * record whose latent holds a value that is not finite (a NaN code, a scale that
+ * is not finite) makes the row's out and lse NaN; what a row may not see never
+ * reaches it.
  *
  * q bf16 [n_rows][num_heads][576] and out bf16 [n_rows][num_heads][512] with
  * strides as in smla_decode (16-byte aligned, strides multiples of 8); sink f32

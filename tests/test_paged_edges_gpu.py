@@ -120,3 +120,51 @@ def test_sinks_that_are_not_finite(name):
     assert (out[2, [0, 1, 2, 3, 4]] == 0).all() and torch.isneginf(lse[2]).all()
     rest = [h for h in range(heads) if h not in (1, 3, 5)]
     assert torch.equal(out[:, rest], fine[:, rest])
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_infinite_queries_and_ropes_follow_their_scores(name):
+    # dim 40 of every key is -1 and dim 41 is +1 or -1: q = +inf there gives scores of
+    # -inf alone (weights of zero, as without a key), q = -inf scores of +inf (NaN), +inf at
+    # dim 41 both (NaN).  Masked pages hold zeros in the tiles, whose product with an
+    # infinity is NaN: the mask has to keep it out
+    heads = KERNELS[name]
+    c = Batch([(1, 3000), (1, 40)], 64)
+    c.rec[:, 40], c.rec[:, 41] = 0xB8, np.where(np.arange(c.rec.shape[0]) % 2, 0xB8, 0x38)
+    c.rec[:, 512:528] = np.ones(4, np.float32).view(np.uint8)
+    c.table[0, 5] = c.table[0, -1] = -1
+    inf = float("inf")
+    q, _, want, want_lse, _ = attend(c, heads, sink=True)
+    bad = q.clone()
+    bad[:, 3, 40], bad[:, 5, 40], bad[:, 7, 41] = inf, -inf, inf
+    _, _, out, lse, _ = attend(c, heads, q=bad, sink=True)
+    assert (out[:, 3] == 0).all() and torch.isneginf(lse[:, 3]).all()
+    for h in (5, 7):
+        assert torch.isnan(out[:, h].float()).all() and torch.isnan(lse[:, h]).all()
+    rest = [h for h in range(heads) if h not in (3, 5, 7)]
+    assert torch.equal(out[:, rest], want[:, rest]) and torch.equal(lse[:, rest], want_lse[:, rest])
+    # an infinite rope of single keys: heads whose q is negative there see scores of -inf,
+    # which drop those keys, the others +inf
+    q[:, :, 560] = torch.where(torch.arange(heads) % 2 == 0, -1.0, 1.0)
+    keys = [c.slot(0, 2), c.slot(0, 2990 - 64), c.slot(1, 39)]
+    c.rec[keys, 528 + 2 * (560 - 512):530 + 2 * (560 - 512)] = np.array([0x7F80], np.uint16).view(np.uint8)
+    _, sk, out, lse, _ = attend(c, heads, q=q, sink=True)
+    assert torch.isnan(out[:, 1::2].float()).all() and torch.isnan(lse[:, 1::2]).all()
+    # the even heads against a cache where those keys' pages hold them no more: 64-bit
+    # softmax over the finite scores
+    lat, _, rope = unpack(c.rec)
+    key = np.concatenate([lat, rope], 1)
+    for r, b, p in c.positions():
+        ids = [c.slot(b, t) for t in range(p + 1) if c.slot(b, t) >= 0]
+        ids = np.array([i for i in ids if i not in keys])
+        s = q[r, ::2].double().numpy() @ key[ids].T / 24
+        m = s.max(1, keepdims=True)
+        w = np.exp(s - m)
+        den = w.sum(1, keepdims=True) + np.exp(sk[::2].double().numpy()[:, None] - m)
+        ref, spread = (w / den) @ key[ids, :512], (w / den) @ np.abs(key[ids, :512])
+        # f32 dot products of 576 terms (doubled for slack), p and the result as bf16
+        ds = 2 * 576 * 2.0 ** -24 * (np.abs(q[r, ::2].double().numpy()) @ np.abs(key[ids]).T).max() / 24
+        err = np.abs(out[r, ::2].double().cpu().numpy() - ref)
+        assert (err <= (2.0 ** -8 + 2 * ds) * spread + 2.0 ** -8 * np.abs(ref)).all()
+        e = np.abs(lse[r, ::2].double().cpu().numpy() - (m[:, 0] + np.log(w.sum(1))))
+        assert (e <= ds + 2.0 ** -18 * (1 + np.abs(m[:, 0]) + np.log(len(ids)))).all()
