@@ -378,7 +378,8 @@ int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_
  * q bf16 [n_rows][num_heads][576] and out bf16 [n_rows][num_heads][512] with
  * strides as in smla_decode (16-byte aligned, strides multiples of 8); sink f32
  * [num_heads] or NULL; lse f32 [n_rows][num_heads] contiguous or NULL;
- * num_heads in [1, SMLA_PAGED_MAX_HEADS].  The records of the token rows
+ * num_heads in [1, SMLA_PAGED_MAX_HEADS]; sm_scale * log2(e) finite in f32
+ * (SMLA_ERR_SHAPE otherwise).  The records of the token rows
  * themselves are read from the cache like all others: write them first.
  * Accuracy as the bf16 tensor-core kernel of smla_decode (k and v enter the
  * products as bf16(e4m3 * scale), exact for scales 2^-116 .. 2^7; p is rounded

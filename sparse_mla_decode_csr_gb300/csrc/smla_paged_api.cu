@@ -52,7 +52,9 @@ int check_copy(const smla_paged_batch* b, const void* latent, int64_t latent_str
 
 int check_attend(const smla_paged_attend_params* p, bool* empty) {
   if (p == nullptr) return SMLA_ERR_NULL;
-  if (p->num_heads < 1 || p->num_heads > SMLA_PAGED_MAX_HEADS || !std::isfinite(p->sm_scale)) return SMLA_ERR_SHAPE;
+  // (the kernels scale by sm_scale * log2(e) in f32: an infinite factor would make 0 * inf of scores of 0)
+  if (p->num_heads < 1 || p->num_heads > SMLA_PAGED_MAX_HEADS || !std::isfinite(p->sm_scale * kLog2e))
+    return SMLA_ERR_SHAPE;
   int rc = check_batch(&p->batch, empty);
   if (rc != SMLA_OK || *empty) return rc;
   if (!p->q || !p->out) return SMLA_ERR_NULL;
