@@ -168,3 +168,55 @@ def test_infinite_queries_and_ropes_follow_their_scores(name):
         assert (err <= (2.0 ** -8 + 2 * ds) * spread + 2.0 ** -8 * np.abs(ref)).all()
         e = np.abs(lse[r, ::2].double().cpu().numpy() - (m[:, 0] + np.log(w.sum(1))))
         assert (e <= ds + 2.0 ** -18 * (1 + np.abs(m[:, 0]) + np.log(len(ids)))).all()
+
+
+# ---- empty sequences in between ----
+
+
+def ms_of(call):
+    call()
+    torch.cuda.synchronize()
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ev[0].record()
+    call()
+    ev[1].record()
+    torch.cuda.synchronize()
+    return ev[0].elapsed_time(ev[1])
+
+
+def with_gap(first, gap, rest):
+    """cu_rows, seq_lens and block table (one page a sequence, -1 for none) of sequences of
+    (rows, length, page), `gap` empty ones behind the `first`."""
+    seqs = list(first) + list(rest)
+    rows = torch.tensor([n for n, _, _ in seqs], dtype=torch.int32)
+    k = len(first)
+    n = torch.cat([rows[:k], torch.zeros(gap, dtype=torch.int32), rows[k:]])
+    cu = torch.cat([torch.zeros(1, dtype=torch.int32), n.cumsum(0, dtype=torch.int32)])
+    sl, table = torch.zeros(len(n), dtype=torch.int32), torch.full((len(n), 1), -1, dtype=torch.int32)
+    at = list(range(k)) + list(range(k + gap, k + gap + len(rest)))
+    sl[at] = torch.tensor([s for _, s, _ in seqs], dtype=torch.int32)
+    table[at, 0] = torch.tensor([p for _, _, p in seqs], dtype=torch.int32)
+    return table.to(DEV), cu.to(DEV), sl.to(DEV)
+
+
+@pytest.mark.parametrize("gap", [0, 1, 2, 33, 1 << 20])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_read_finds_rows_behind_empty_sequences(dtype, gap):
+    # row 2432 of 16-bit reads shares its warp with the first row behind the gap
+    page = 2500
+    g = gen(2)
+    lat = torch.randn(3 * page, 512, generator=g).to(torch.bfloat16)
+    rope = torch.randn(3 * page, 64, generator=g).to(torch.bfloat16)
+    rec = oracle.pack_records(bits(lat), bits(rope))
+    kv = torch.from_numpy(rec).view(3, page, REC).to(DEV)
+    table, cu, sl = with_gap([(2433, 2440, 1)], gap, [(1, 7, 2), (3, 3, 0)])
+    kind = torch.bfloat16 if dtype == "bf16" else torch.float32
+    out = torch.full((2440, 512), 7.0, dtype=kind, device=DEV)
+    out_rope = torch.full((2440, 64), 7.0, dtype=kind, device=DEV)
+    ms = ms_of(lambda: smla.smla_paged_read(kv, table, cu, sl, out, out_rope))
+    slots = [page + 7 + i for i in range(2433)] + [2 * page + 6, 0, 1, 2]
+    vals, _, rp = unpack(rec[slots])
+    assert torch.equal(out[:2437].cpu(), torch.from_numpy(vals).to(kind))
+    assert torch.equal(out_rope[:2437].cpu(), torch.from_numpy(rp).to(kind))
+    assert (out[2437:] == 7.0).all() and (out_rope[2437:] == 7.0).all()
+    assert ms < 2.0, ms  # some 20 us; one load after the other through 2^20 sequences: 72 ms
