@@ -8,7 +8,7 @@ import torch
 
 import oracle
 import sparse_mla_decode_csr_gb300 as smla
-from smla_testlib import bits
+from smla_testlib import allowance, bits
 from test_paged_gpu import DEV, REC, Batch, attend, check, expect_records, gen, reference_operands, unpack
 
 pytestmark = pytest.mark.gpu
@@ -220,3 +220,58 @@ def test_a_read_finds_rows_behind_empty_sequences(dtype, gap):
     assert torch.equal(out_rope[:2437].cpu(), torch.from_numpy(rp).to(kind))
     assert (out[2437:] == 7.0).all() and (out_rope[2437:] == 7.0).all()
     assert ms < 2.0, ms  # some 20 us; one load after the other through 2^20 sequences: 72 ms
+
+
+@pytest.mark.parametrize("gap", [1, 2, 3, 31, 32, 33, 1000, 1 << 16])
+@pytest.mark.parametrize("heads,rows", [(4, 3), (64, 40), (128, 2), (16, 300)])
+def test_attend_goes_past_empty_sequences(heads, rows, gap):
+    # several row tiles a worker, so that workers go from one side of the gap to the
+    # other; the same rows without the gap, of which the oracle checks a sample
+    page = 1024
+    c = Batch([(rows, 1024)] * 3, page, spare_pages=0)
+    kv = c.cache()
+    pages = [int(p) for p in c.table[:, 0]]
+    first, rest = [(rows, 1000, pages[0]), (rows, 700, pages[1])], [(rows - 1, 900, pages[2])]
+    n = 3 * rows - 1
+    q = torch.randn(n, heads, 576, generator=gen(7)).to(torch.bfloat16)
+    got, took = [], []
+    for g in (0, gap):
+        table, cu, sl = with_gap(first, g, rest)
+        out = torch.empty(n, heads, 512, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(n, heads, device=DEV)
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        qd = q.to(DEV)
+        took.append(ms_of(lambda: smla.smla_paged_attend(qd, kv, table, cu, sl, 1 / 24, None, out, lse, status=st)))
+        assert int(st) == 0
+        got.append((out.cpu(), lse.cpu()))
+    c.lens = [(rows, 1000), (rows, 700), (rows - 1, 900)]
+    picked = [x for i, x in enumerate((r, b, p) for b, (k, s) in enumerate(c.lens) for r, b, p in
+                                      [(b * rows + i, b, s - k + i) for i in range(k)]) if i % max(1, n // 40) == 0]
+    idx, ptr = [], [0]
+    for _, b, p in picked:
+        idx += [pages[b] * page + t for t in range(p + 1)]
+        ptr.append(len(idx))
+    ids = [r for r, _, _ in picked]
+    idx, ptr = np.array(idx, np.int32), np.array(ptr, np.int32)
+    qq = q.double().numpy()[ids]
+    ref, ref_lse, _ = oracle.sparse_mla_decode(qq, c.rec, idx, ptr, None, 1 / 24, None)
+    a_out, a_lse = allowance(qq, c.rec, idx, ptr, None, 1 / 24, None)
+    for out, lse in got:
+        assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+        assert (np.abs(out.double().numpy()[ids] - ref) <= a_out + 2.0 ** -8 * np.abs(ref) + 1e-30).all()
+        assert (np.abs(lse.double().numpy()[ids] - ref_lse) <= a_lse + 2.0 ** -18 * (1 + np.abs(ref_lse).max())).all()
+    # (all rows, also those that are not in the sample: p and the result as bf16, of values
+    # up to ~2)
+    assert (got[0][0].float() - got[1][0].float()).abs().max() <= 4 * 2.0 ** -8 * 2
+    assert (got[0][1] - got[1][1]).abs().max() <= 1e-4
+
+
+def test_attend_takes_no_longer_with_a_large_gap():
+    # pairs of CTAs: one of them goes past 2^16 empty sequences (60 ms one by one)
+    kv = torch.zeros(1, 1024, REC, dtype=torch.uint8, device=DEV)
+    table, cu, sl = with_gap([(1, 1000, 0)] * 33, 1 << 16, [(1, 900, 0)] * 20)
+    q = torch.zeros(53, 128, 576, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty(53, 128, 512, dtype=torch.bfloat16, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    ms = ms_of(lambda: smla.smla_paged_attend(q, kv, table, cu, sl, 1 / 24, None, out, None, status=st))
+    assert int(st) == 0 and ms < 3.0, ms
