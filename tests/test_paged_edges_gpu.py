@@ -275,3 +275,136 @@ def test_attend_takes_no_longer_with_a_large_gap():
     st = torch.zeros(1, dtype=torch.int32, device=DEV)
     ms = ms_of(lambda: smla.smla_paged_attend(q, kv, table, cu, sl, 1 / 24, None, out, None, status=st))
     assert int(st) == 0 and ms < 3.0, ms
+
+
+# ---- each kernel on keys that rows may not see and queries that are bad ----
+
+# (rows of a chunk + empty sequences) by their mean number of rows, which chooses the kernel
+EMPTY_FOR = {"pair": 0, "narrow64": 2, "narrow32": 5, "few": 20}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", sorted(EMPTY_FOR))
+def test_hidden_keys_reach_no_row_in_any_kernel(name, causal):
+    # 10 tokens x 16 heads over 1 + empty sequences: a mean of 160, 54, 27 and 8 rows.  The
+    # later tokens' records hold a NaN code, an infinite and a NaN scale, an infinite rope
+    c = Batch([(10, 75)] + [(0, 0)] * EMPTY_FOR[name], 16)
+    q, _, want, want_lse, _ = attend(c, 16)
+    for p, at, value in ((70, slice(7, 8), np.array([0x7F], np.uint8)), (71, slice(512, 516), np.array([np.inf], np.float32)),
+                         (72, slice(528, 530), np.array([0x7F80], np.uint16)), (73, slice(512, 516), np.array([np.nan], np.float32))):
+        c.rec[c.slot(0, p), at] = value.view(np.uint8)
+    i = int(c.table[0, 4]) * 16
+    c.rec[i + 11:i + 16] = 0xFF  # slots past the end, in the last page
+    _, _, out, lse, _ = attend(c, 16, q=q, causal=causal)
+    if causal:
+        assert torch.equal(out[:5], want[:5]) and torch.equal(lse[:5], want_lse[:5])
+        assert torch.isnan(out[5:].float()).all() and torch.isnan(lse[5:]).all()
+    else:
+        assert torch.isnan(out.float()).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("name,empty", [("pair", 0), ("narrow64", 1), ("narrow32", 3), ("few", 20)])
+def test_a_bad_query_stays_in_its_row_in_any_kernel(name, empty):
+    # 10 tokens x 16 heads over 2 + empty sequences: a mean of 80, 54, 32 and 8 rows; long
+    # sharp rows beside the bad ones move their references after them
+    c = Batch([(9, 100), (1, 900)] + [(0, 0)] * empty, 16, std=2.0)
+    q, _, want, want_lse, _ = attend(c, 16, sm_scale=0.5)
+    q2 = q.clone()
+    q2[4, 3, 17], q2[9, 5, 570], q2[9, 6, 300] = float("nan"), float("nan"), -float("nan")
+    _, _, out, lse, _ = attend(c, 16, q=q2, sm_scale=0.5)
+    keep = torch.ones(c.rows, 16, dtype=torch.bool)
+    for r, h in ((4, 3), (9, 5), (9, 6)):
+        assert torch.isnan(out[r, h].float()).all() and torch.isnan(lse[r, h])
+        keep[r, h] = False
+    assert torch.equal(out.cpu()[keep], want.cpu()[keep]) and torch.equal(lse.cpu()[keep], want_lse.cpu()[keep])
+
+
+@pytest.mark.parametrize("heads", [30, 64])
+def test_narrow_tiles_return_every_code_exactly(heads):
+    # one key: out is its latent (as for 16 and 128 heads)
+    c = Batch([(1, 1)] * 8, 1)
+    codes = np.array([x for x in range(256) if x & 0x7F != 0x7F] + [0, 0], np.uint8)
+    scales = [2.0 ** e for e in (-116, -40, -22, -9, 0, 5, 7)] + [0.0]
+    for b in range(8):
+        s = c.slot(b, 0)
+        c.rec[s, :512] = np.concatenate([codes, codes[::-1]])
+        c.rec[s, 512:528] = np.full(4, scales[b], np.float32).view(np.uint8)
+    q, _, out, lse, _ = attend(c, heads, q=torch.zeros(8, heads, 576, dtype=torch.bfloat16))
+    lat = unpack(c.rec)[0]
+    for b in range(8):
+        assert (out[b].double().cpu().numpy() == lat[c.slot(b, 0)]).all(), scales[b]
+    assert (lse == 0).all()
+
+
+@pytest.mark.parametrize("heads", [10, 20])
+def test_narrow_tiles_foreign_scales_round_once(heads):
+    # 3 tokens: 30 and 60 rows
+    c = Batch([(3, 270)], 16)
+    sc = torch.exp2(torch.rand(c.n_pages * 16, 4, generator=gen(4)) * 6 - 4).float().numpy()
+    sc[::3] = np.ldexp(1.0, np.random.default_rng(0).integers(-130, 9, sc[::3].shape)).astype(np.float32)
+    c.rec[:, 512:528] = sc.view(np.uint8)
+    q, _, out, lse, _ = attend(c, heads)
+    rows, ref, ref_lse, (a_out, a_lse) = reference_operands(c, q)
+    err = np.abs(out.double().cpu().numpy()[rows] - ref) - (a_out + 2.0 ** -8 * np.abs(ref))
+    assert err.max() <= 0
+    assert (np.abs(lse.double().cpu().numpy()[rows] - ref_lse) <= a_lse + 2.0 ** -18 * (1 + np.abs(ref_lse).max())).all()
+
+
+@pytest.mark.parametrize("heads", [30, 64])
+def test_narrow_tiles_sharp_softmax_and_odd_scales(heads):
+    c = Batch([(1, 700), (1, 1500), (1, 64), (1, 65)], 20, std=3.0, page_pad=32, front=1, behind=2)
+    c.table[torch.rand(c.table.shape, generator=gen(1)) < 0.05] = -1
+    for scale in (1.0, -0.3, 0.0):
+        q, sk, out, lse, _ = attend(c, heads, sm_scale=scale, sink=True)
+        check(c, q, out, lse, scale, sk, True)
+
+
+@pytest.mark.parametrize("heads", [30, 64])
+def test_narrow_tiles_wait_timeout_sets_the_status_and_leaves_the_context_usable(heads):
+    c = Batch([(1, 500), (1, 900)], 64)
+    try:
+        smla.smla_set_wait_limit(20_000_000, stall_first_wait=True)
+        *_, st = attend(c, heads)
+        assert st & smla.STATUS_TIMEOUT
+    finally:
+        smla.smla_set_wait_limit(0)
+    q, sk, out, lse, st = attend(c, heads)
+    assert st == 0
+    check(c, q, out, lse, 1 / 24, sk, True)
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_repeated_launches_give_the_same_bits(name):
+    # sums in fixed order, also of row tiles shared between many workers
+    heads = KERNELS[name]
+    c = Batch([(1, 5000), (1, 900), (1, 50)], 64)
+    q, _, want, want_lse, _ = attend(c, heads, sink=True)
+    assert torch.isfinite(want.float()).all()
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    for i in range(12):
+        flush.fill_(i)
+        _, _, out, lse, _ = attend(c, heads, q=q, sink=True)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("heads", [4, 30, 64, 128])
+@pytest.mark.parametrize("bad", [[0, 6, 3], [7, 0, 0], [5, 5, 2], [-4, 900, -900], [900, 3, 900]])
+def test_boundaries_that_decrease_leave_the_tensors_alone(heads, bad):
+    # which rows they name is not defined; rows in front of and behind the tensors and the
+    # records of the cache stay as they are
+    c = Batch([(4, 40), (3, 30)], 16)
+    kv, (table, _, sl) = c.cache(), c.dev()
+    before = c.buf.clone()
+    cu = torch.tensor(bad, dtype=torch.int32, device=DEV)
+    guard, n = 5, 7
+    q = torch.randn(n, heads, 576, generator=gen(1)).to(torch.bfloat16).to(DEV)
+    out = torch.full((n + 2 * guard, heads, 512), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((n + 2 * guard, heads), 7.0, device=DEV)
+    lat, rope = torch.full((n + 2 * guard, 512), 7.0, device=DEV), torch.full((n + 2 * guard, 64), 7.0, device=DEV)
+    mid = slice(guard, guard + n)
+    smla.smla_paged_attend(q, kv, table, cu, sl, 1 / 24, None, out[mid], lse[mid])
+    smla.smla_paged_read(kv, table, cu, sl, lat[mid], rope[mid])
+    torch.cuda.synchronize()
+    for t in (out, lse, lat, rope):
+        assert (t[:guard] == 7.0).all() and (t[guard + n:] == 7.0).all()
+    assert torch.equal(c.buf, before)
