@@ -383,7 +383,13 @@ int smla_paged_read(const smla_paged_batch* batch, void* latent, int64_t latent_
  * themselves are read from the cache like all others: write them first.
  * Accuracy as the bf16 tensor-core kernel of smla_decode (k and v enter the
  * products as bf16(e4m3 * scale), exact for scales 2^-116 .. 2^7; p is rounded
- * to bf16; sums, maxima and the softmax statistics are f32). */
+ * to bf16; sums, maxima and the softmax statistics are f32).
+ * One kernel serves a call, chosen by the mean rows (n_rows * num_heads /
+ * n_seqs) of its sequences: up to 16, up to 64, or more.  Results do not depend
+ * on it beyond rounding, times do.  Empty and padding sequences count in n_seqs:
+ * pass as many as there are where a chunk matters.  A batch of many single tokens
+ * and a long chunk may be faster as two calls.  Time also grows by up to 2.6 us
+ * for every 1000 sequences, empty or not. */
 typedef struct smla_paged_attend_params {
   smla_paged_batch batch;
   int32_t num_heads;

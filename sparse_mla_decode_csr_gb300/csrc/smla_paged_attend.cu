@@ -45,8 +45,9 @@
 // What bounds the pair kernel: shared memory.  A tile of 64 keys takes ~2420 cycles,
 // in which the operands' reads (1248), the loaders' and softmax warps' accesses (579)
 // and the bulk copies (512) keep its port busy for ~2340.  One chunk of 2048 tokens,
-// 64 heads, after 8192 earlier positions: 2455 us = 1070 TFLOP/s, 56% of the measured
-// bf16 peak; 7 chunks of up to 300 tokens, 16 heads, up to 4927 positions: 222 us.
+// 64 heads, after 8192 earlier positions: 2467 us = 1065 TFLOP/s, 56% of the measured
+// bf16 peak; 7 chunks of up to 300 tokens, 16 heads, up to 4927 positions: 225 us.
+// A tile of the pair takes 1.23 us when it has 128 rows of one token (128 heads).
 //
 // Schedule.  A row tile takes a few slots for its start (kPairStart and so on: what
 // a unit's first tile and last store take, in key tiles) and one per key tile; the
@@ -1239,7 +1240,10 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
         y0 = ex2(y0);
         y1 = ex2(y1);
         add2(sum0, sum1, y0, y1, sum0, sum1);
-        p[c] = pack_bf16x2(y0, y1);  // P as the product's bf16 operand; the sum keeps f32
+        // P as the product's bf16 operand (V is bf16, and one kind::f16 product has one type);
+        // the sum keeps f32.  Relative RMS error of out 0.0017-0.0022, with P in f32
+        // 0.0016-0.0017 (out's own rounding); P as two bf16 terms would read V twice
+        p[c] = pack_bf16x2(y0, y1);
       }
       l = l * alpha + (sum0 + sum1);
       if (g > 0) meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
@@ -1405,10 +1409,11 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // Warps (16): 0-3 softmax, 4-11 loaders, 12-13 half of QK's K-steps each, 14-15
 // two blocks of PV each.
 //
-// What bounds it: the loaders' conversion (~1.85 us a tile of 64 records by eight warps
-// at the register limit), and for short rows the ~10 us until the first scores and the
-// partials' way through L2.  4 x 64 heads over up to 16384 positions: 36 us; 64 x 64
-// heads over 4096: 87 us.
+// What bounds it: the loaders (2.1 us a tile of 64 records by eight warps at the register
+// limit, the same for 17, 32 and 64 rows: 3.0 TB/s of records over all SMs), whose
+// largest stall is the wait for their own global loads, and for short rows the ~10 us
+// until the first scores and the partials' way through L2.  4 x 64 heads over up to 16384
+// positions: 37 us; 64 x 64 heads over 4096: 88 us.
 
 template <int kN>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
@@ -1709,11 +1714,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
 // warp takes 24 of the keys.  Per tile: S read, maxima exchanged, P stored, then warp 0
 // issues the next QK, warps 1 and 2 two blocks of O^T += V^T P^T each.
 //
-// 64 x 16 heads over up to 4096 positions: 52 us (131 MB of records: 2.5 TB/s; 60 us with
+// 64 x 16 heads over up to 4096 positions: 53 us (131 MB of records: 2.5 TB/s; 60 us with
 // eight loaders, tiles of 64 keys and Q in shared memory, 62 us with Q in tensor memory
-// and a third stage instead of more loaders); one token, 16 heads, 500 positions: 14 us.
-// Bound: ~2.4 us a tile of 96 keys, still the loaders, and ~18 us of start, partials and
-// merge.
+// and a third stage instead of more loaders); one token, 16 heads, 500 positions: 15 us.
+// Bound: 2.2 us a tile of 96 keys (4.3 TB/s of records over all SMs), still the loaders,
+// and ~18 us of start, partials and merge.
 
 // QK of tile g, by warp 0.
 __device__ __forceinline__ void few_issue_qk(const AttendArgs& a, Misc* ms, uint64_t k0, uint32_t tmem, uint32_t g) {
@@ -2164,9 +2169,15 @@ paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
 // Rows of a narrow tile (16, 32, 64), or 0 for the pair kernel: by the mean number
 // of rows (tokens x heads) of a sequence, since the lengths themselves are on the
 // device.  Any split is computed correctly by either.  Measured at 64 sequences of
-// 4096 positions (us): 64 rows 86 in a narrow tile of 64, 102 in the pair kernel; 96
-// rows 148 and 104; 128 rows 152 and 107; 16 rows 62 in the few-row kernel, 73 and 77 in
-// narrow tiles of 32 and 64, 97 in the pair kernel.
+// 4096 positions (graph replays, us; rows: few-row kernel / narrow tiles of 32 / of 64 /
+// pair kernel):
+//   16: 63 / 77 / 78 / 99    24: - / 78 / 80 / 100    32: 106 / 80 / 82 / 100
+//   64: 192 / 140 / 88 / 104    96: 273 / 201 / 148 / 106    128: - / - / 154 / 108
+// One kernel serves the whole call, so a batch of unlike sequences gets what its mean
+// gives: 63 single tokens and one of two, 16 heads, take 77 us in tiles of 32 (63 without
+// the second token); 63 tokens and a chunk of 512 177 us in one call, 63 + 97 as two;
+// 255 tokens and the chunk 373, 191 + 97 as two.  Empty sequences count: a chunk of 2048
+// tokens, 4 heads, takes 84 us alone or among 64 sequences, 276 among 512.
 static int narrow_rows(const smla_paged_attend_params& p) {
   if (p.num_heads > kCtaRows) return 0;
   const int64_t mean = (p.batch.n_rows * p.num_heads + p.batch.n_seqs - 1) / p.batch.n_seqs;
