@@ -408,3 +408,87 @@ def test_boundaries_that_decrease_leave_the_tensors_alone(heads, bad):
     for t in (out, lse, lat, rope):
         assert (t[:guard] == 7.0).all() and (t[guard + n:] == 7.0).all()
     assert torch.equal(c.buf, before)
+
+
+# ---- calls at once, and steps in a graph ----
+
+
+def test_calls_of_every_kernel_at_once_give_the_bits_of_calls_alone():
+    # four streams, a kernel each, eight calls in a row without a wait in between
+    jobs = []
+    for i, (name, heads) in enumerate(sorted(KERNELS.items())):
+        c = Batch([(1, 2500), (1, 700)] if name != "pair" else [(3, 1500), (5, 333)], 64, seed=i)
+        q, _, want, want_lse, _ = attend(c, heads)
+        jobs.append((c, heads, q.to(DEV), c.cache(), c.dev(), want, want_lse, torch.cuda.Stream()))
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for c, heads, q, kv, dev, want, want_lse, stream in jobs:
+            out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+            stream.wait_stream(torch.cuda.current_stream())
+            smla.smla_paged_attend(q, kv, *dev, 1 / 24, None, out, lse, stream=stream)
+            got.append((out, lse, want, want_lse))
+    torch.cuda.synchronize()
+    for out, lse, want, want_lse in got:
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_a_serving_step_in_a_graph(heads):
+    # write, attend and read back as one graph over a batch of fixed size (4 slots, 6 token
+    # rows), replayed as sequences grow, move to other pages, finish and start
+    page, n_pages, rows = 16, 40, 6
+    g = gen(heads)
+    rec = oracle.pack_records(bits(torch.randn(n_pages * page, 512, generator=g).to(torch.bfloat16)),
+                              bits(torch.randn(n_pages * page, 64, generator=g).to(torch.bfloat16)))
+    kv = torch.from_numpy(rec.copy()).view(n_pages, page, REC).to(DEV)
+    lat = torch.zeros(rows, 512, dtype=torch.bfloat16, device=DEV)
+    rope = torch.zeros(rows, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros(rows, heads, 576, dtype=torch.bfloat16, device=DEV)
+    table = torch.full((4, 10), -1, dtype=torch.int32, device=DEV)
+    cu, sl = torch.zeros(5, dtype=torch.int32, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+    out = torch.zeros(rows, heads, 512, dtype=torch.bfloat16, device=DEV)
+    lse, back = torch.zeros(rows, heads, device=DEV), torch.zeros(rows, 512, device=DEV)
+    back_rope, status = torch.zeros(rows, 64, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def step():
+        smla.smla_paged_write(lat, rope, kv, table, cu, sl, status=status)
+        smla.smla_paged_attend(q, kv, table, cu, sl, 1 / 24, None, out, lse, status=status)
+        smla.smla_paged_read(kv, table, cu, sl, back, back_rope, status=status)
+
+    step()  # (no rows yet)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for lens in ([(1, 30), (1, 1), (3, 100), (1, 17)], [(2, 32), (0, 0), (1, 101), (1, 18)], [(0, 0), (0, 0), (0, 0), (6, 150)],
+                 [(0, 0)] * 4):
+        order = torch.randperm(n_pages, generator=g).to(torch.int32)
+        c = Batch([(0, 0)] * 4, page)
+        c.lens, c.n_pages, c.rows, c.rec = lens, n_pages, rows, rec
+        c.table = torch.full((4, 10), -1, dtype=torch.int32)
+        at = 0
+        for b, (_, s) in enumerate(lens):
+            k = -(-s // page)
+            c.table[b, :k] = order[at:at + k]
+            at += k
+        c.cu = torch.tensor([0] + [sum(n for n, _ in lens[:b + 1]) for b in range(4)], dtype=torch.int32)
+        new, new_rope = (torch.randn(rows, d, generator=g).to(torch.bfloat16) for d in (512, 64))
+        qq = torch.randn(rows, heads, 576, generator=g).to(torch.bfloat16)
+        for there, here in ((lat, new), (rope, new_rope), (q, qq), (table, c.table), (cu, c.cu),
+                            (sl, torch.tensor([s for _, s in lens], dtype=torch.int32))):
+            there.copy_(here)
+        for t in (out, lse, back, back_rope):
+            t.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for r, b, p in c.positions():
+            rec[c.slot(b, p)] = oracle.pack_records(bits(new[r:r + 1]), bits(new_rope[r:r + 1]))[0]
+        assert np.array_equal(kv.view(-1, REC).cpu().numpy(), rec)
+        check(c, qq, out, lse, 1 / 24, None, True)
+        vals, _, rp = unpack(rec)
+        n = int(c.cu[-1])
+        slots = [c.slot(b, p) for _, b, p in c.positions()]
+        assert np.array_equal(back[:n].cpu().double().numpy(), vals[slots]) and (back[n:] == 7.0).all()
+        assert np.array_equal(back_rope[:n].cpu().double().numpy(), rp[slots]) and (back_rope[n:] == 7.0).all()
+        assert int(status) == 0
