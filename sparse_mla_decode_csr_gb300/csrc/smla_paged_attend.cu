@@ -1143,12 +1143,13 @@ __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, ui
   }
 }
 
-// Output factor and LSE of a row (finish_head_v) with the sink of its head.  A sink of
-// +inf holds all of the weight: out = 0, where inf - inf would give NaN.
+// Output factor and LSE of a row (finish_head_v) with the sink of its head.  A sink that
+// is +inf in log2 units (above 2.36e38) holds all of the weight: out = 0, where inf - inf
+// would give NaN.
 __device__ __forceinline__ void finish_row(const AttendArgs& a, int32_t head, float m, float l, float* factor, float* lse) {
   const float sink = a.sink != nullptr ? __ldg(a.sink + head) : 0.f;
   finish_head_v(m, l, a.sink != nullptr, sink, factor, lse);
-  if (sink == INFINITY && l >= 0.f) *factor = 0.f;
+  if (sink * kLog2e == INFINITY && l >= 0.f) *factor = 0.f;
 }
 
 // The last part of a row tile: the merge kernel joins the parts from the worker

@@ -9,7 +9,7 @@ import torch
 import oracle
 import sparse_mla_decode_csr_gb300 as smla
 from smla_testlib import allowance, bits
-from test_paged_gpu import DEV, REC, Batch, attend, check, expect_records, gen, reference_operands, unpack
+from test_paged_gpu import DEV, REC, Batch, attend, check, expect_records, gen, reference, reference_operands, unpack
 
 pytestmark = pytest.mark.gpu
 
@@ -408,6 +408,23 @@ def test_boundaries_that_decrease_leave_the_tensors_alone(heads, bad):
     for t in (out, lse, lat, rope):
         assert (t[:guard] == 7.0).all() and (t[guard + n:] == 7.0).all()
     assert torch.equal(c.buf, before)
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_the_largest_finite_sinks_hold_all_or_none_of_the_weight(name):
+    heads = KERNELS[name]
+    c = Batch([(1, 3000), (1, 40)], 64)
+    q = torch.randn(c.rows, heads, 576, generator=gen(5)).to(torch.bfloat16)
+    sink = torch.full((heads,), 3e38)  # times log2(e) beyond the largest f32
+    sink[::2] = -3e38
+    out = torch.empty(c.rows, heads, 512, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(c.rows, heads, device=DEV)
+    smla.smla_paged_attend(q.to(DEV), c.cache(), *c.dev(), 1 / 24, sink.to(DEV), out, lse)
+    assert (out[:, 1::2] == 0).all() and torch.isfinite(lse).all()
+    sink[1::2] = 0.0
+    rows, ref, ref_lse, (a_out, a_lse) = reference(c, q, 1 / 24, sink, True)
+    err = np.abs(out.double().cpu().numpy() - ref)[:, ::2]
+    assert (err <= (a_out + 2.0 ** -8 * np.abs(ref))[:, ::2]).all()
 
 
 # ---- calls at once, and steps in a graph ----
