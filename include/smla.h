@@ -416,6 +416,96 @@ size_t smla_paged_attend_workspace_size(const smla_paged_attend_params* params);
 
 int smla_paged_attend(const smla_paged_attend_params* params, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- New rows with their rotation, trees of drafted tokens -------------------
+ *
+ * Serving calls around smla_paged_attend.  A step over plain tokens is
+ * smla_paged_append, smla_paged_attend; one that verifies drafted trees is
+ * smla_paged_tree, smla_paged_append, smla_paged_attend_tree, smla_paged_accept.
+ * All lengths, boundaries and trees are read on the device. */
+
+/* Turns of the 32 rope pairs per position, as fractions of 2^64 modulo a whole turn
+ * (two's complement), from the angles inv_freq in radians: host arithmetic on host
+ * arrays of 32 entries, within 2^-64 turns plus 2^-100 of the angle.  |inv_freq| <= 2^32
+ * (SMLA_ERR_SHAPE otherwise, also for a NaN). */
+int smla_rotation_turns(const double* inv_freq, uint64_t* turns);
+
+/* smla_paged_write with the rope of keys and queries rotated on the way.  With t the
+ * turn of pair k at a row's rotation position, p * inv_freq[k] radians,
+ *   (x, y) -> rope_scale * (x cos t - y sin t, x sin t + y cos t),
+ * the pair being dims 2k and 2k + 1 (interleaved) or k and k + 32.  The angle is exact
+ * modulo a turn for every int32 position; the products are f32, and each result is
+ * rounded once to bf16.
+ *   latent, rope, dtype  as in smla_paged_write (rope before the rotation)
+ *   turns       device, smla_rotation_turns
+ *   rope_scale  finite; it enters cosine and sine
+ *   positions   int32 [n_rows] on the device, rotation positions of the rows (of a tree's
+ *               nodes: smla_paged_tree), or NULL: the rows' positions in the cache.  Where
+ *               a record is stored does not depend on it.
+ *   q_rope      [n_rows][num_heads][64] of type dtype -> q_out, bf16, e.g. the last 64 dims
+ *               of smla_paged_attend's q; 16-byte aligned, strides multiples of 16 bytes.
+ *               They may be the same bf16 memory, with the same strides; another overlap
+ *               is undefined.  num_heads = 0: no queries.
+ * Rows of no sequence are left alone, in q_out too.  A row whose record is masked has
+ * its queries rotated all the same. */
+typedef struct smla_paged_append_params {
+  smla_paged_batch batch;
+  const void* latent;
+  int64_t latent_stride;
+  const void* rope;
+  int64_t rope_stride;
+  int32_t dtype;
+  int32_t interleaved;
+  const uint64_t* turns;
+  float rope_scale;
+  int32_t num_heads;
+  const int32_t* positions;
+  const void* q_rope;
+  int64_t q_rope_stride_row;
+  int64_t q_rope_stride_head;
+  void* q_out;
+  int64_t q_out_stride_row;
+  int64_t q_out_stride_head;
+} smla_paged_append_params;
+
+int smla_paged_append(const smla_paged_append_params* params, void* stream);
+
+/* Masks and positions of drafted trees.  The token rows of sequence b are the nodes
+ * 0, 1, ... of its tree, a parent before its children; parents[r] is the node that row r
+ * hangs on, or negative for a root (there may be several).  For node i
+ *   mask[r], bit j % 32 of word j / 32 = node j is i or an ancestor of i
+ *   positions[r] = (position of node 0) + (number of ancestors of i)
+ * A parent that is not a lower node makes its row a root and sets
+ * SMLA_STATUS_INDEX_OOB; so does a node that its masks' words cannot hold, whose bit is
+ * left out.  All words of the rows of a sequence are written; rows of no sequence
+ * are left alone.  mask uint32 [n_rows][mask_stride], mask_words used, or NULL with
+ * mask_words = 0; positions int32 [n_rows] or NULL.  The time grows with the depth. */
+int smla_paged_tree(const int32_t* parents, const int32_t* cu_rows, const int32_t* seq_lens, int64_t n_rows,
+                    int32_t n_seqs, uint32_t* mask, int64_t mask_stride, int32_t mask_words, int32_t* positions,
+                    int32_t* status, void* stream);
+
+/* smla_paged_attend where the token rows of a sequence see each other by masks: of the
+ * sequence's row j, a row sees the key if bit j % 32 of word j / 32 of its mask is set,
+ * and of earlier positions all.  Rows behind the masks' words are not seen; bits behind the
+ * sequence's rows mean nothing.  With causal = 1 a row in addition sees no position
+ * behind its own (in the cache), which for trees changes nothing.  A row that sees
+ * nothing gives out = 0 and lse = -inf; what a row may not see never reaches it.  mask
+ * uint32 [n_rows][mask_stride], mask_words used (NULL with mask_words = 0: the history
+ * alone).  Workspace, accuracy and the choice of the kernel as smla_paged_attend. */
+int smla_paged_attend_tree(const smla_paged_attend_params* params, const uint32_t* mask, int64_t mask_stride,
+                           int32_t mask_words, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Keeps the accepted path of each tree: path[b] names nodes of sequence b, rising, and the
+ * record of its i-th node moves to the position of node 0 plus i (byte for byte, so that
+ * the rotation, made for that depth, holds); new_lens[b] = position of node 0 + number of
+ * nodes accepted.  The path ends at its first negative entry (padding), or at one
+ * that is no node of the tree or does not rise, which sets SMLA_STATUS_INDEX_OOB.
+ * A record whose old or new place is masked stays where it is.  Records of the tree behind
+ * the accepted ones are left as they are.  path int32 [n_seqs][path_stride],
+ * path_len used; new_lens int32 [n_seqs], which may be the batch's seq_lens.  As in
+ * smla_paged_write, the rows' positions have to lie in different slots. */
+int smla_paged_accept(const smla_paged_batch* batch, const int32_t* path, int64_t path_stride, int32_t path_len,
+                      int32_t* new_lens, void* stream);
+
 /* Name of a status code. */
 const char* smla_strerror(int status);
 

@@ -35,6 +35,7 @@ KERNEL_TENSOR_CORE_BF16 = 2
 KERNEL_TENSOR_CORE_FP8 = 3
 NOALLOC_SCRATCH_BYTES = 64 << 20  # SMLA_NOALLOC_SCRATCH_BYTES
 PAGED_MAX_HEADS = 128
+MAX_ROWS = 1 << 30  # token rows of a call
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # SMLA_DTYPE_*
 SMLA_ERR_NULL = -1
 SMLA_ERR_SHAPE = -2
@@ -126,6 +127,28 @@ class PagedAttendParams(ctypes.Structure):
     ]
 
 
+class PagedAppendParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", PagedBatch),
+        ("latent", ctypes.c_void_p),
+        ("latent_stride", ctypes.c_int64),
+        ("rope", ctypes.c_void_p),
+        ("rope_stride", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("turns", ctypes.c_void_p),
+        ("rope_scale", ctypes.c_float),
+        ("num_heads", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
+        ("q_rope", ctypes.c_void_p),
+        ("q_rope_stride_row", ctypes.c_int64),
+        ("q_rope_stride_head", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p),
+        ("q_out_stride_row", ctypes.c_int64),
+        ("q_out_stride_head", ctypes.c_int64),
+    ]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -154,6 +177,20 @@ def _load():
     lib.smla_paged_attend.argtypes = [ctypes.POINTER(PagedAttendParams), ctypes.c_void_p, ctypes.c_size_t,
                                       ctypes.c_void_p]
     lib.smla_paged_attend.restype = ctypes.c_int
+    lib.smla_rotation_turns.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    lib.smla_rotation_turns.restype = ctypes.c_int
+    lib.smla_paged_append.argtypes = [ctypes.POINTER(PagedAppendParams), ctypes.c_void_p]
+    lib.smla_paged_append.restype = ctypes.c_int
+    lib.smla_paged_tree.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                    ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                    ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    lib.smla_paged_tree.restype = ctypes.c_int
+    lib.smla_paged_attend_tree.argtypes = [ctypes.POINTER(PagedAttendParams), ctypes.c_void_p, ctypes.c_int64,
+                                           ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    lib.smla_paged_attend_tree.restype = ctypes.c_int
+    lib.smla_paged_accept.argtypes = [ctypes.POINTER(PagedBatch), ctypes.c_void_p, ctypes.c_int64,
+                                      ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+    lib.smla_paged_accept.restype = ctypes.c_int
     lib.smla_strerror.argtypes = [ctypes.c_int]
     lib.smla_strerror.restype = ctypes.c_char_p
     lib.smla_device_check.argtypes = []
@@ -168,6 +205,8 @@ lib = _load()
 EXPORTED_SYMBOLS = ("smla_plan", "smla_decode_workspace_size", "smla_decode", "smla_decode_noalloc",
                     "smla_pack_records", "smla_paged_write", "smla_paged_read",
                     "smla_paged_attend_workspace_size", "smla_paged_attend",
+                    "smla_rotation_turns", "smla_paged_append", "smla_paged_tree", "smla_paged_attend_tree",
+                    "smla_paged_accept",
                     "smla_strerror", "smla_device_check", "smla_set_wait_limit")
 
 
@@ -350,6 +389,7 @@ def smla_pack_records(latent: torch.Tensor, rope: torch.Tensor, kv_out: torch.Te
 _BATCH_FORMAT = "PqqiiPqPPqi4xP"
 _pack_batch = struct.Struct(_BATCH_FORMAT).pack
 _pack_attend = struct.Struct(_BATCH_FORMAT + "iiPqqf4xPPqqP").pack
+_pack_append = struct.Struct(_BATCH_FORMAT + "PqPqiiPfiPPqqPqq").pack
 
 
 def _packed(name: str, restype, *argtypes):
@@ -363,6 +403,11 @@ _write_packed = _packed("smla_paged_write", ctypes.c_int, *_copy_args)
 _read_packed = _packed("smla_paged_read", ctypes.c_int, *_copy_args)
 _workspace_packed = _packed("smla_paged_attend_workspace_size", ctypes.c_size_t)
 _attend_packed = _packed("smla_paged_attend", ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)
+_attend_tree_packed = _packed("smla_paged_attend_tree", ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                              ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p)
+_append_packed = _packed("smla_paged_append", ctypes.c_int, ctypes.c_void_p)
+_accept_packed = _packed("smla_paged_accept", ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                         ctypes.c_void_p, ctypes.c_void_p)
 
 
 def _fail(code: int, what: str, why: str):
@@ -417,7 +462,8 @@ def _paged_batch(what: str, kv_cache: torch.Tensor, block_table: torch.Tensor, c
             n_rows, n_seqs, 0 if status is None else status.data_ptr())
 
 
-def _paged_copy(what, call, kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status) -> None:
+def _rows(what, latent, rope) -> tuple:
+    """Rows, dtype and strides of latent [rows, 512] and rope [rows, 64], checked."""
     dtype = DTYPES.get(latent.dtype)
     if dtype is None or rope.dtype != latent.dtype:
         _fail(SMLA_ERR_SHAPE, what, "latent and rope of one type, bf16, f16 or f32")
@@ -432,6 +478,11 @@ def _paged_copy(what, call, kv_cache, block_table, cu_rows, seq_lens, latent, ro
         _fail(SMLA_ERR_STRIDE, what, "the rows of latent and rope are contiguous")
     if n <= 1:  # (the stride of a single row says nothing)
         ls, rs = LATENT_DIM, ROPE_DIM
+    return n, dtype, ls, rs
+
+
+def _paged_copy(what, call, kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status) -> None:
+    n, dtype, ls, rs = _rows(what, latent, rope)
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
     device = _current_device(what, (latent, rope, kv_cache, block_table, cu_rows, seq_lens, status))
     rc = call(_pack_batch(*batch), latent.data_ptr(), ls, rope.data_ptr(), rs, dtype, _launch_stream(stream, device))
@@ -477,19 +528,8 @@ def smla_paged_attend_workspace_size(n_rows: int, num_heads: int, n_seqs: int, p
     return int(lib.smla_paged_attend_workspace_size(ctypes.byref(p)))
 
 
-def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
-                      seq_lens: torch.Tensor, sm_scale: float, sink: Optional[torch.Tensor], out: torch.Tensor,
-                      lse: Optional[torch.Tensor], stream=None, *, causal: bool = True,
-                      status: Optional[torch.Tensor] = None, workspace_tensor: Optional[torch.Tensor] = None) -> None:
-    """Attention of new token rows over a paged cache, into ``out`` (bf16
-    [rows, H, 512]) and ``lse`` (f32 [rows, H] or None).
-
-    q: bf16 [rows, H, 576], H up to 128; batch as smla_paged_write (the rows'
-    own records are read from the cache: write them first).  A row at position
-    p sees positions 0..p (causal) or its whole sequence; sink: f32 [H] or None.
-    workspace_tensor: uint8, smla_paged_attend_workspace_size bytes; without it
-    one is allocated for this call on its stream.  See include/smla.h."""
-    what = "smla_paged_attend"
+def _attend(what: str, q, kv_cache, block_table, cu_rows, seq_lens, mask, sm_scale, sink, out, lse, stream, causal,
+            status, workspace_tensor) -> None:
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != QK_DIM:
         _fail(SMLA_ERR_SHAPE, what, f"q is bf16 [rows, heads, {QK_DIM}]")
     n, heads, _ = q.shape
@@ -510,9 +550,11 @@ def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
         _fail(SMLA_ERR_SHAPE, what, "lse is contiguous f32 [rows, heads]")
     if workspace_tensor is not None and not workspace_tensor.is_contiguous():
         _fail(SMLA_ERR_STRIDE, what, "workspace_tensor is contiguous")
+    if mask is not None:
+        mask_row, words = _mask_layout(what, mask, n)
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
     device = _current_device(what, (q, out, sink, lse, kv_cache, block_table, cu_rows, seq_lens, status,
-                                    workspace_tensor))
+                                    workspace_tensor, mask))
     try:
         p = _pack_attend(*batch, heads, 1 if causal else 0, q.data_ptr(), q_row, q_head, sm_scale,
                          0 if sink is None else sink.data_ptr(), out.data_ptr(), o_row, o_head,
@@ -533,8 +575,194 @@ def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torc
                     stream = torch.cuda.ExternalStream(s) if s else torch.cuda.default_stream()
                 with torch.cuda.stream(stream):
                     ws = kv_cache.new_empty(nbytes)
-    rc = _attend_packed(p, None if ws is None else ws.data_ptr(),
-                               0 if ws is None else ws.nbytes, s)
+    ws_at, ws_bytes = (None, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
+    if mask is None:
+        rc = _attend_packed(p, ws_at, ws_bytes, s)
+    else:
+        rc = _attend_tree_packed(p, mask.data_ptr(), mask_row, words, ws_at, ws_bytes, s)
+    if rc != 0:
+        raise SmlaError(rc, what)
+
+
+def smla_paged_attend(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
+                      seq_lens: torch.Tensor, sm_scale: float, sink: Optional[torch.Tensor], out: torch.Tensor,
+                      lse: Optional[torch.Tensor], stream=None, *, causal: bool = True,
+                      status: Optional[torch.Tensor] = None, workspace_tensor: Optional[torch.Tensor] = None) -> None:
+    """Attention of new token rows over a paged cache, into ``out`` (bf16
+    [rows, H, 512]) and ``lse`` (f32 [rows, H] or None).
+
+    q: bf16 [rows, H, 576], H up to 128; batch as smla_paged_write (the rows'
+    own records are read from the cache: write them first).  A row at position
+    p sees positions 0..p (causal) or its whole sequence; sink: f32 [H] or None.
+    workspace_tensor: uint8, smla_paged_attend_workspace_size bytes; without it
+    one is allocated for this call on its stream.  See include/smla.h."""
+    _attend("smla_paged_attend", q, kv_cache, block_table, cu_rows, seq_lens, None, sm_scale, sink, out, lse, stream,
+            causal, status, workspace_tensor)
+
+
+# ---- rotation and trees of drafted tokens ----
+
+
+def smla_rotation_turns(inv_freq, device=None) -> torch.Tensor:
+    """The rotation table of smla_paged_append: int64 [32] on `device` (the current CUDA
+    device by default) from the 32 angles per position, in radians (a tensor or a
+    sequence).  Made on the host; keep it for all calls."""
+    f = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+    if f.shape != (ROPE_DIM // 2,):
+        _fail(SMLA_ERR_SHAPE, "smla_rotation_turns", f"{ROPE_DIM // 2} angles per position")
+    turns = torch.empty(ROPE_DIM // 2, dtype=torch.int64)
+    rc = lib.smla_rotation_turns(f.data_ptr(), turns.data_ptr())
+    if rc != 0:
+        raise SmlaError(rc, "smla_rotation_turns")
+    return turns.to("cuda" if device is None else device)
+
+
+def _queries(what: str, x: torch.Tensor, name: str, n: int) -> tuple:
+    """Heads and strides of a rope part [rows, heads, 64], checked."""
+    if x.dim() != 3 or x.shape[0] != n or x.shape[2] != ROPE_DIM:
+        _fail(SMLA_ERR_SHAPE, what, f"{name} is [rows, heads, {ROPE_DIM}]")
+    heads = x.shape[1]
+    row, head, one = x.stride()
+    if n and heads and one != 1:
+        _fail(SMLA_ERR_STRIDE, what, f"the last dimension of {name} is contiguous")
+    # (the stride of a dimension of one element says nothing)
+    if heads <= 1:
+        head = ROPE_DIM
+    return heads, row if n > 1 else heads * head, head
+
+
+def smla_paged_append(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor,
+                      cu_rows: torch.Tensor, seq_lens: torch.Tensor, turns: torch.Tensor, stream=None, *,
+                      q_rope: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None, interleaved: bool = True, rope_scale: float = 1.0,
+                      status: Optional[torch.Tensor] = None) -> None:
+    """smla_paged_write with the rope of keys and queries rotated on the way.
+
+    latent [rows, 512], rope [rows, 64] and q_rope [rows, H, 64]: bf16, f16 or
+    f32, before the rotation.  The records get the rotated rope, q_out (bf16
+    [rows, H, 64], e.g. q[..., 512:]) the rotated queries; it may be q_rope
+    itself.  turns: smla_rotation_turns.  A row turns by its position in the
+    cache, or by positions (int32 [rows], e.g. of smla_paged_tree); pairs are
+    dims (2k, 2k + 1), or (k, k + 32) without interleaved; rope_scale
+    multiplies the results.  Batch and masked rows as smla_paged_write.  See
+    include/smla.h."""
+    what = "smla_paged_append"
+    n, dtype, ls, rs = _rows(what, latent, rope)
+    if turns.dtype != torch.int64 or turns.shape != (ROPE_DIM // 2,) or not turns.is_contiguous():
+        _fail(SMLA_ERR_SHAPE, what, f"turns is int64 [{ROPE_DIM // 2}], made by smla_rotation_turns")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (n,)):
+        _fail(SMLA_ERR_SHAPE, what, "positions is int32 [rows]")
+    if positions is not None and n > 1 and positions.stride(0) != 1:
+        _fail(SMLA_ERR_STRIDE, what, "positions is contiguous")
+    if (q_rope is None) != (q_out is None):
+        _fail(SMLA_ERR_NULL, what, "q_rope and q_out belong together")
+    heads = q_row = q_head = o_row = o_head = 0
+    if q_rope is not None:
+        if q_rope.dtype != latent.dtype or q_out.dtype != torch.bfloat16:
+            _fail(SMLA_ERR_SHAPE, what, "q_rope has the type of latent, q_out is bf16")
+        heads, q_row, q_head = _queries(what, q_rope, "q_rope", n)
+        out_heads, o_row, o_head = _queries(what, q_out, "q_out", n)
+        if heads != out_heads:
+            _fail(SMLA_ERR_SHAPE, what, "q_rope and q_out have the same heads")
+    batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, n, status)
+    device = _current_device(what, (latent, rope, kv_cache, block_table, cu_rows, seq_lens, turns, q_rope, q_out,
+                                    positions, status))
+    p = _pack_append(*batch, latent.data_ptr(), ls, rope.data_ptr(), rs, dtype, 1 if interleaved else 0,
+                     turns.data_ptr(), rope_scale, heads, 0 if positions is None else positions.data_ptr(),
+                     0 if q_rope is None else q_rope.data_ptr(), q_row, q_head,
+                     0 if q_out is None else q_out.data_ptr(), o_row, o_head)
+    rc = _append_packed(p, _launch_stream(stream, device))
+    if rc != 0:
+        raise SmlaError(rc, what)
+
+
+def _mask_layout(what: str, mask: torch.Tensor, n: int) -> tuple:
+    """Row stride and words of a mask int32 [rows, words], checked."""
+    if mask.dtype != torch.int32 or mask.dim() != 2 or mask.shape[0] != n:
+        _fail(SMLA_ERR_SHAPE, what, "mask is int32 [rows, words]")
+    words = mask.shape[1]
+    row, one = mask.stride()
+    if n and words > 1 and one != 1:
+        _fail(SMLA_ERR_STRIDE, what, "the rows of mask are contiguous")
+    return row if n > 1 else words, words
+
+
+def smla_paged_tree(parents: torch.Tensor, cu_rows: torch.Tensor, seq_lens: torch.Tensor,
+                    mask: Optional[torch.Tensor], positions: Optional[torch.Tensor], stream=None, *,
+                    status: Optional[torch.Tensor] = None) -> None:
+    """Masks and positions of trees of drafted tokens, from their parents.
+
+    The token rows of sequence b are the nodes of its tree, a parent before its
+    children; parents (int32 [rows]): a row's parent node, negative for a root.
+    mask (int32 [rows, words] or None): bit j % 32 of word j // 32 is set for
+    the node itself and its ancestors; positions (int32 [rows] or None): the
+    position of node 0 plus the node's depth.  A parent that is not a lower
+    node, or a node that the words cannot hold, sets STATUS_INDEX_OOB.  See
+    include/smla.h."""
+    what = "smla_paged_tree"
+    i32 = torch.int32
+    if parents.dtype != i32 or cu_rows.dtype != i32 or seq_lens.dtype != i32 or parents.dim() != 1 or \
+            cu_rows.dim() != 1 or seq_lens.dim() != 1:
+        _fail(SMLA_ERR_SHAPE, what, "parents, cu_rows and seq_lens are int32 vectors")
+    n, n_seqs = parents.shape[0], seq_lens.shape[0]
+    if cu_rows.shape[0] != n_seqs + 1:
+        _fail(SMLA_ERR_SHAPE, what, "n_seqs + 1 entries of cu_rows for n_seqs of seq_lens")
+    if positions is not None and (positions.dtype != i32 or positions.shape != (n,)):
+        _fail(SMLA_ERR_SHAPE, what, "positions is int32 [rows]")
+    if n_seqs and (cu_rows.stride(0) != 1 or (n_seqs > 1 and seq_lens.stride(0) != 1)) or \
+            n > 1 and (parents.stride(0) != 1 or (positions is not None and positions.stride(0) != 1)):
+        _fail(SMLA_ERR_STRIDE, what, "parents, cu_rows, seq_lens and positions are contiguous")
+    if status is not None and (status.dtype != i32 or status.numel() < 1):
+        _fail(SMLA_ERR_SHAPE, what, "status is int32 [1]")
+    mask_row, words = (0, 0) if mask is None else _mask_layout(what, mask, n)
+    device = _current_device(what, (parents, cu_rows, seq_lens, mask, positions, status))
+    rc = lib.smla_paged_tree(parents.data_ptr(), cu_rows.data_ptr(), seq_lens.data_ptr(), n, n_seqs, _ptr(mask),
+                             mask_row, words, _ptr(positions), _ptr(status), _launch_stream(stream, device))
+    if rc != 0:
+        raise SmlaError(rc, what)
+
+
+def smla_paged_attend_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
+                           seq_lens: torch.Tensor, mask: torch.Tensor, sm_scale: float, sink: Optional[torch.Tensor],
+                           out: torch.Tensor, lse: Optional[torch.Tensor], stream=None, *, causal: bool = False,
+                           status: Optional[torch.Tensor] = None,
+                           workspace_tensor: Optional[torch.Tensor] = None) -> None:
+    """smla_paged_attend for trees of drafted tokens: of its sequence's token rows a
+    row sees row j if bit j % 32 of word j // 32 of its mask (int32 [rows, words],
+    e.g. of smla_paged_tree) is set, and of earlier positions all.  With causal
+    a row in addition sees no position behind its own.  Everything else, the
+    workspace's size included, as smla_paged_attend.  See include/smla.h."""
+    what = "smla_paged_attend_tree"
+    if mask is None:
+        _fail(SMLA_ERR_NULL, what, "mask is int32 [rows, words]")
+    _attend(what, q, kv_cache, block_table, cu_rows, seq_lens, mask, sm_scale, sink, out, lse,
+            stream, causal, status, workspace_tensor)
+
+
+def smla_paged_accept(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: torch.Tensor,
+                      seq_lens: torch.Tensor, path: torch.Tensor, new_lens: torch.Tensor, stream=None, *,
+                      n_rows: int = MAX_ROWS, status: Optional[torch.Tensor] = None) -> None:
+    """Keeps the accepted path of each tree of drafted tokens.
+
+    path: int32 [n_seqs, width], rising nodes of each tree, then negative
+    entries.  The record of the i-th node of the path moves to the position of
+    node 0 plus i, and new_lens[b] (int32 [n_seqs], which may be seq_lens) becomes
+    the position of node 0 plus the number of nodes.  An entry that is no node or
+    does not rise ends the path and sets STATUS_INDEX_OOB.  n_rows: rows of the
+    token tensors, which clamp cu_rows in the other calls.  See include/smla.h."""
+    what = "smla_paged_accept"
+    batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, int(n_rows), status)
+    n_seqs = seq_lens.shape[0]
+    if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] != n_seqs:
+        _fail(SMLA_ERR_SHAPE, what, "path is int32 [n_seqs, width]")
+    if new_lens.dtype != torch.int32 or new_lens.shape != (n_seqs,):
+        _fail(SMLA_ERR_SHAPE, what, "new_lens is int32 [n_seqs]")
+    width = path.shape[1]
+    if n_seqs and ((width > 1 and path.stride(1) != 1) or (n_seqs > 1 and new_lens.stride(0) != 1)):
+        _fail(SMLA_ERR_STRIDE, what, "the rows of path and new_lens are contiguous")
+    device = _current_device(what, (kv_cache, block_table, cu_rows, seq_lens, path, new_lens, status))
+    rc = _accept_packed(_pack_batch(*batch), path.data_ptr(), path.stride(0) if n_seqs > 1 else width, width,
+                        new_lens.data_ptr(), _launch_stream(stream, device))
     if rc != 0:
         raise SmlaError(rc, what)
 

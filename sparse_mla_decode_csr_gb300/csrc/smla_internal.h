@@ -72,12 +72,25 @@ struct AttendPlan {
   int64_t merge_off, ml_off, o_off, total;
 };
 AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms);
-cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendPlan& plan, void* workspace,
-                                cudaStream_t stream);
+// The token rows that a row sees beside the history: bit j of its mask, its sequence's
+// row j (a tree); without masks (words < 0) all that the causal edge leaves.
+struct TreeMasks {
+  const uint32_t* mask = nullptr;
+  int64_t stride = 0;
+  int32_t words = -1;
+};
+cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const TreeMasks& tree, const AttendPlan& plan,
+                                void* workspace, cudaStream_t stream);
 cudaError_t paged_set_wait_limit(uint64_t ns, int stall);
 cudaError_t launch_paged_write(const smla_paged_batch& b, const void* latent, int64_t latent_stride, const void* rope,
                                int64_t rope_stride, int32_t dtype, cudaStream_t stream);
 cudaError_t launch_paged_read(const smla_paged_batch& b, void* latent, int64_t latent_stride, void* rope,
                               int64_t rope_stride, int32_t dtype, cudaStream_t stream);
+cudaError_t launch_paged_append(const smla_paged_append_params& p, cudaStream_t stream);
+// (of the batch: cu_rows, seq_lens and the sizes)
+cudaError_t launch_paged_tree(const smla_paged_batch& b, const int32_t* parents, uint32_t* mask, int64_t mask_stride,
+                              int32_t mask_words, int32_t* positions, cudaStream_t stream);
+cudaError_t launch_paged_accept(const smla_paged_batch& b, const int32_t* path, int64_t path_stride, int32_t path_len,
+                                int32_t* new_lens, cudaStream_t stream);
 
 }  // namespace smla

@@ -145,6 +145,9 @@ struct AttendArgs {
   float* o_part;                  // [2 workers][part_rows][512]
   float* ml_part;                 // [2 workers][part_rows][2]
   int32_t* merge;                 // [workers][4]: rows to merge (0: none), first token row, first worker
+  const uint32_t* mask;           // kTree: bit j of a token row's words: it sees its sequence's row j
+  int64_t mask_stride;
+  int32_t mask_words;
 };
 
 struct Misc {
@@ -404,6 +407,17 @@ __device__ int64_t slots_before(const AttendArgs& a, const Seq& s, int32_t j) {
   if (hi > lo) sum += tile_sum(hi - lo, G, P + G * (lo + 1) + kTileKeys - 1);
   sum += int64_t(n - hi) * key_tiles(C);
   return sum;
+}
+
+// Which of the keys [key0, key0 + 32) a row of a tree sees by its mask: all before `past`,
+// the position of node 0, then the mask's bits, none behind its words.
+__device__ __forceinline__ uint32_t tree_keys(const uint32_t* mask, int32_t words, int32_t past, int32_t key0) {
+  const int32_t node = key0 - past;
+  if (node <= -32) return ~0u;
+  const int32_t w = node >> 5;  // -1: the history's last keys
+  const uint32_t lo = w < 0 ? ~0u : w < words ? __ldg(mask + w) : 0u;
+  const uint32_t hi = w + 1 < words ? __ldg(mask + w + 1) : 0u;
+  return __funnelshift_r(lo, hi, node & 31);
 }
 
 // A row tile's part that this worker works on.
@@ -1161,6 +1175,7 @@ __device__ __noinline__ void name_merge(const AttendArgs& a, const Misc* ms, int
   a.merge[worker * 4] = u.tokens * a.heads;
 }
 
+template <bool kTree>
 __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem, uint32_t rank,
                                              int32_t pair) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1183,10 +1198,16 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   while (units.next(a, u)) {
     const bool live = m < u.tokens * a.heads;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
+    const int32_t past = kTree ? seq_at(a, u.seq).past : 0;
+    const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
     float ref = -INFINITY, l = 0.f;
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
+      const int32_t key0 = t * kTileKeys + 32 * half;
+      const bool nodes = kTree && key0 + 32 > past;  // (the same for all rows)
+      uint32_t tree = ~0u;
+      if (nodes && live) tree = tree_keys(mask, a.mask_words, past, key0);
       meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       uint32_t s[64];  // the two accumulators' 32 columns
@@ -1213,11 +1234,10 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] *= by;
       }
-      const int32_t key0 = t * kTileKeys + 32 * half;
-      if (__any_sync(0xffffffffu, key0 + 32 > see) || flags) {
+      if (__any_sync(0xffffffffu, key0 + 32 > see) || flags || nodes) {
         // bit c: key c is seen
         const int32_t n = see - key0;
-        const uint32_t seen = ~flags & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
+        const uint32_t seen = tree & ~flags & (n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u);
 #pragma unroll
         for (int c = 0; c < 32; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
       }
@@ -1319,6 +1339,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   }
 }
 
+template <bool kTree>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
@@ -1367,7 +1388,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
   if (warp < kFirstLoader) {
-    softmax_role(a, ms, base, tmem, rank, pair);
+    softmax_role<kTree>(a, ms, base, tmem, rank, pair);
   } else if (warp < kIssuerQk) {
     loader_role(a, ms, base, rank);
   } else if (warp == kCopier) {
@@ -1416,7 +1437,7 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // until the first scores and the partials' way through L2.  4 x 64 heads over up to 16384
 // positions: 37 us; 64 x 64 heads over 4096: 88 us.
 
-template <int kN>
+template <int kN, bool kTree>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                     int32_t worker) {
   using L = Narrow<kN>;
@@ -1438,9 +1459,18 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const bool live = mine && m < rows;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
+    const int32_t past = kTree ? seq_at(a, u.seq).past : 0;
+    const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
     float ref = -INFINITY, l = 0.f;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
+      const int32_t first = t * kTileKeys + kKeys * slice;
+      const bool nodes = kTree && first + kKeys > past;  // (the same for all rows)
+      uint64_t tree = ~0ull;
+      if (nodes && live) {
+        tree = tree_keys(mask, a.mask_words, past, first);
+        if (kKeys > 32) tree |= uint64_t(tree_keys(mask, a.mask_words, past, first + 32)) << 32;
+      }
       meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       float x[kKeys];
@@ -1463,9 +1493,9 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) x[c] *= by;
       }
-      const int32_t n = see - t * kTileKeys - kKeys * slice;
-      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0) {
-        const uint64_t seen = ~flags & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull);
+      const int32_t n = see - first;
+      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0 || nodes) {
+        const uint64_t seen = tree & ~flags & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull);
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
       }
@@ -1644,7 +1674,7 @@ __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, ui
   }
 }
 
-template <int kN>
+template <int kN, bool kTree>
 __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   const uint32_t base = smem_u32(raw_smem);
@@ -1682,7 +1712,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
   if (warp < kFirstLoader) {
-    narrow_softmax_role<kN>(a, ms, base, tmem, worker);
+    narrow_softmax_role<kN, kTree>(a, ms, base, tmem, worker);
   } else if (warp < kNarrowQk) {
     narrow_loader_role<kN>(a, ms, base);
   } else {
@@ -1739,6 +1769,7 @@ __device__ __forceinline__ void few_issue_qk(const AttendArgs& a, Misc* ms, uint
   __syncwarp();
 }
 
+template <bool kTree>
 __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                  int32_t worker) {
   using L = Narrow<16>;
@@ -1766,6 +1797,8 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
     const int32_t key0 = t0 * kTileKeys, stop = t1 * kTileKeys, end = min(u.end, stop);
     const bool live = mine && m < rows;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, end), 0) : end;
+    const int32_t past = kTree ? seq_at(a, u.seq).past : 0;
+    const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
     float ref = -INFINITY, l = 0.f;
     // q (every warp has seen the last QK and PV of the unit before done)
     load_q_tmem(a, base + L::kOffP, lane_base + kTmemQFew, u.row0, rows);
@@ -1773,6 +1806,10 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
     if (warp == 0) few_issue_qk(a, ms, k0, tmem, g);
     for (int32_t key = key0; key < stop; key += L::kKeys, ++g) {
       const uint32_t stage = g & 1;
+      const int32_t first = key + kKeys * slice;
+      const bool nodes = kTree && first + kKeys > past;  // (the same for all rows)
+      uint32_t tree = ~0u;
+      if (nodes && live) tree = tree_keys(mask, a.mask_words, past, first);
       meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       float x[kKeys];
@@ -1793,9 +1830,9 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) x[c] *= by;
       }
-      const int32_t n = see - key - kKeys * slice;
-      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0) {
-        const uint32_t seen = ~flags & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
+      const int32_t n = see - first;
+      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0 || nodes) {
+        const uint32_t seen = tree & ~flags & (n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u);
 #pragma unroll
         for (int c = 0; c < kKeys; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
       }
@@ -1920,6 +1957,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
   }
 }
 
+template <bool kTree>
 __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_few_kernel(const __grid_constant__ AttendArgs a) {
   extern __shared__ __align__(1024) uint8_t raw_smem[];
   const uint32_t base = smem_u32(raw_smem);
@@ -1954,7 +1992,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_few_kernel(con
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
   if (warp < kFirstLoader) {
-    few_compute_role(a, ms, base, tmem, worker);
+    few_compute_role<kTree>(a, ms, base, tmem, worker);
     // every MMA complete before the memory it reads goes away
     __syncwarp();
     if (warp < 3 && elect_one()) {  // (the lane that issued them: the same for the same mask)
@@ -2231,6 +2269,18 @@ static cudaError_t launch_narrow(void (*kernel)(AttendArgs), int smem, const Att
   return cudaGetLastError();
 }
 
+template <bool kTree>
+static cudaError_t launch_kernel(const AttendArgs& a, const AttendPlan& plan, cudaStream_t stream) {
+  if (plan.narrow == 16) return launch_narrow(paged_attend_few_kernel<kTree>, kNarrowSmem<16>, a, stream);
+  if (plan.narrow == 32) return launch_narrow(paged_attend_narrow_kernel<32, kTree>, kNarrowSmem<32>, a, stream);
+  if (plan.narrow == 64) return launch_narrow(paged_attend_narrow_kernel<64, kTree>, kNarrowSmem<64>, a, stream);
+  const cudaError_t err =
+      cudaFuncSetAttribute(paged_attend_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
+  if (err != cudaSuccess) return err;
+  paged_attend_kernel<kTree><<<2 * plan.workers, kAttendThreads, kAttendSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 static cudaError_t launch_merge(void (*kernel)(AttendArgs), const AttendArgs& a, dim3 grid, int threads,
                                 cudaStream_t stream) {
   cudaLaunchConfig_t config{};
@@ -2245,8 +2295,8 @@ static cudaError_t launch_merge(void (*kernel)(AttendArgs), const AttendArgs& a,
   return cudaLaunchKernelEx(&config, kernel, a);
 }
 
-cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendPlan& plan, void* workspace,
-                                cudaStream_t stream) {
+cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const TreeMasks& tree, const AttendPlan& plan,
+                                void* workspace, cudaStream_t stream) {
   AttendArgs a{};
   a.b = make_paged_args(p.batch);
   a.q = static_cast<const uint16_t*>(p.q);
@@ -2269,19 +2319,10 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const AttendP
   a.merge = reinterpret_cast<int32_t*>(ws + plan.merge_off);
   a.ml_part = reinterpret_cast<float*>(ws + plan.ml_off);
   a.o_part = reinterpret_cast<float*>(ws + plan.o_off);
-  cudaError_t err;
-  if (plan.narrow == 16) {
-    err = launch_narrow(paged_attend_few_kernel, kNarrowSmem<16>, a, stream);
-  } else if (plan.narrow == 32) {
-    err = launch_narrow(paged_attend_narrow_kernel<32>, kNarrowSmem<32>, a, stream);
-  } else if (plan.narrow == 64) {
-    err = launch_narrow(paged_attend_narrow_kernel<64>, kNarrowSmem<64>, a, stream);
-  } else {
-    err = cudaFuncSetAttribute(paged_attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
-    if (err != cudaSuccess) return err;
-    paged_attend_kernel<<<2 * plan.workers, kAttendThreads, kAttendSmem, stream>>>(a);
-    err = cudaGetLastError();
-  }
+  a.mask = tree.mask;
+  a.mask_stride = tree.stride;
+  a.mask_words = tree.words;
+  const cudaError_t err = tree.words < 0 ? launch_kernel<false>(a, plan, stream) : launch_kernel<true>(a, plan, stream);
   if (err != cudaSuccess || plan.workers == 1) return err;
   // Row tiles of 8 parts or more on average: several warps share a row's parts, and the
   // grid is as large as the row tiles, not as the workers (4 x 64 heads, 38 parts: 42.9 us

@@ -1,0 +1,145 @@
+// Drafted-token trees over the paged cache: the nodes' masks and positions from
+// their parents (smla_paged_tree), and the accepted path's records moved up behind the
+// history (smla_paged_accept).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "smla_internal.h"
+#include "smla_paged.cuh"
+
+namespace smla {
+namespace {
+
+// ---- masks and positions ----
+//
+// With p(i) the parent of node i, the mask of i is {i} and the mask of p(i), its position
+// past + the number of ancestors.  A thread takes a node and walks up its ancestors.
+// A parent is a lower node than its child (anything else is a root), so the walk ends,
+// and the mask's bits come in falling order: one word at a time is kept in a register.
+
+constexpr int kTreeThreads = 128;
+
+__global__ void __launch_bounds__(kTreeThreads)
+paged_tree_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict__ parents, uint32_t* __restrict__ mask,
+                  int64_t mask_stride, int32_t mask_words, int32_t* __restrict__ positions) {
+  const int32_t b = blockIdx.x;
+  const int32_t row0 = cu_at(a, b), n = cu_at(a, b + 1) - row0;
+  if (n <= 0) return;
+  const int32_t past = seq_len_at(a, b) - n;
+  bool odd = false;
+  for (int32_t i = blockIdx.y * kTreeThreads + threadIdx.x; i < n; i += gridDim.y * kTreeThreads) {
+    uint32_t* out = mask != nullptr ? mask + int64_t(row0 + i) * mask_stride : nullptr;
+    int32_t word = mask_words - 1;  // the lowest word that is not stored yet
+    uint32_t bits = 0;
+    int32_t depth = -1;
+    for (int32_t at = i; at >= 0; ++depth) {
+      if (mask != nullptr) {
+        const int32_t w = at >> 5;
+        odd |= w >= mask_words;
+        for (; word > w; --word) {
+          out[word] = bits;
+          bits = 0;
+        }
+        if (word == w) bits |= 1u << (at & 31);
+      }
+      const int32_t up = __ldg(parents + row0 + at);
+      odd |= up >= at;
+      at = up < at ? up : -1;
+    }
+    if (mask != nullptr) {
+      for (; word >= 0; --word) {
+        out[word] = bits;
+        bits = 0;
+      }
+    }
+    if (positions != nullptr) positions[row0 + i] = past + depth;
+  }
+  if (odd && a.status) atomicOr(a.status, SMLA_STATUS_INDEX_OOB);
+}
+
+// ---- the accepted path ----
+//
+// Record of node path[i] -> position past + i.  The path rises, so path[i] >= i: a
+// record's new place is never that of a node that comes later in the path, and 32 steps
+// of the path at a time may be moved one after the other, each batch read whole
+// before it is written.
+
+constexpr int kAcceptWarps = 8;
+constexpr int kPerWarp = 32 / kAcceptWarps;
+constexpr int kRecordChunks = kRecordBytes / 16;  // 41: a lane's one or two
+
+__global__ void __launch_bounds__(32 * kAcceptWarps)
+paged_accept_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict__ path, int64_t path_stride,
+                    int32_t path_len, int32_t* new_lens) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t b = blockIdx.x;
+  const int32_t row0 = cu_at(a, b), n = max(cu_at(a, b + 1) - row0, 0);
+  // (new_lens may be seq_lens: not through the read-only path)
+  const int32_t past = max(*reinterpret_cast<const volatile int32_t*>(a.seq_lens + b), 0) - n;
+  const int32_t* steps = path + int64_t(b) * path_stride;
+  int32_t accepted = 0, before = -1;
+  for (int32_t i0 = 0; i0 < path_len; i0 += 32) {
+    // lane l: step i0 + l; the path ends at the first step that is no higher node
+    const int32_t i = i0 + lane;
+    const int32_t node = i < path_len ? __ldg(steps + i) : -1;
+    int32_t last = __shfl_up_sync(0xffffffffu, node, 1);
+    if (lane == 0) last = before;
+    const uint32_t bad = __ballot_sync(0xffffffffu, node < 0 || node >= n || node <= last);
+    const int32_t good = bad ? __ffs(bad) - 1 : 32;
+    if (warp == 0 && lane == good && node >= 0 && a.status) atomicOr(a.status, SMLA_STATUS_INDEX_OOB);
+    uint8_t* from = nullptr;
+    uint8_t* to = nullptr;
+    if (lane < good && node != i && lane / kPerWarp == warp) {
+      from = record_at(a, b, past + node);
+      to = record_at(a, b, past + i);
+    }
+    uint4 v[kPerWarp][2];
+    uint8_t* dst[kPerWarp];
+#pragma unroll
+    for (int k = 0; k < kPerWarp; ++k) {
+      const int src_lane = warp * kPerWarp + k;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(from), src_lane));
+      dst[k] = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(to), src_lane));
+      if (src == nullptr) dst[k] = nullptr;
+      if (dst[k] == nullptr) continue;
+      v[k][0] = *reinterpret_cast<const uint4*>(src + lane * 16);
+      if (lane < kRecordChunks - 32) v[k][1] = *reinterpret_cast<const uint4*>(src + 512 + lane * 16);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPerWarp; ++k) {
+      if (dst[k] == nullptr) continue;
+      *reinterpret_cast<uint4*>(dst[k] + lane * 16) = v[k][0];
+      if (lane < kRecordChunks - 32) *reinterpret_cast<uint4*>(dst[k] + 512 + lane * 16) = v[k][1];
+    }
+    accepted += good;
+    if (good < 32) break;
+    before = __shfl_sync(0xffffffffu, node, 31);
+  }
+  __syncthreads();  // (every thread has read the length)
+  if (threadIdx.x == 0) new_lens[b] = max(past + accepted, 0);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tree(const smla_paged_batch& b, const int32_t* parents, uint32_t* mask, int64_t mask_stride,
+                              int32_t mask_words, int32_t* positions, cudaStream_t st) {
+  const PagedArgs a = make_paged_args(b);
+  // blocks beside each other for one sequence, by the mean of their rows
+  const int64_t mean = (b.n_rows + b.n_seqs - 1) / b.n_seqs;
+  const int64_t split = (mean + kTreeThreads - 1) / kTreeThreads;
+  const dim3 grid(unsigned(b.n_seqs), unsigned(split < 1024 ? split : 1024));
+  paged_tree_kernel<<<grid, kTreeThreads, 0, st>>>(a, parents, mask, mask_stride, mask_words, positions);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_accept(const smla_paged_batch& b, const int32_t* path, int64_t path_stride, int32_t path_len,
+                                int32_t* new_lens, cudaStream_t st) {
+  const PagedArgs a = make_paged_args(b);
+  paged_accept_kernel<<<unsigned(b.n_seqs), 32 * kAcceptWarps, 0, st>>>(a, path, path_stride, path_len, new_lens);
+  return cudaGetLastError();
+}
+
+}  // namespace smla
