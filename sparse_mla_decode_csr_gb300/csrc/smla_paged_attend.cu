@@ -1175,6 +1175,47 @@ __device__ __noinline__ void name_merge(const AttendArgs& a, const Misc* ms, int
   a.merge[worker * 4] = u.tokens * a.heads;
 }
 
+// The 256 dims of 32 rows that a warp's lanes hold in tensor memory, a row a lane, times the
+// row's factor (zeros for one without a key) as bf16 to the row's place (null: none).  Rows are not next to each other, and
+// a lane's own 16 bytes of one are half a sector: written so, a unit's O took 8 us.  32 dims of
+// the rows at a time change hands in 2 KB of shared memory instead, so that four lanes store 64
+// bytes of a row together.
+__device__ __forceinline__ void write_rows(uint32_t o_at, uint32_t buf, uint16_t* dst, float factor, bool zero) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = buf + lane * 64, swizzle = (lane >> 1) & 3;
+  uint16_t* to[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    to[i] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(dst), 8 * i + (lane >> 2)));
+#pragma unroll 1
+  for (int c = 0; c < 256; c += 32) {
+    uint32_t o[32];
+    uint32_t(&lo)[16] = *reinterpret_cast<uint32_t(*)[16]>(o);
+    uint32_t(&hi)[16] = *reinterpret_cast<uint32_t(*)[16]>(o + 16);
+    __syncwarp();  // (the last 32 dims are read; lanes may have skipped their stores)
+    tmem_ld16(o_at + c, lo);
+    tmem_ld16(o_at + c + 16, hi);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = zero ? 0u
+                    : pack_bf16x2(__uint_as_float(o[8 * k + 2 * i]) * factor,
+                                  __uint_as_float(o[8 * k + 2 * i + 1]) * factor);
+      st_shared_v4(mine + ((k ^ swizzle) << 4), v[0], v[1], v[2], v[3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2);
+      const uint4 v = ld_shared_v4(buf + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+      if (to[i] != nullptr) *reinterpret_cast<uint4*>(to[i] + c + (lane & 3) * 8) = v;
+    }
+  }
+}
+
 template <bool kTree>
 __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem, uint32_t rank,
                                              int32_t pair) {
@@ -1186,6 +1227,9 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   const uint32_t lane_base = tmem + (uint32_t(warp) << 21);  // lane 32 warp
   const uint32_t p_full = map_to(smem_u32(&ms->p_full), 0), s_empty = map_to(smem_u32(ms->s_empty), 0);
   const uint32_t p_row = base + kOffP + row * 128;
+  // this warp's share, while O is written, of the part of P that it and the warp of the
+  // same rows fill (after their barrier of the next tile)
+  const uint32_t p_area = base + kOffP + (warp & 1) * 4096 + half * 2048;
   // scores are scaled after the mask and the maximum, so the factor has to be positive
   const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
   Units units;
@@ -1195,10 +1239,10 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   // (a wait that gives up does not end this role: its warps meet at named
   // barriers, so all of them run through every tile)
   if (ms->stall) meet_after(ms, a, &ms->never, 0);
-  while (units.next(a, u)) {
+  for (bool more = units.next(a, u); more;) {
     const bool live = m < u.tokens * a.heads;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
-    const int32_t past = kTree ? seq_at(a, u.seq).past : 0;
+    const int32_t past = kTree ? units.s.past : 0;
     const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
     float ref = -INFINITY, l = 0.f;
     const int32_t t0 = u.t0, t1 = u.t1;
@@ -1289,52 +1333,47 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       __syncwarp();
       if (lane == 0) arrive_at(p_full);
     }
-    // the unit's end: row sums of the two halves, then O
+    // the unit's end: row sums of the two halves, then O.  (The next unit is looked up
+    // while the last PV runs.)
+    const Unit done = u;
+    more = units.next(a, u);
     ms->lsum[warp * 32 + lane] = l;
     group_barrier(1 + (warp & 1), 64);
     l += ms->lsum[(warp ^ 2) * 32 + lane];
     meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
-    const bool whole = u.t0 == 0 && u.t1 == u.tiles;
-    const int64_t part = 2 * int64_t(pair) + (u.t0 > 0 ? 0 : 1);
+    const bool whole = done.t0 == 0 && done.t1 == done.tiles;
+    const int64_t part = 2 * int64_t(pair) + (done.t0 > 0 ? 0 : 1);
     float factor = 1.f;
-    const int64_t tok_row = int64_t(u.row0) + tok;
-    if (live && half == 0) {
-      if (!whole) {
-        a.ml_part[(part * a.part_rows + m) * 2] = ref;
-        a.ml_part[(part * a.part_rows + m) * 2 + 1] = l;
-      }
-    }
+    const int64_t tok_row = int64_t(done.row0) + tok;
     if (whole) {
       float lse;
       finish_row(a, head, ref, l, &factor, &lse);
       if (live && half == 0 && a.lse) a.lse[tok_row * a.heads + head] = lse;
-    }
-    uint16_t* dst = a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 256 * half;
-    float* pdst = a.o_part + (part * kLatent + 256 * half) * kPairRows + m * 4;  // (see paged_merge_pair_kernel)
+      write_rows(lane_base, p_area, live ? a.out + tok_row * a.o_row + int64_t(head) * a.o_head + 256 * half : nullptr,
+                 factor, l == 0.f);
+    } else {
+      if (live && half == 0) {
+        a.ml_part[(part * a.part_rows + m) * 2] = ref;
+        a.ml_part[(part * a.part_rows + m) * 2 + 1] = l;
+      }
+      float* pdst = a.o_part + (part * kLatent + 256 * half) * kPairRows + m * 4;  // (see paged_merge_pair_kernel)
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 16) {
-      uint32_t o[16];
-      __syncwarp();  // (dead lanes skip the stores, and the load is the whole warp's)
-      tmem_ld16(lane_base + c, o);
-      tmem_wait_ld();
-      if (live && whole) {
-        uint32_t v[8];
+      for (int c = 0; c < 256; c += 16) {
+        uint32_t o[16];
+        __syncwarp();  // (dead lanes skip the stores, and the load is the whole warp's)
+        tmem_ld16(lane_base + c, o);
+        tmem_wait_ld();
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = l == 0.f ? 0u
-                          : pack_bf16x2(__uint_as_float(o[2 * i]) * factor, __uint_as_float(o[2 * i + 1]) * factor);
-        *reinterpret_cast<uint4*>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(v[4], v[5], v[6], v[7]);
-      } else if (live) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<uint4*>(pdst + (c + i) * kPairRows) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<uint4*>(pdst + (c + i) * kPairRows) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        }
       }
     }
     tc_fence_before();
-    if (!whole && u.t0 > 0 && u.t1 == u.tiles && rank == 0 && threadIdx.x == 0) {
-      name_merge(a, ms, pair, u);
+    if (!whole && done.t0 > 0 && done.t1 == done.tiles && rank == 0 && threadIdx.x == 0) {
+      name_merge(a, ms, pair, done);
     }
   }
 }
@@ -1459,7 +1498,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const bool live = mine && m < rows;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
-    const int32_t past = kTree ? seq_at(a, u.seq).past : 0;
+    const int32_t past = kTree ? units.s.past : 0;
     const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
     float ref = -INFINITY, l = 0.f;
     for (int32_t t = t0; t < t1; ++t, ++g) {
@@ -1797,7 +1836,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
     const int32_t key0 = t0 * kTileKeys, stop = t1 * kTileKeys, end = min(u.end, stop);
     const bool live = mine && m < rows;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, end), 0) : end;
-    const int32_t past = kTree ? seq_at(a, u.seq).past : 0;
+    const int32_t past = kTree ? units.s.past : 0;
     const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
     float ref = -INFINITY, l = 0.f;
     // q (every warp has seen the last QK and PV of the unit before done)
