@@ -28,8 +28,8 @@
 // peer's (both are 128-byte-swizzled rows of 64 dims, so a 32-key block is one
 // contiguous piece of 4 KB).
 //
-// Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 issue MMAs (even CTA
-// only), 15 copier.  Per tile g (stage g & 1):
+// Warps (16): 0-3 softmax and epilogue, 4-11 loaders, 12-14 issue MMAs (in the even CTA;
+// 12 of the odd one hands out the units), 15 copier.  Per tile g (stage g & 1):
 //   loaders   two groups of four warps take turns at the tiles, a warp 8 of the
 //             CTA's 32 keys: records into registers, dequantised there, and as soon
 //             as QK(g - 2) and the copies out of its K are done, stored.  What a
@@ -88,7 +88,9 @@ constexpr int kFirstLoader = 4;
 constexpr int kIssuerQk = 12;  // and 13
 constexpr int kIssuerPv = 14;
 constexpr int kCopier = 15;
+constexpr int kScheduler = 12;  // (of the odd CTA)
 constexpr int kAttendThreads = 16 * 32;
+constexpr int kLoaderRegs = 160, kIssuerRegs = 64;  // see paged_attend_kernel
 constexpr int kStageK = 9 * kOwnKeys * 128;   // nine 64-dim blocks of 128-byte rows
 constexpr int kStageV = 4 * kTileKeys * 128;  // four 64-dim blocks
 constexpr int kVBlock = kTileKeys * 128;
@@ -125,6 +127,7 @@ constexpr uint32_t kTmemS = 256;              // the S buffers, behind O's 256 c
 constexpr int kPairStart = 8, kNarrowStart = 2, kFewStart = 4;
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kJobs = 4;  // units ahead: the loaders look up to three tiles past the softmax warps
 constexpr uint32_t kIdescQK = idesc_bf16(kPairRows, kTileKeys, 0, 0);
 constexpr uint32_t kIdescPV = idesc_bf16(kPairRows, 256, 0, 1);
 
@@ -161,11 +164,16 @@ struct Misc {
   int32_t first_seq, first_j;
   int64_t first_slot, beg, end, total;
   int64_t warp_sum[16];
+  // pair and narrow kernels: the units ahead, in a ring (see scheduler_role)
+  uint4 job[kJobs][3];
+  uint64_t job_full[kJobs], job_empty[kJobs];
+  int32_t progress;  // tiles that the softmax warps have come to; INT32_MAX: they are done
+  int32_t stop;
   float tmax[2][128];
   float lsum[128];
   float alpha[2][kCtaRows], factor[kCtaRows];  // narrow kernel: per row
   // per tile: a byte per 8 keys, bit: a key before the end that has no record
-  uint8_t flags[4][kTileKeys / 8];
+  alignas(8) uint8_t flags[4][kTileKeys / 8];  // (read eight at a time)
   uint8_t flags_few[4][16];  // few-row kernel: 12 are used
 };
 constexpr int kAttendSmem = kOffMisc + int(sizeof(Misc));
@@ -292,7 +300,7 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
 }
 
 // Gives up the pipeline of both CTAs (see wait_for).
-__device__ __noinline__ void give_up(Misc* ms, int32_t* status) {
+__device__ __forceinline__ void give_up(Misc* ms, int32_t* status) {
   if (atomicExch(&ms->dead, 1) == 0 && status) atomicOr(status, SMLA_STATUS_TIMEOUT);
   uint32_t ctas;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
@@ -328,6 +336,25 @@ __device__ __forceinline__ bool wait_for(Misc* ms, const AttendArgs& a, uint64_t
 // The same for a whole warp: one answer for all lanes.
 __device__ __forceinline__ bool warp_wait(Misc* ms, const AttendArgs& a, uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_for(ms, a, bar, parity));
+}
+
+// The pair kernel's waits, whose limit its scheduler keeps (see scheduler_role): it
+// sets `dead` in both CTAs once the softmax warps get no further.  Short code, so that it
+// can stand in the roles' loops; thread_wait for one thread, pair_wait for a warp.  (`dead`
+// is looked at every 32nd time: shared memory is what bounds the kernel.)
+__device__ __forceinline__ bool thread_wait(Misc* ms, uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if ((i & 31u) == 0 && *reinterpret_cast<volatile int32_t*>(&ms->dead)) return false;
+  return true;
+}
+__device__ __forceinline__ bool pair_wait(Misc* ms, uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, thread_wait(ms, bar, parity));
+}
+
+// For a softmax warp of the pair, which goes on in any case (see meet_after).
+__device__ __forceinline__ void meet_pair(Misc* ms, uint64_t* bar, uint32_t parity) {
+  thread_wait(ms, bar, parity);
+  __syncwarp();
 }
 
 // The same for a warp that goes on in any case (its role ends with the last tile, also
@@ -445,9 +472,7 @@ struct Units {
   }
 
   // The next unit of this worker; false when there is none.
-  __device__ __noinline__ bool next(const AttendArgs& a, Unit& u) { return next_inline(a, u); }
-
-  __device__ __forceinline__ bool next_inline(const AttendArgs& a, Unit& u) {
+  __device__ __forceinline__ bool next(const AttendArgs& a, Unit& u) {
     while (slot < end && seq < a.b.n_seqs) {
       if (j >= s.tiles) {
         // the next sequence; from an empty one in doubling steps, over boundaries that are
@@ -477,6 +502,116 @@ struct Units {
     return false;
   }
 };
+
+// A unit as the roles of the pair and narrow kernels get it.
+struct Job {
+  int32_t tokens;  // 0: there is no more
+  int32_t seq, row0, pos0, end, t0, t1;
+  int32_t past;    // position of the sequence's first token row
+  int32_t whole;   // the row tile's only part
+  int32_t first;   // of a row tile's last part: the worker that holds its first one; else -1
+};
+
+__device__ __forceinline__ void read_job(const Misc* ms, uint32_t n, Job& u) {
+  const uint32_t at = smem_u32(ms->job[n % kJobs]);
+  const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 16), c = ld_shared_v4(at + 32);
+  u.tokens = a.x, u.seq = a.y, u.row0 = a.z, u.pos0 = a.w;
+  u.end = b.x, u.t0 = b.y, u.t1 = b.z, u.past = b.w;
+  u.whole = c.x, u.first = c.y;
+}
+
+__device__ __forceinline__ int32_t job_row(const Misc* ms, uint32_t n) { return int32_t(ld_shared_u32(smem_u32(&ms->job[n % kJobs][0].z))); }
+
+// The next unit, n counting them: for a softmax warp, another role's warp, the copier's
+// thread.  False when there is none, or after a wait that gave up.  (The softmax warps of a
+// pair that has given up go through all units all the same, in step.)
+__device__ __forceinline__ bool next_softmax(Misc* ms, uint32_t& n, Job& u) {
+  bool got;
+  while (!(got = mbar_try_wait(&ms->job_full[n % kJobs], (n / kJobs) & 1)))
+    if (*reinterpret_cast<volatile int32_t*>(&ms->stop)) break;
+  if (!__all_sync(0xffffffffu, got)) return false;
+  read_job(ms, n++, u);
+  return u.tokens > 0;
+}
+__device__ __forceinline__ bool next_unit(Misc* ms, uint32_t& n, Job& u) {
+  if (!pair_wait(ms, &ms->job_full[n % kJobs], (n / kJobs) & 1)) return false;
+  read_job(ms, n++, u);
+  return u.tokens > 0;
+}
+__device__ __forceinline__ bool next_thread(Misc* ms, uint32_t& n, Job& u) {
+  if (!thread_wait(ms, &ms->job_full[n % kJobs], (n / kJobs) & 1)) return false;
+  read_job(ms, n++, u);
+  return u.tokens > 0;
+}
+
+// One thread (of the odd CTA) finds the pair's units and hands them to the roles of both
+// CTAs, kJobs ahead of the softmax warps.  (Each role looking units up by itself cost up to
+// 10,000 cycles at each unit's end, three quarters of them instruction fetches: the roles'
+// loops leave nothing else in the instruction cache.)  A slot of the ring is free once
+// the softmax warps are through with its unit's tiles, when every other role is too.
+//
+// It also keeps the limit of all waits: when the softmax warps get no further for longer,
+// it sets `dead` in both CTAs, which ends every other role and lets the softmax warps run
+// through the rest without waiting; should they not, `stop` ends them.
+__device__ __forceinline__ void scheduler_role(const AttendArgs& a, Misc* ms) {
+  Units units;
+  units.start(a, ms);
+  const int64_t G = max(min(int64_t(a.workers), ms->total), int64_t(1));
+  // until the softmax warps have freed the slot of unit n - kJobs, or (n = 0) are done
+  int32_t seen = -1;
+  uint64_t since = globaltimer(), limit = ms->wait_ns;
+  auto wait = [&](uint32_t n) {
+    for (;;) {
+      for (uint32_t i = 0; i < 64; ++i) {
+        if (n != 0 && mbar_try_wait(&ms->job_empty[n % kJobs], ((n - kJobs) / kJobs) & 1)) return true;
+        if (n == 0 && *reinterpret_cast<volatile int32_t*>(&ms->progress) == INT32_MAX) return true;
+        __nanosleep(100);
+      }
+      const uint64_t now = globaltimer();
+      const int32_t p = *reinterpret_cast<volatile int32_t*>(&ms->progress);
+      if (p != seen) {
+        seen = p;
+        since = now;
+      } else if (now - since > limit) {
+        if (limit != ms->wait_ns) return false;
+        give_up(ms, a.b.status);
+        limit = ms->wait_ns + kWaitNs;
+      }
+    }
+  };
+  bool more = true, fine = true;
+  for (uint32_t n = 0; more && fine; ++n) {
+    const uint32_t slot = n % kJobs;
+    Unit u;
+    more = units.next(a, u);
+    if (n >= kJobs) fine = wait(n);
+    if (!fine) break;
+    uint32_t w[12];
+    w[0] = more ? u.tokens : 0, w[1] = u.seq, w[2] = u.row0, w[3] = u.pos0;
+    w[4] = u.end, w[5] = u.t0, w[6] = u.t1, w[7] = units.s.past;
+    w[8] = u.t0 == 0 && u.t1 == u.tiles;
+    w[9] = more && u.t0 > 0 && u.t1 == u.tiles ? int32_t(((u.slot + 1) * G - 1) / ms->total) : -1;
+    w[10] = w[11] = 0;
+    const uint32_t at = smem_u32(ms->job[slot]), bar = smem_u32(&ms->job_full[slot]);
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r) {
+      const uint32_t to = map_to(at, r), full = map_to(bar, r);
+      asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(full), "r"(48)
+                   : "memory");
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        asm volatile(
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to + 16 * i),
+            "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3]), "r"(full)
+            : "memory");
+    }
+  }
+  if (fine) fine = wait(0);
+  if (!fine) {
+    ms->stop = 1;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to(smem_u32(&ms->stop), 0)), "r"(1) : "memory");
+  }
+}
 
 // The worker's range of slots and the row tile it starts in, by all threads.
 template <int kThreads>
@@ -738,28 +873,37 @@ __device__ __noinline__ void load_q_tmem(const AttendArgs& a, uint32_t buf, uint
 
 // A loader warp's cursor over the pair's tiles and the addresses of its 8 keys there.
 struct Cursor {
-  Units units;
-  bool more;
-  int32_t t, t0, t1, end, seq, row0, rows;  // of the cursor's unit
+  uint32_t n;         // units up to the cursor's
+  bool more, starts;  // starts: at the unit's first tile
+  int32_t t, t1, seq, end;  // the tile; of its unit
 
-  __device__ __forceinline__ void next_unit(const AttendArgs& a) {
-    Unit u;
-    more = units.next(a, u);
-    t = t0 = u.t0, t1 = u.t1, end = u.end, seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
+  __device__ __forceinline__ void start(const AttendArgs& a, Misc* ms) {
+    n = 0;
+    take_unit(a, ms);
   }
-  __device__ __forceinline__ void step(const AttendArgs& a) {
-    if (more && ++t == t1) next_unit(a);
+  __device__ __forceinline__ void take_unit(const AttendArgs& a, Misc* ms) {
+    Job u;
+    more = next_unit(ms, n, u);
+    starts = true;
+    t = u.t0, t1 = u.t1, seq = u.seq, end = u.end;
+  }
+  __device__ __forceinline__ void step(const AttendArgs& a, Misc* ms) {
+    if (!more) return;
+    starts = false;
+    if (++t == t1) take_unit(a, ms);
   }
   // Page id and offset at the cursor: lanes 0-7 the warp's keys, lanes 8-15 the peer
   // warp's (both CTAs need to know which keys have no record).  The id
   // is first looked at when the loads set out; in: a key before the end.
-  __device__ __forceinline__ void look_up(const AttendArgs& a, int32_t rank, int w, int32_t& id, int32_t& offset,
-                                          bool& in) const {
+  __device__ __forceinline__ void look_up(const AttendArgs& a, const Misc* ms, int32_t rank, int w, int32_t& id,
+                                          int32_t& offset, bool& in) const {
     const int lane = threadIdx.x & 31;
     id = -1;
+    in = false;
+    if (!more) return;
     const int32_t owner = rank ^ (lane >> 3);
     const int32_t pos = t * kTileKeys + owner * kOwnKeys + w * kKeysPerWarp + (lane & 7);
-    in = more && lane < 2 * kKeysPerWarp && pos < end;  // (the end lies within the table)
+    in = lane < 2 * kKeysPerWarp && pos < end;  // (the end lies within the table)
     if (in) {
       const uint32_t page = page_of(a.b, uint32_t(pos));
       offset = pos - int32_t(page) * a.b.page_size;
@@ -778,7 +922,7 @@ struct KeyCursor {
 
   __device__ __forceinline__ void next_unit(const AttendArgs& a) {
     Unit u;
-    more = units.next_inline(a, u);
+    more = units.next(a, u);
     key = key0 = u.t0 * kTileKeys, stop = u.t1 * kTileKeys, end = min(u.end, stop);
     seq = u.seq, row0 = u.row0, rows = u.tokens * a.heads;
   }
@@ -829,9 +973,8 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   // loads set out as soon as its registers are free and land while the other group
   // works.
   Cursor c;
-  c.units.start(a, ms);
-  c.next_unit(a);
-  if (group == 1) c.step(a);
+  c.start(a, ms);
+  if (group == 1) c.step(a, ms);
   // rec: lane j's record (0: none)
   auto issue = [&](uint64_t rec, Raw& r) {
     const uint64_t first = __shfl_sync(0xffffffffu, rec, 0);
@@ -850,24 +993,26 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
   Raw raw;
   int32_t id, offset = 0;
   bool in;
-  c.look_up(a, int32_t(rank), w, id, offset, in);
+  c.look_up(a, ms, int32_t(rank), w, id, offset, in);
   for (uint32_t g = group; c.more; g += 2) {
     const uint64_t rec = record_address(a, id, offset);
     const uint32_t holes = __ballot_sync(0xffffffffu, rec == 0 && in);
     issue(rec, raw);
-    if (c.t == c.t0) {
+    if (c.starts) {
       // q of the unit, once the last QK of the unit before is done.  (A parity tells
       // a phase from its neighbours only, so QK(g - 3) has to be known as past, which
       // is on the other group's barrier: QK(g - 2) says so.)
-      if (g >= 2 && !warp_wait(ms, a, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
-      if (g >= 1 && !warp_wait(ms, a, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
-      load_q(a, base + kOffQ, rank, w, kLoaderWarps, c.row0, c.rows, 1);
+      if (g >= 2 && !pair_wait(ms, &ms->qk_done[group], ((g - 2) >> 1) & 1)) return;
+      if (g >= 1 && !pair_wait(ms, &ms->qk_done[group ^ 1], ((g - 1) >> 1) & 1)) return;
+      Job u;
+      read_job(ms, c.n - 1, u);
+      load_q(a, base + kOffQ, rank, w, kLoaderWarps, u.row0, u.tokens * a.heads, 1);
       finish_q();
       if (lane == 0) arrive_at(q_full);
     }
-    c.step(a);
-    c.step(a);
-    c.look_up(a, int32_t(rank), w, id, offset, in);
+    c.step(a, ms);
+    c.step(a, ms);
+    c.look_up(a, ms, int32_t(rank), w, id, offset, in);
     // convert the landed records
     uint32_t v[kKeysPerWarp][2][4];
     uint32_t odd = 0, top = 0;
@@ -904,7 +1049,7 @@ __device__ __forceinline__ void loader_role(const AttendArgs& a, Misc* ms, uint3
     }
     if (g >= 2) {
       const uint32_t parity = ((g - 2) >> 1) & 1;
-      if (!warp_wait(ms, a, &ms->qk_done[group], parity) || !warp_wait(ms, a, &ms->v_full[group], parity)) return;
+      if (!pair_wait(ms, &ms->qk_done[group], parity) || !pair_wait(ms, &ms->v_full[group], parity)) return;
     }
 #pragma unroll
     for (int j = 0; j < kKeysPerWarp; ++j) {
@@ -1042,13 +1187,12 @@ __device__ __forceinline__ void copier_role(const AttendArgs& a, Misc* ms, uint3
     full[r] = map_to(smem_u32(ms->v_full), r);
     v_at[r] = map_to(base + kOffV + rank * (kOwnKeys * 128), r);
   }
-  Units units;
-  units.start(a, ms);
   bool more;
+  uint32_t n = 0;
   int32_t t, t1;
   auto next_unit = [&]() {
-    Unit u;
-    more = units.next(a, u);
+    Job u;
+    more = next_thread(ms, n, u);
     t = u.t0, t1 = u.t1;
   };
   next_unit();
@@ -1100,18 +1244,15 @@ __device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, ui
                                                uint32_t which) {
   const uint64_t q0 = smem_desc(base + kOffQ, 16, 1024, kSw128);
   const uint64_t k0 = smem_desc(base + kOffK, 16, 1024, kSw128);
-  Units units;
-  units.start(a, ms);
-  Unit u;
-  uint32_t g = 0, n_units = 0;
-  while (units.next(a, u)) {
-    if (!warp_wait(ms, a, &ms->q_full, n_units & 1)) return;
-    ++n_units;
+  Job u;
+  uint32_t g = 0, n = 0;
+  while (next_unit(ms, n, u)) {
+    if (!pair_wait(ms, &ms->q_full, (n - 1) & 1)) return;
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      if (!warp_wait(ms, a, &ms->k_full[stage], (g >> 1) & 1)) return;
-      if (g >= 2 && !warp_wait(ms, a, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
+      if (!pair_wait(ms, &ms->k_full[stage], (g >> 1) & 1)) return;
+      if (g >= 2 && !pair_wait(ms, &ms->s_empty[stage], ((g - 2) >> 1) & 1)) return;
       tc_fence_after();
       const uint32_t d = tmem + kTmemS + 64 * stage + 32 * which;
       const uint64_t qd = q0 + which * 2, kd = k0 + uint64_t((stage * kStageK) >> 4) + which * 2;
@@ -1131,16 +1272,14 @@ __device__ __forceinline__ void issuer_qk_role(const AttendArgs& a, Misc* ms, ui
 __device__ __forceinline__ void issuer_pv_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem) {
   const uint64_t p0 = smem_desc(base + kOffP, 16, 1024, kSw128);
   const uint64_t v0 = smem_desc(base + kOffV, kVBlock, 1024, kSw128);
-  Units units;
-  units.start(a, ms);
-  Unit u;
-  uint32_t g = 0;
-  while (units.next(a, u)) {
+  Job u;
+  uint32_t g = 0, n = 0;
+  while (next_unit(ms, n, u)) {
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
-      if (!warp_wait(ms, a, &ms->v_full[stage], (g >> 1) & 1)) return;
-      if (!warp_wait(ms, a, &ms->p_full, g & 1)) return;
+      if (!pair_wait(ms, &ms->v_full[stage], (g >> 1) & 1)) return;
+      if (!pair_wait(ms, &ms->p_full, g & 1)) return;
       tc_fence_after();
       const uint64_t vd = v0 + uint64_t((stage * kStageV) >> 4);
       if (elect_one()) {
@@ -1168,11 +1307,14 @@ __device__ __forceinline__ void finish_row(const AttendArgs& a, int32_t head, fl
 
 // The last part of a row tile: the merge kernel joins the parts from the worker
 // that holds its first key tile up to this one.
+__device__ __forceinline__ void name_merge(const AttendArgs& a, int32_t worker, int32_t first, int32_t row0, int32_t tokens) {
+  a.merge[worker * 4 + 1] = row0;
+  a.merge[worker * 4 + 2] = first;
+  a.merge[worker * 4] = tokens * a.heads;
+}
 __device__ __noinline__ void name_merge(const AttendArgs& a, const Misc* ms, int32_t worker, const Unit& u) {
   const int64_t G = max(min(int64_t(a.workers), ms->total), int64_t(1));
-  a.merge[worker * 4 + 1] = u.row0;
-  a.merge[worker * 4 + 2] = int32_t(((u.slot + 1) * G - 1) / ms->total);
-  a.merge[worker * 4] = u.tokens * a.heads;
+  name_merge(a, worker, int32_t(((u.slot + 1) * G - 1) / ms->total), u.row0, u.tokens);
 }
 
 // The 256 dims of 32 rows that a warp's lanes hold in tensor memory, a row a lane, times the
@@ -1232,27 +1374,26 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
   const uint32_t p_area = base + kOffP + (warp & 1) * 4096 + half * 2048;
   // scores are scaled after the mask and the maximum, so the factor has to be positive
   const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
-  Units units;
-  units.start(a, ms);
-  Unit u;
-  uint32_t g = 0;
+  const uint32_t job_empty = map_to(smem_u32(ms->job_empty), 1);
+  Job u;
+  uint32_t g = 0, n = 0;
   // (a wait that gives up does not end this role: its warps meet at named
   // barriers, so all of them run through every tile)
-  if (ms->stall) meet_after(ms, a, &ms->never, 0);
-  for (bool more = units.next(a, u); more;) {
+  if (ms->stall) meet_pair(ms, &ms->never, 0);
+  while (next_softmax(ms, n, u)) {
     const bool live = m < u.tokens * a.heads;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
-    const int32_t past = kTree ? units.s.past : 0;
-    const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
+    const int32_t past = kTree ? u.past : 0;
     float ref = -INFINITY, l = 0.f;
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
+      if (threadIdx.x == 0) *reinterpret_cast<volatile int32_t*>(&ms->progress) = int32_t(g);
       const int32_t key0 = t * kTileKeys + 32 * half;
       const bool nodes = kTree && key0 + 32 > past;  // (the same for all rows)
       uint32_t tree = ~0u;
-      if (nodes && live) tree = tree_keys(mask, a.mask_words, past, key0);
-      meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
+      if (nodes && live) tree = tree_keys(a.mask + (int64_t(job_row(ms, n - 1)) + tok) * a.mask_stride, a.mask_words, past, key0);
+      meet_pair(ms, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
       uint32_t s[64];  // the two accumulators' 32 columns
       {
@@ -1311,7 +1452,7 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
         p[c] = pack_bf16x2(y0, y1);
       }
       l = l * alpha + (sum0 + sum1);
-      if (g > 0) meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      if (g > 0) meet_pair(ms, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
       if (t > t0 && __any_sync(0xffffffffu, move)) {
         tc_fence_after();
 #pragma unroll 1
@@ -1333,19 +1474,20 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       __syncwarp();
       if (lane == 0) arrive_at(p_full);
     }
-    // the unit's end: row sums of the two halves, then O.  (The next unit is looked up
-    // while the last PV runs.)
-    const Unit done = u;
-    more = units.next(a, u);
+    // the unit's end: row sums of the two halves, then O.  (The rest of the unit is read
+    // again rather than kept: the loop has no registers left.)
+    read_job(ms, n - 1, u);
     ms->lsum[warp * 32 + lane] = l;
     group_barrier(1 + (warp & 1), 64);
     l += ms->lsum[(warp ^ 2) * 32 + lane];
-    meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    meet_pair(ms, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
-    const bool whole = done.t0 == 0 && done.t1 == done.tiles;
-    const int64_t part = 2 * int64_t(pair) + (done.t0 > 0 ? 0 : 1);
+    __syncwarp();
+    if (lane == 0) arrive_at(job_empty + 8 * ((n - 1) % kJobs));
+    const bool whole = u.whole != 0;
+    const int64_t part = 2 * int64_t(pair) + (u.t0 > 0 ? 0 : 1);
     float factor = 1.f;
-    const int64_t tok_row = int64_t(done.row0) + tok;
+    const int64_t tok_row = int64_t(u.row0) + tok;
     if (whole) {
       float lse;
       finish_row(a, head, ref, l, &factor, &lse);
@@ -1372,10 +1514,9 @@ __device__ __forceinline__ void softmax_role(const AttendArgs& a, Misc* ms, uint
       }
     }
     tc_fence_before();
-    if (!whole && done.t0 > 0 && done.t1 == done.tiles && rank == 0 && threadIdx.x == 0) {
-      name_merge(a, ms, pair, done);
-    }
+    if (u.first >= 0 && rank == 0 && threadIdx.x == 0) name_merge(a, pair, u.first, u.row0, u.tokens);
   }
+  if (threadIdx.x == 0) *reinterpret_cast<volatile int32_t*>(&ms->progress) = INT32_MAX;
 }
 
 template <bool kTree>
@@ -1405,6 +1546,12 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
       mbar_init(&ms->qk_done[i], 2);
       mbar_init(&ms->pv_done[i], 1);
     }
+    for (int i = 0; i < kJobs; ++i) {
+      mbar_init(&ms->job_full[i], 1);
+      mbar_init(&ms->job_empty[i], 8);  // (used in the odd CTA)
+    }
+    ms->progress = 0;
+    ms->stop = 0;
     mbar_init(&ms->q_full, 2 * kLoaderWarps);
     mbar_init(&ms->p_full, 8);
     mbar_init(&ms->drain, 3);
@@ -1426,11 +1573,29 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
+  auto leave = [&]() {
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+  };
+  // The loaders' registers hold a tile on its way and one being converted: at the launch's 128
+  // some spill (16 bytes cost the chunk above 2470 -> 2680 us), so the four warps that issue
+  // and copy give them theirs: 128 + 2 * 160 + 64 = 4 * 128.  (ptxas wants no calls where there
+  // are fewer registers, no function called with both counts, and no code behind shared.)
   if (warp < kFirstLoader) {
     softmax_role<kTree>(a, ms, base, tmem, rank, pair);
-  } else if (warp < kIssuerQk) {
+    leave();
+    return;
+  }
+  if (warp < kIssuerQk) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLoaderRegs));
     loader_role(a, ms, base, rank);
-  } else if (warp == kCopier) {
+    leave();
+    return;
+  }
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssuerRegs));
+  if (warp == kCopier) {
     if ((threadIdx.x & 31) == 0) copier_role(a, ms, base, rank);
   } else if (rank == 0) {
     if (warp == kIssuerPv) issuer_pv_role(a, ms, base, tmem);
@@ -1445,11 +1610,10 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
                    : "memory");
       if (!mbar_wait(&ms->drain, 0, kWaitNs)) give_up(ms, a.b.status);
     }
+  } else if (warp == kScheduler) {
+    if ((threadIdx.x & 31) == 0) scheduler_role(a, ms);
   }
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();
+  leave();
   tc_fence_after();
   if (warp == kCopier) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -1494,7 +1658,7 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   Unit u;
   uint32_t g = 0;
   if (ms->stall) meet_after(ms, a, &ms->never, 0);
-  while (units.next_inline(a, u)) {
+  while (units.next(a, u)) {
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const bool live = mine && m < rows;
     const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
@@ -1659,7 +1823,7 @@ __device__ __forceinline__ void narrow_qk_role(const AttendArgs& a, Misc* ms, ui
   units.start(a, ms);
   Unit u;
   uint32_t g = 0, n_units = 0;
-  while (units.next_inline(a, u)) {
+  while (units.next(a, u)) {
     const int32_t t0 = u.t0, t1 = u.t1;
     if (!warp_wait(ms, a, &ms->q_full, n_units++ & 1)) return;
     for (int32_t t = t0; t < t1; ++t, ++g) {
@@ -1692,7 +1856,7 @@ __device__ __forceinline__ void narrow_pv_role(const AttendArgs& a, Misc* ms, ui
   units.start(a, ms);
   Unit u;
   uint32_t g = 0;
-  while (units.next_inline(a, u)) {
+  while (units.next(a, u)) {
     const int32_t t0 = u.t0, t1 = u.t1;
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
@@ -1831,7 +1995,7 @@ __device__ __forceinline__ void few_compute_role(const AttendArgs& a, Misc* ms, 
   uint32_t g = 0;
   // (a wait that gives up does not end this role: its warps meet at named barriers)
   if (ms->stall) meet_after(ms, a, &ms->never, 0);
-  while (units.next_inline(a, u)) {
+  while (units.next(a, u)) {
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
     const int32_t key0 = t0 * kTileKeys, stop = t1 * kTileKeys, end = min(u.end, stop);
     const bool live = mine && m < rows;
