@@ -120,11 +120,12 @@ constexpr int kNarrowQk = 12;  // and 13
 constexpr int kNarrowPv = 14;  // and 15
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 256;              // the S buffers, behind O's 256 columns
-// Slots of a row tile's start, by measurement (us): the pair kernel with 1 / 4 / 8 / 12
-// at 32 drafts of 5 tokens, 64 heads: 88 / 80 / 76 / 76; the narrow kernel with 1 / 2 / 4
+// Slots of a row tile's start, by measurement (us): the pair kernel with 2 / 4 / 8
+// at 32 drafts of 5 tokens, 64 heads: 51.7 / 51.5 / 53.9, 32 trees of up to 60 nodes: 300 / 295
+// / 302; the narrow kernel with 1 / 2 / 4
 // at 4 x 64 heads: 43.7 / 42.2 / 41.3, at 64 x 64 heads over 4096: 88.2 / 86.4 / 87.9; the
 // few-row kernel with 1 / 2 / 4 at 64 x 16 heads: 53.5 / 53.2 / 51.8.
-constexpr int kPairStart = 8, kNarrowStart = 2, kFewStart = 4;
+constexpr int kPairStart = 4, kNarrowStart = 2, kFewStart = 4;
 constexpr float kMoveMargin = 8.f;            // log2 units; p <= 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kJobs = 4;  // units ahead: the loaders look up to three tiles past the softmax warps

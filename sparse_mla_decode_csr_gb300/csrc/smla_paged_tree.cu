@@ -14,46 +14,93 @@ namespace {
 // ---- masks and positions ----
 //
 // With p(i) the parent of node i, the mask of i is {i} and the mask of p(i), its position
-// past + the number of ancestors.  A thread takes a node and walks up its ancestors.
-// A parent is a lower node than its child (anything else is a root), so the walk ends,
-// and the mask's bits come in falling order: one word at a time is kept in a register.
+// past + the number of ancestors.  A thread takes a node and walks up its ancestors; a
+// parent is a lower node than its child (anything else is a root), so the walk ends, and
+// the mask's words are met from the last to the first.  The block's nodes collect 32 words
+// each in shared memory at a time, which then leave row after row.
+//
+// Bound: the walk, a chain of look-ups.  It reads a copy of the parents in shared memory that
+// holds each node's parent and grandparent, so that a look-up goes two nodes up; the bits are
+// set by shared-memory atomics, whose results nobody waits for (sequences of more than 2048
+// nodes: one node at a time, through L1).
 
 constexpr int kTreeThreads = 128;
+constexpr int kTreeWords = 32;
+constexpr int kTreePitch = kTreeWords + 1;  // (a column's threads hit different banks)
+constexpr int kStagedNodes = 2048;
 
 __global__ void __launch_bounds__(kTreeThreads)
 paged_tree_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict__ parents, uint32_t* __restrict__ mask,
                   int64_t mask_stride, int32_t mask_words, int32_t* __restrict__ positions) {
-  const int32_t b = blockIdx.x;
+  __shared__ int2 staged[kStagedNodes];  // parent and grandparent, -1: none
+  __shared__ uint32_t bits[kTreeThreads * kTreePitch];
+  const int32_t b = blockIdx.x, tid = threadIdx.x;
   const int32_t row0 = cu_at(a, b), n = cu_at(a, b + 1) - row0;
-  if (n <= 0) return;
+  const int32_t step = gridDim.y * kTreeThreads;
+  if (int32_t(blockIdx.y) * kTreeThreads >= n) return;
   const int32_t past = seq_len_at(a, b) - n;
+  const bool near = n <= kStagedNodes;
   bool odd = false;
-  for (int32_t i = blockIdx.y * kTreeThreads + threadIdx.x; i < n; i += gridDim.y * kTreeThreads) {
-    uint32_t* out = mask != nullptr ? mask + int64_t(row0 + i) * mask_stride : nullptr;
-    int32_t word = mask_words - 1;  // the lowest word that is not stored yet
-    uint32_t bits = 0;
-    int32_t depth = -1;
-    for (int32_t at = i; at >= 0; ++depth) {
-      if (mask != nullptr) {
-        const int32_t w = at >> 5;
-        odd |= w >= mask_words;
-        for (; word > w; --word) {
-          out[word] = bits;
-          bits = 0;
+  // the parent of a node, -1 for a root
+  auto parent = [&](int32_t i) {
+    const int32_t up = __ldg(parents + row0 + i);
+    odd |= up >= i;
+    return up < i && up >= 0 ? up : -1;
+  };
+  if (near) {
+#pragma unroll 4
+    for (int32_t i = tid; i < n; i += kTreeThreads) staged[i].x = parent(i);
+    __syncthreads();
+#pragma unroll 4
+    for (int32_t i = tid; i < n; i += kTreeThreads) {
+      const int32_t up = staged[i].x;
+      staged[i].y = up >= 0 ? staged[up].x : -1;
+    }
+    __syncthreads();
+  }
+  for (int32_t i0 = blockIdx.y * kTreeThreads; i0 < n; i0 += step) {
+    const int32_t i = i0 + tid;
+    int32_t at = i < n ? i : -1, depth = -1;
+    if (mask_words > 0 && at >> 5 >= mask_words) odd = true;
+    // words [w0, w0 + 32) of these nodes, from the last ones down; without a mask one round
+    const int32_t last = mask_words > 0 ? (mask_words - 1) / kTreeWords * kTreeWords : 0;
+    for (int32_t w0 = last; w0 >= 0; w0 -= kTreeWords) {
+      const int32_t words = min(mask_words - w0, kTreeWords), lo = 32 * w0;
+      for (int32_t w = 0; w < words; ++w) bits[tid * kTreePitch + w] = 0;
+      auto meet = [&](int32_t node) {
+        const int32_t w = (node >> 5) - w0;
+        if (w < words) atomicOr(&bits[tid * kTreePitch + w], 1u << (node & 31));
+        ++depth;
+      };
+      if (near) {
+        while (at >= lo) {
+          const int2 up = staged[at];
+          meet(at);
+          at = up.x;
+          if (at >= lo) {
+            meet(at);
+            at = up.y;
+          }
         }
-        if (word == w) bits |= 1u << (at & 31);
+      } else {
+        while (at >= lo) {
+          meet(at);
+          at = parent(at);
+        }
       }
-      const int32_t up = __ldg(parents + row0 + at);
-      odd |= up >= at;
-      at = up < at ? up : -1;
-    }
-    if (mask != nullptr) {
-      for (; word >= 0; --word) {
-        out[word] = bits;
-        bits = 0;
+      if (words <= 0) continue;
+      __syncthreads();
+      // a row by as many lanes as the next power of two above its words
+      const int32_t shift = words > 1 ? 32 - __clz(words - 1) : 0;
+      const int32_t w = tid & ((1 << shift) - 1), rows = min(n - i0, kTreeThreads);
+      uint32_t* out = mask + int64_t(row0 + i0) * mask_stride + w0 + w;
+      if (w < words) {
+#pragma unroll 4
+        for (int32_t r = tid >> shift; r < rows; r += kTreeThreads >> shift) out[r * mask_stride] = bits[r * kTreePitch + w];
       }
+      __syncthreads();
     }
-    if (positions != nullptr) positions[row0 + i] = past + depth;
+    if (positions != nullptr && i < n) positions[row0 + i] = past + depth;
   }
   if (odd && a.status) atomicOr(a.status, SMLA_STATUS_INDEX_OOB);
 }
