@@ -202,6 +202,8 @@ def _load():
 
 lib = _load()
 
+from . import _smla as _native  # noqa: E402  (built beside libsmla.so, which it calls)
+
 EXPORTED_SYMBOLS = ("smla_plan", "smla_decode_workspace_size", "smla_decode", "smla_decode_noalloc",
                     "smla_pack_records", "smla_paged_write", "smla_paged_read",
                     "smla_paged_attend_workspace_size", "smla_paged_attend",
@@ -382,9 +384,11 @@ def smla_pack_records(latent: torch.Tensor, rope: torch.Tensor, kv_out: torch.Te
 
 # ---- the paged cache ----
 #
-# These calls can take less time on the GPU than their checks do here, so the
-# checks read each tensor's properties once, the messages are made on failure, and
-# the C structs (PagedBatch, PagedAttendParams) are packed as bytes.
+# These calls can take less time on the GPU than their checks do here.  Well-formed calls
+# on the current stream are therefore made by _smla.so (csrc/smla_binding.cpp), which
+# answers False to all others and does nothing for them: they go through the checks
+# here, which name what is wrong.  The checks read each tensor's properties once, the
+# messages are made on failure, and the C structs are packed as bytes.
 
 _BATCH_FORMAT = "PqqiiPqPPqi4xP"
 _pack_batch = struct.Struct(_BATCH_FORMAT).pack
@@ -503,6 +507,8 @@ def smla_paged_write(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.T
     skipped and set STATUS_INDEX_OOB.  The rows' positions must lie in different
     slots.  An infinite latent takes its whole block of 128 values to the scale
     2^120, where ordinary values become zero.  See include/smla.h."""
+    if _native.write(kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status):
+        return
     _paged_copy("smla_paged_write", _write_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
 
@@ -514,6 +520,8 @@ def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: 
     [rows, 64] (bf16, f16 or f32).  Batch as smla_paged_write: row r of sequence
     b gets position seq_lens[b] - (cu_rows[b + 1] - r); masked positions give
     zeros, rows of no sequence are left as they were.  See include/smla.h."""
+    if _native.read(kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status):
+        return
     _paged_copy("smla_paged_read", _read_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
 
@@ -530,6 +538,9 @@ def smla_paged_attend_workspace_size(n_rows: int, num_heads: int, n_seqs: int, p
 
 def _attend(what: str, q, kv_cache, block_table, cu_rows, seq_lens, mask, sm_scale, sink, out, lse, stream, causal,
             status, workspace_tensor) -> None:
+    if _native.attend(kv_cache, block_table, cu_rows, seq_lens, q, sm_scale, sink, out, lse, causal, stream, status,
+                      workspace_tensor, mask):
+        return
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != QK_DIM:
         _fail(SMLA_ERR_SHAPE, what, f"q is bf16 [rows, heads, {QK_DIM}]")
     n, heads, _ = q.shape
@@ -646,6 +657,9 @@ def smla_paged_append(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.
     dims (2k, 2k + 1), or (k, k + 32) without interleaved; rope_scale
     multiplies the results.  Batch and masked rows as smla_paged_write.  See
     include/smla.h."""
+    if _native.append(kv_cache, block_table, cu_rows, seq_lens, latent, rope, turns, q_rope, q_out, positions,
+                      interleaved, rope_scale, stream, status):
+        return
     what = "smla_paged_append"
     n, dtype, ls, rs = _rows(what, latent, rope)
     if turns.dtype != torch.int64 or turns.shape != (ROPE_DIM // 2,) or not turns.is_contiguous():
@@ -699,6 +713,8 @@ def smla_paged_tree(parents: torch.Tensor, cu_rows: torch.Tensor, seq_lens: torc
     position of node 0 plus the node's depth.  A parent that is not a lower
     node, or a node that the words cannot hold, sets STATUS_INDEX_OOB.  See
     include/smla.h."""
+    if _native.tree(parents, cu_rows, seq_lens, mask, positions, stream, status):
+        return
     what = "smla_paged_tree"
     i32 = torch.int32
     if parents.dtype != i32 or cu_rows.dtype != i32 or seq_lens.dtype != i32 or parents.dim() != 1 or \
@@ -750,6 +766,8 @@ def smla_paged_accept(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows
     the position of node 0 plus the number of nodes.  An entry that is no node or
     does not rise ends the path and sets STATUS_INDEX_OOB.  n_rows: rows of the
     token tensors, which clamp cu_rows in the other calls.  See include/smla.h."""
+    if _native.accept(kv_cache, block_table, cu_rows, seq_lens, path, new_lens, n_rows, stream, status):
+        return
     what = "smla_paged_accept"
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, int(n_rows), status)
     n_seqs = seq_lens.shape[0]

@@ -53,6 +53,7 @@ TREES = [
     # lens, words, pad
     ([(1, 1)], 1, 0), ([(60, 500)] * 5, 2, 0), ([(5, 9), (0, 4), (1, 70), (33, 33), (64, 64), (65, 90)], 3, 1),
     ([(500, 700), (129, 129)], 16, 2), ([(1000, 1000)], 32, 0), ([(7, 3), (2, 0)], 1, 0), ([(3, 10)] * 300, 1, 0),
+    ([(2500, 2600), (2048, 2048), (40, 50)], 79, 1),  # more nodes than shared memory takes, more words than a round
 ]
 
 
@@ -546,3 +547,58 @@ def test_tokens_after_a_step_attend_over_what_was_accepted():
                                None, out, lse)
         outs.append((out, lse))
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# ---- the two ways into the library ----
+
+
+def test_calls_through_the_checks_in_python_give_the_same():
+    # (a stream given by hand goes through them; without one _smla.so makes the call)
+    states = []
+    for stream in (None, torch.cuda.current_stream()):
+        c = Batch([(20, 300), (9, 100), (0, 7)], 16)
+        s = step_state(c, 16, 60)
+        step(s, stream)
+        lat, rope = torch.empty(c.rows, 512, device=DEV), torch.empty(c.rows, 64, device=DEV)
+        smla.smla_paged_read(s["kv"], s["table"], s["cu"], s["sl"], lat, rope, stream)
+        smla.smla_paged_write(lat, rope, s["kv"], s["table"], s["cu"], s["sl"], stream)
+        out, lse = torch.empty_like(s["out"]), torch.empty_like(s["lse"])
+        smla.smla_paged_attend(s["q"], s["kv"], s["table"], s["cu"], s["sl"], 1 / 24, None, out, lse, stream)
+        torch.cuda.synchronize()
+        states.append([s[k] for k in ("mask", "pos", "q", "kv", "out", "lse", "new")] + [lat, rope, out, lse])
+    for a, b in zip(*states):
+        assert torch.equal(a, b)
+
+
+def test_well_formed_calls_are_taken_and_others_are_not():
+    native = smla._native
+    c = Batch([(5, 40), (3, 9)], 16)
+    s = step_state(c, 4, 61)
+    batch = (s["kv"], s["table"], s["cu"], s["sl"])
+    tree = (s["parents"], s["cu"], s["sl"], s["mask"], s["pos"])
+    append = (*batch, s["lat"], s["rope"], s["turns"], s["q_rope"], s["q"][..., 512:], s["pos"], True, 1.0)
+    attend = (*batch, s["q"], 1 / 24, None, s["out"], s["lse"], True)
+    calls = [(native.write, (*batch, s["lat"], s["rope"])), (native.read, (*batch, s["lat"].clone(), s["rope"].clone())),
+             (native.append, append), (native.tree, tree), (native.accept, (*batch, s["path"], s["new"], c.rows))]
+    for call, args in calls:
+        assert call(*args, None, None) is True and call(*args, None, s["status"]) is True
+        assert call(*args, torch.cuda.current_stream(), None) is False  # a stream by hand
+        assert call(*args, None, s["lse"]) is False                     # a status that is none
+        for i, x in enumerate(args):
+            if torch.is_tensor(x):
+                assert call(*args[:i], x.cpu(), *args[i + 1:], None, None) is False
+                assert call(*args[:i], x.double(), *args[i + 1:], None, None) is False
+                wide = torch.zeros(*x.shape[:-1], 2 * x.shape[-1], dtype=x.dtype, device=DEV)[..., ::2]
+                # (the stride of a dimension of one element, the mask's words here, says nothing)
+                assert call(*args[:i], wide, *args[i + 1:], None, None) is (x.shape[-1] == 1)
+    for mask in (None, s["mask"]):
+        assert native.attend(*attend, None, None, None, mask) is True
+        assert native.attend(*attend, torch.cuda.current_stream(), None, None, mask) is False
+        for i, x in enumerate(attend):
+            if torch.is_tensor(x):
+                assert native.attend(*attend[:i], x.cpu(), *attend[i + 1:], None, None, None, mask) is False
+                assert native.attend(*attend[:i], x.double(), *attend[i + 1:], None, None, None, mask) is False
+    assert native.attend(*attend, None, None, s["lse"].t(), None) is False  # a workspace that is not contiguous
+    assert native.attend(*attend, None, None, torch.zeros(256, dtype=torch.uint8, device=DEV), None) is False  # too small
+    assert native.attend(*batch, s["q"], 1e40, None, s["out"], s["lse"], True, None, None, None, None) is False
+    torch.cuda.synchronize()
