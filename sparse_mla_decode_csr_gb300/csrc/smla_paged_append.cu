@@ -43,9 +43,9 @@ struct AppendArgs {
   int32_t heads;
 };
 
-// Cosine and sine, times the scale, of pair `lane` at a position.
-__device__ __forceinline__ float2 rotation(const AppendArgs& a, int32_t pos) {
-  const uint64_t turn = __ldg(a.turns + (threadIdx.x & 31)) * uint64_t(int64_t(pos));
+// Cosine and sine, times the scale, of a pair that turns so far a position.
+__device__ __forceinline__ float2 rotation(const AppendArgs& a, uint64_t turns, int32_t pos) {
+  const uint64_t turn = turns * uint64_t(int64_t(pos));
   float s, c;
   sincospif(float(int32_t(turn >> 32)) * 0x1p-31f, &s, &c);
   return make_float2(c * a.scale, s * a.scale);
@@ -102,11 +102,13 @@ __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(const __grid_
         if (head < a.heads) q[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + chunk_at(j) * 16));
     }
   }
+  const uint64_t turns = __ldg(a.turns + lane);  // of pair `lane`
+  const int32_t given = a.positions != nullptr ? __ldg(a.positions + row) : 0;
   const int32_t b = seq_of_row(a.b, row);
   const int32_t end = cu_at(a.b, b + 1);
   if (row >= end || cu_at(a.b, b) > row) return;  // no sequence's row
   const int32_t pos = seq_len_at(a.b, b) - (end - row);
-  const float2 cs = rotation(a, a.positions != nullptr ? __ldg(a.positions + row) : pos);
+  const float2 cs = rotation(a, turns, a.positions != nullptr ? given : pos);
   if (record) {
     uint64_t at = 0;
     if (lane == 0) at = reinterpret_cast<uint64_t>(record_at(a.b, b, pos));

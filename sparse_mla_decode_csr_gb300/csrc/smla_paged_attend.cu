@@ -381,6 +381,7 @@ __device__ __forceinline__ int64_t tile_sum(int32_t n, int32_t g, int32_t b) {
   const int32_t gcd = min(g & -g, kTileKeys), shift = __popc(kTileKeys / gcd - 1), period = 1 << shift;
   int64_t residues = int64_t(n >> shift) * (period * (b & (gcd - 1)) + gcd * (period * (period - 1) / 2));
   int32_t r = b & (kTileKeys - 1), rest = 0;
+#pragma unroll 1
   for (int32_t i = n & (period - 1); i > 0; --i) {
     rest += r;
     r = (r + g) & (kTileKeys - 1);
@@ -621,6 +622,7 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
   const int32_t per = (a.b.n_seqs + kThreads - 1) / kThreads;
   const int32_t s0 = min(tid * per, a.b.n_seqs), s1 = min(s0 + per, a.b.n_seqs);
   int64_t sum = 0;
+#pragma unroll 1
   for (int32_t s = s0; s < s1; ++s) {
     const Seq q = seq_at(a, s);
     sum += slots_before(a, q, q.tiles);
@@ -654,12 +656,13 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
   if (beg < end && before <= beg && beg < before + sum) {
     int64_t slot = before;
     int32_t s = s0;
-    Seq q = seq_at(a, s);
-    int64_t n = slots_before(a, q, q.tiles);
-    while (slot + n <= beg) {
-      slot += n;
-      q = seq_at(a, ++s);
+    int64_t n = 0;
+#pragma unroll 1
+    for (;; ++s) {
+      const Seq q = seq_at(a, s);
       n = slots_before(a, q, q.tiles);
+      if (slot + n > beg) break;
+      slot += n;
     }
     ms->first_seq = s;
     ms->first_slot = slot;
@@ -1641,18 +1644,45 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // until the first scores and the partials' way through L2.  4 x 64 heads over up to 16384
 // positions: 37 us; 64 x 64 heads over 4096: 88 us.
 
+// Loads of 16 rows and 32 columns by the whole warp: lane l gets columns 8 j + 2 (l % 4)
+// and the next of rows l / 4 and l / 4 + 8, as o[4 j], o[4 j + 1] and o[4 j + 2], o[4 j + 3].
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t at, uint32_t (&o)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
+        "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+      : "r"(at));
+}
+
+// Stores four 8 x 8 matrices of 16-bit values, which lie over the warp's lanes as above; lane
+// l's address is that of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// S of 64 rows lies in the first 16 lanes of each warp's quarter.  All 32 lanes share a row's
+// keys, four lanes a row, two rows a lane (with one lane a row the other half idled: 64 trees of
+// up to 4 nodes, 16 heads, up to 4096 positions: 72.2 us, 69.8 so).
 template <int kN, bool kTree>
 __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* ms, uint32_t base, uint32_t tmem,
                                                     int32_t worker) {
   using L = Narrow<kN>;
-  constexpr int kCopies = kCtaRows / kN, kKeys = kN;  // a thread's keys of a tile
+  constexpr int kCopies = kCtaRows / kN, kKeys = kN;  // a warp's keys of a tile
+  constexpr int kX = kKeys / 4;                       // a thread's of each of its rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t m = (16 * warp + (lane & 15)) % kN;   // this thread's row
-  const int slice = 16 * warp / kN;                   // and keys [kKeys slice, + kKeys)
-  const bool mine = lane < 16;
-  const int32_t tok = m / a.heads, head = m - tok * a.heads;
+  const int slice = 16 * warp / kN;  // keys [kKeys slice, + kKeys)
+  const bool leads = (lane & 3) == 0;
+  int32_t m[2], tok[2], head[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    m[h] = (16 * warp + (lane >> 2) + 8 * h) % kN;
+    tok[h] = m[h] / a.heads, head[h] = m[h] - tok[h] * a.heads;
+  }
   const uint32_t lane_base = tmem + (uint32_t(warp) << 21);
-  const uint32_t p_row = base + L::kOffP + m * 128;
+  // this lane's address in stmatrix4: of 16 rows and two 8-key chunks
+  const int32_t p_m = (16 * warp + (lane & 15)) % kN;
+  const uint32_t p_row = base + L::kOffP + p_m * 128, p_chunk = slice * (kKeys / 8) + (lane >> 4);
   const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);
   Units units;
   units.start(a, ms);
@@ -1661,32 +1691,46 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
   if (ms->stall) meet_after(ms, a, &ms->never, 0);
   while (units.next(a, u)) {
     const int32_t rows = u.tokens * a.heads, t0 = u.t0, t1 = u.t1;
-    const bool live = mine && m < rows;
-    const int32_t see = a.causal && live ? max(min(u.pos0 + tok + 1, u.end), 0) : u.end;
     const int32_t past = kTree ? units.s.past : 0;
-    const uint32_t* mask = kTree ? a.mask + (int64_t(u.row0) + tok) * a.mask_stride : nullptr;
-    float ref = -INFINITY, l = 0.f;
+    bool live[2];
+    int32_t see[2];
+    float ref[2], l[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      live[h] = m[h] < rows;
+      see[h] = a.causal && live[h] ? max(min(u.pos0 + tok[h] + 1, u.end), 0) : u.end;
+      ref[h] = -INFINITY, l[h] = 0.f;
+    }
     for (int32_t t = t0; t < t1; ++t, ++g) {
       const uint32_t stage = g & 1;
       const int32_t first = t * kTileKeys + kKeys * slice;
       const bool nodes = kTree && first + kKeys > past;  // (the same for all rows)
-      uint64_t tree = ~0ull;
-      if (nodes && live) {
-        tree = tree_keys(mask, a.mask_words, past, first);
-        if (kKeys > 32) tree |= uint64_t(tree_keys(mask, a.mask_words, past, first + 32)) << 32;
+      uint64_t tree[2] = {~0ull, ~0ull};
+      if (nodes) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (live[h]) {
+            const uint32_t* mask = a.mask + (int64_t(u.row0) + tok[h]) * a.mask_stride;
+            tree[h] = tree_keys(mask, a.mask_words, past, first);
+            if (kKeys > 32) tree[h] |= uint64_t(tree_keys(mask, a.mask_words, past, first + 32)) << 32;
+          }
       }
       meet_after(ms, a, &ms->qk_done[stage], (g >> 1) & 1);
       tc_fence_after();
-      float x[kKeys];
+      float x[2][kX];
       const uint32_t s_at = lane_base + kTmemS + 128 * stage + kKeys * slice;
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 16) {
+      for (int c = 0; c < kKeys / 32; ++c) {
         uint32_t s0[16], s1[16];
-        tmem_ld16(s_at + c, s0);
-        tmem_ld16(s_at + 64 + c, s1);
+        tmem_ld_rows16(s_at + 32 * c, s0);
+        tmem_ld_rows16(s_at + 64 + 32 * c, s1);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) add2(s0[i], s0[i + 1], s1[i], s1[i + 1], x[c + i], x[c + i + 1]);
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            add2(s0[4 * j + 2 * h], s0[4 * j + 2 * h + 1], s1[4 * j + 2 * h], s1[4 * j + 2 * h + 1], x[h][8 * c + 2 * j],
+                 x[h][8 * c + 2 * j + 1]);
       }
       const uint64_t flags = *reinterpret_cast<const uint64_t*>(&ms->flags[g & 3][0]) >> (kKeys * slice);
       tc_fence_before();
@@ -1695,44 +1739,67 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
       if (a.scale_log2 <= 0.f) {
         const float by = a.scale_log2 < 0.f ? -1.f : 0.f;
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) x[c] *= by;
-      }
-      const int32_t n = see - first;
-      if (__any_sync(0xffffffffu, n < kKeys) || flags != 0 || nodes) {
-        const uint64_t seen = tree & ~flags & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c) x[c] = (seen >> c) & 1u ? x[c] : -INFINITY;
+          for (int c = 0; c < kX; ++c) x[h][c] *= by;
       }
-      float tm = x[0];
+      if (__any_sync(0xffffffffu, min(see[0], see[1]) - first < kKeys) || flags != 0 || nodes) {
 #pragma unroll
-      for (int c = 1; c < kKeys; ++c) tm = fmaxf(tm, x[c]);
+        for (int h = 0; h < 2; ++h) {
+          const int32_t n = see[h] - first;
+          const uint64_t seen = (tree[h] & ~flags & (n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull)) >> (2 * (lane & 3));
+#pragma unroll
+          for (int c = 0; c < kX; ++c) x[h][c] = (seen >> (8 * (c >> 1) + (c & 1))) & 1u ? x[h][c] : -INFINITY;
+        }
+      }
+      float tm[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tm[h] = x[h][0];
+#pragma unroll
+        for (int c = 1; c < kX; ++c) tm[h] = fmaxf(tm[h], x[h][c]);
+        tm[h] = fmaxf(tm[h], __shfl_xor_sync(0xffffffffu, tm[h], 1));
+        tm[h] = fmaxf(tm[h], __shfl_xor_sync(0xffffffffu, tm[h], 2));
+      }
       if (kCopies > 1) {
-        ms->tmax[stage][warp * 32 + lane] = tm;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (leads) ms->tmax[stage][slice * kN + m[h]] = tm[h];
         group_barrier(1, 128);
 #pragma unroll
-        for (int k = 1; k < kCopies; ++k) tm = fmaxf(tm, ms->tmax[stage][(warp ^ (k * (kN / 16))) * 32 + lane]);
-      }
-      tm *= scale;
-      const bool move = live && tm > ref + kMoveMargin;
-      const float nref = move ? tm : ref;
-      const float use = nref == -INFINITY ? 0.f : nref;
-      const float alpha = move ? ex2(ref - use) : 1.f;
-      ref = nref;
-      if (mine && slice == 0) ms->alpha[stage][m] = alpha;
-      __syncwarp();
-      const bool moved = named_barrier_or(1, 128, move);
-      uint32_t p[kKeys / 2];
-      float sum0 = 0.f, sum1 = 0.f;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int c = 0; c < kKeys / 2; ++c) {
-        float y0, y1;
-        fma2(x[2 * c], x[2 * c + 1], scale, -use, y0, y1);
-        y0 = ex2(y0);
-        y1 = ex2(y1);
-        add2(sum0, sum1, y0, y1, sum0, sum1);
-        p[c] = pack_bf16x2(y0, y1);
+          for (int k = 1; k < kCopies; ++k) tm[h] = fmaxf(tm[h], ms->tmax[stage][(slice ^ k) * kN + m[h]]);
       }
-      l = l * alpha + (sum0 + sum1);
+      bool move[2];
+      float use[2], alpha[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        tm[h] *= scale;
+        move[h] = live[h] && tm[h] > ref[h] + kMoveMargin;
+        const float nref = move[h] ? tm[h] : ref[h];
+        use[h] = nref == -INFINITY ? 0.f : nref;
+        alpha[h] = move[h] ? ex2(ref[h] - use[h]) : 1.f;
+        ref[h] = nref;
+        if (leads && slice == 0) ms->alpha[stage][m[h]] = alpha[h];
+      }
+      __syncwarp();
+      const bool moved = named_barrier_or(1, 128, move[0] || move[1]);
+      uint32_t p[2][kX / 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < kX / 2; ++c) {
+          float y0, y1;
+          fma2(x[h][2 * c], x[h][2 * c + 1], scale, -use[h], y0, y1);
+          y0 = ex2(y0);
+          y1 = ex2(y1);
+          add2(sum0, sum1, y0, y1, sum0, sum1);
+          p[h][c] = pack_bf16x2(y0, y1);
+        }
+        l[h] = l[h] * alpha[h] + (sum0 + sum1);
+      }
       if (g > 0) meet_after(ms, a, &ms->pv_done[stage ^ 1], ((g - 1) >> 1) & 1);
       if (t > t0 && moved) {
         tc_fence_after();
@@ -1749,12 +1816,9 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
         }
         tmem_wait_st();
       }
-      if (mine) {
 #pragma unroll
-        for (int c = 0; c < kKeys / 8; ++c)
-          st_shared_v4(p_row + (((slice * (kKeys / 8) + c) ^ (m & 7)) << 4), p[4 * c], p[4 * c + 1], p[4 * c + 2],
-                       p[4 * c + 3]);
-      }
+      for (int c = 0; c < kKeys / 8; c += 2)
+        stmatrix4(p_row + (((p_chunk + c) ^ (p_m & 7)) << 4), p[0][c], p[1][c], p[0][c + 1], p[1][c + 1]);
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
@@ -1762,24 +1826,37 @@ __device__ __forceinline__ void narrow_softmax_role(const AttendArgs& a, Misc* m
     }
     const bool whole = t0 == 0 && t1 == u.tiles;
     const int64_t part = 2 * int64_t(worker) + (t0 > 0 ? 0 : 1);
-    if (kCopies > 1) {
-      ms->lsum[warp * 32 + lane] = l;
-      group_barrier(1, 128);
-      l = 0.f;
 #pragma unroll
-      for (int k = 0; k < kCopies; ++k) l += ms->lsum[(warp ^ (k * (kN / 16))) * 32 + lane];
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
-    if (mine && slice == 0) {
-      float factor = 1.f;
-      if (whole) {
-        float lse;
-        finish_row(a, head, ref, l, &factor, &lse);
-        if (live && a.lse) a.lse[(int64_t(u.row0) + tok) * a.heads + head] = lse;
-      } else if (live) {
-        a.ml_part[(part * a.part_rows + m) * 2] = ref;
-        a.ml_part[(part * a.part_rows + m) * 2 + 1] = l;
+    if (kCopies > 1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (leads) ms->lsum[slice * kN + m[h]] = l[h];
+      group_barrier(1, 128);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        l[h] = 0.f;
+#pragma unroll
+        for (int k = 0; k < kCopies; ++k) l[h] += ms->lsum[k * kN + m[h]];
       }
-      ms->factor[m] = factor;
+    }
+    if (leads && slice == 0) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float factor = 1.f;
+        if (whole) {
+          float lse;
+          finish_row(a, head[h], ref[h], l[h], &factor, &lse);
+          if (live[h] && a.lse) a.lse[(int64_t(u.row0) + tok[h]) * a.heads + head[h]] = lse;
+        } else if (live[h]) {
+          a.ml_part[(part * a.part_rows + m[h]) * 2] = ref[h];
+          a.ml_part[(part * a.part_rows + m[h]) * 2 + 1] = l[h];
+        }
+        ms->factor[m[h]] = factor;
+      }
     }
     group_barrier(1, 128);
     meet_after(ms, a, &ms->pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);

