@@ -51,6 +51,32 @@ inline PagedArgs make_paged_args(const smla_paged_batch& b) {
   return a;
 }
 
+// ---- launch order ----
+//
+// Short kernels are launched as dependents of whatever is before them in the stream: they may
+// be placed while that ends, and wait for all of it, and for its memory, before they
+// read or write anything.  Every thread waits, also one without work: a grid's end then
+// always means the end of those before it.  It saves 0.3 to 0.5 us of calls that take 2.5
+// to 3.  (Letting the next one be placed at their start saves no more; attend kernels
+// launched so were no faster, the largest 4% slower.)
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    const Args&... args) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(unsigned(threads));
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = attr;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, Params(args)...);
+}
+
 __device__ __forceinline__ uint32_t page_of(const PagedArgs& a, uint32_t pos) {
   const uint32_t t = __umulhi(a.page_mul, pos);
   return (t + ((pos - t) >> a.page_sh1)) >> a.page_sh2;

@@ -70,6 +70,7 @@ template <int kDtype, bool kInterleaved>
 __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(const __grid_constant__ AppendArgs a) {
   using E = Elem<kDtype>;
   constexpr int kChunks = 16 / E::kPer;  // a lane's of a head
+  wait_for_primary();
   const int lane = threadIdx.x & 31;
   const int64_t row64 = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (row64 >= a.b.n_rows) return;
@@ -154,11 +155,11 @@ __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(const __grid_
 }
 
 template <int kDtype>
-void append_typed(const AppendArgs& a, bool interleaved, cudaStream_t st) {
+cudaError_t append_typed(const AppendArgs& a, bool interleaved, cudaStream_t st) {
   const dim3 grid(unsigned((int64_t(a.b.n_rows) + kWarps - 1) / kWarps),
                   unsigned(1 + (a.heads + kHeadsPerWarp - 1) / kHeadsPerWarp));
-  if (interleaved) paged_append_kernel<kDtype, true><<<grid, 32 * kWarps, 0, st>>>(a);
-  else paged_append_kernel<kDtype, false><<<grid, 32 * kWarps, 0, st>>>(a);
+  if (interleaved) return launch_dependent(paged_append_kernel<kDtype, true>, grid, 32 * kWarps, 0, st, a);
+  return launch_dependent(paged_append_kernel<kDtype, false>, grid, 32 * kWarps, 0, st, a);
 }
 
 }  // namespace
@@ -181,10 +182,9 @@ cudaError_t launch_paged_append(const smla_paged_append_params& p, cudaStream_t 
   a.q_out_head = p.q_out_stride_head * 2;
   a.scale = p.rope_scale;
   a.heads = p.num_heads;
-  if (p.dtype == SMLA_DTYPE_BF16) append_typed<SMLA_DTYPE_BF16>(a, p.interleaved != 0, st);
-  else if (p.dtype == SMLA_DTYPE_F16) append_typed<SMLA_DTYPE_F16>(a, p.interleaved != 0, st);
-  else append_typed<SMLA_DTYPE_F32>(a, p.interleaved != 0, st);
-  return cudaGetLastError();
+  if (p.dtype == SMLA_DTYPE_BF16) return append_typed<SMLA_DTYPE_BF16>(a, p.interleaved != 0, st);
+  if (p.dtype == SMLA_DTYPE_F16) return append_typed<SMLA_DTYPE_F16>(a, p.interleaved != 0, st);
+  return append_typed<SMLA_DTYPE_F32>(a, p.interleaved != 0, st);
 }
 
 }  // namespace smla

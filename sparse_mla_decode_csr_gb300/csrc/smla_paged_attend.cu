@@ -188,7 +188,6 @@ static_assert(kAttendSmem <= 232448 && kNarrowSmem<16> <= 232448 && kNarrowSmem<
 // be placed as soon as those of the attend kernel leave, and wait there for all of
 // it to be complete.
 __device__ __forceinline__ void let_dependents_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---- cluster helpers ----
 
@@ -2562,20 +2561,6 @@ static cudaError_t launch_kernel(const AttendArgs& a, const AttendPlan& plan, cu
   return cudaGetLastError();
 }
 
-static cudaError_t launch_merge(void (*kernel)(AttendArgs), const AttendArgs& a, dim3 grid, int threads,
-                                cudaStream_t stream) {
-  cudaLaunchConfig_t config{};
-  config.gridDim = grid;
-  config.blockDim = dim3(unsigned(threads));
-  config.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  config.attrs = attr;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, kernel, a);
-}
-
 cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const TreeMasks& tree, const AttendPlan& plan,
                                 void* workspace, cudaStream_t stream) {
   AttendArgs a{};
@@ -2613,11 +2598,11 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const TreeMas
   const bool many = plan.workers >= 8 * plan.merge_tiles;
   const unsigned jobs = unsigned(many ? plan.merge_tiles : plan.workers);
   if (plan.narrow) {
-    if (many) return launch_merge(paged_merge_kernel<2>, a, dim3(jobs, unsigned(plan.narrow)), 256, stream);
-    return launch_merge(paged_merge_kernel<1>, a, dim3(jobs, unsigned(plan.narrow) / 2), 256, stream);
+    if (many) return launch_dependent(paged_merge_kernel<2>, dim3(jobs, unsigned(plan.narrow)), 256, 0, stream, a);
+    return launch_dependent(paged_merge_kernel<1>, dim3(jobs, unsigned(plan.narrow) / 2), 256, 0, stream, a);
   }
-  if (many) return launch_merge(paged_merge_pair_kernel<4>, a, dim3(jobs, 32), 512, stream);
-  return launch_merge(paged_merge_pair_kernel<1>, a, dim3(jobs, 16), 256, stream);
+  if (many) return launch_dependent(paged_merge_pair_kernel<4>, dim3(jobs, 32), 512, 0, stream, a);
+  return launch_dependent(paged_merge_pair_kernel<1>, dim3(jobs, 16), 256, 0, stream, a);
 }
 
 cudaError_t paged_set_wait_limit(uint64_t ns, int stall) {

@@ -35,6 +35,7 @@ paged_tree_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict
                   int64_t mask_stride, int32_t mask_words, int32_t* __restrict__ positions) {
   __shared__ int2 staged[kStagedNodes];  // parent and grandparent, -1: none
   __shared__ uint32_t bits[kTreeThreads * kTreePitch];
+  wait_for_primary();
   const int32_t b = blockIdx.x, tid = threadIdx.x;
   const int32_t row0 = cu_at(a, b), n = cu_at(a, b + 1) - row0;
   const int32_t step = gridDim.y * kTreeThreads;
@@ -120,6 +121,7 @@ constexpr int kRecordChunks = kRecordBytes / 16;  // 41: a lane's one or two
 __global__ void __launch_bounds__(32 * kAcceptWarps)
 paged_accept_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict__ path, int64_t path_stride,
                     int32_t path_len, int32_t* new_lens) {
+  wait_for_primary();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t b = blockIdx.x;
   const int32_t row0 = cu_at(a, b), n = max(cu_at(a, b + 1) - row0, 0);
@@ -179,15 +181,14 @@ cudaError_t launch_paged_tree(const smla_paged_batch& b, const int32_t* parents,
   const int64_t mean = (b.n_rows + b.n_seqs - 1) / b.n_seqs;
   const int64_t split = (mean + kTreeThreads - 1) / kTreeThreads;
   const dim3 grid(unsigned(b.n_seqs), unsigned(split < 1024 ? split : 1024));
-  paged_tree_kernel<<<grid, kTreeThreads, 0, st>>>(a, parents, mask, mask_stride, mask_words, positions);
-  return cudaGetLastError();
+  return launch_dependent(paged_tree_kernel, grid, kTreeThreads, 0, st, a, parents, mask, mask_stride, mask_words, positions);
 }
 
 cudaError_t launch_paged_accept(const smla_paged_batch& b, const int32_t* path, int64_t path_stride, int32_t path_len,
                                 int32_t* new_lens, cudaStream_t st) {
   const PagedArgs a = make_paged_args(b);
-  paged_accept_kernel<<<unsigned(b.n_seqs), 32 * kAcceptWarps, 0, st>>>(a, path, path_stride, path_len, new_lens);
-  return cudaGetLastError();
+  return launch_dependent(paged_accept_kernel, dim3(unsigned(b.n_seqs)), 32 * kAcceptWarps, 0, st, a, path, path_stride,
+                          path_len, new_lens);
 }
 
 }  // namespace smla
