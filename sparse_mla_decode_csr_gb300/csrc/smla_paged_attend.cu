@@ -42,12 +42,15 @@
 //             p = 2^(x - m_ref), the reference moves (and O is rescaled in TMEM)
 //             only when a score exceeds it by more than 8, so p <= 2^8
 //
-// What bounds the pair kernel: shared memory.  A tile of 64 keys takes ~2420 cycles,
-// in which the operands' reads (1248), the loaders' and softmax warps' accesses (579)
-// and the bulk copies (512) keep its port busy for ~2340.  One chunk of 2048 tokens,
-// 64 heads, after 8192 earlier positions: 2467 us = 1065 TFLOP/s, 56% of the measured
-// bf16 peak; 7 chunks of up to 300 tokens, 16 heads, up to 4927 positions: 225 us.
-// A tile of the pair takes 1.23 us when it has 128 rows of one token (128 heads).
+// What bounds the pair kernel: shared memory.  For a tile of 64 keys the operands' reads
+// (1248 cycles), the loaders' and softmax warps' accesses (579) and the bulk copies (512) keep
+// its port busy for ~2340.  One chunk of 2048 tokens, 64 heads, after 8192 earlier
+// positions: 2352 us = 1117 TFLOP/s, 57% of the measured bf16 peak; 7 chunks of up to 300
+// tokens, 16 heads, up to 4927 positions: 203 us; 32 trees of up to 60 nodes, 64 heads, up to
+// 2000 positions: 295 us.  A row-tile change costs 4 to 5 us beside its tiles.
+//
+// Trees (kTree): of its sequence's token rows a row sees those in its mask, whatever their
+// order, instead of the ones up to its own.  Only tiles that reach past the history look at it.
 //
 // Schedule.  A row tile takes a few slots for its start (kPairStart and so on: what
 // a unit's first tile and last store take, in key tiles) and one per key tile; the
@@ -1641,7 +1644,8 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // limit, the same for 17, 32 and 64 rows: 3.0 TB/s of records over all SMs), whose
 // largest stall is the wait for their own global loads, and for short rows the ~10 us
 // until the first scores and the partials' way through L2.  4 x 64 heads over up to 16384
-// positions: 37 us; 64 x 64 heads over 4096: 88 us.
+// positions: 36 us; 64 x 64 heads over 4096: 87 us; 64 trees of up to 4 nodes, 16 heads,
+// over up to 4096: 68 us.
 
 // Loads of 16 rows and 32 columns by the whole warp: lane l gets columns 8 j + 2 (l % 4)
 // and the next of rows l / 4 and l / 4 + 8, as o[4 j], o[4 j + 1] and o[4 j + 2], o[4 j + 3].
@@ -2490,8 +2494,8 @@ paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
 // device.  Any split is computed correctly by either.  Measured at 64 sequences of
 // 4096 positions (graph replays, us; rows: few-row kernel / narrow tiles of 32 / of 64 /
 // pair kernel):
-//   16: 63 / 77 / 78 / 99    24: - / 78 / 80 / 100    32: 106 / 80 / 82 / 100
-//   64: 192 / 140 / 88 / 104    96: 273 / 201 / 148 / 106    128: - / - / 154 / 108
+//   16: 62 / 77 / 77 / 89    24: - / 78 / 78 / 90    32: 105 / 80 / 82 / 89
+//   64: 192 / 139 / 87 / 92    96: 277 / 200 / 146 / 95    128: - / - / 152 / 98
 // One kernel serves the whole call, so a batch of unlike sequences gets what its mean
 // gives: 63 single tokens and one of two, 16 heads, take 77 us in tiles of 32 (63 without
 // the second token); 63 tokens and a chunk of 512 177 us in one call, 63 + 97 as two;

@@ -22,8 +22,8 @@ namespace {
 // Bound: the walk, a chain of look-ups.  It reads a copy of the parents in shared memory that
 // holds each node's parent and grandparent, so that a look-up goes two nodes up; the bits are
 // set by shared-memory atomics, whose results nobody waits for (sequences of more than 2048
-// nodes: one node at a time, through L1).  7 trees of up to 500 nodes, 40 deep: 7.2 us (12.8
-// with one node a look-up and the words stored by each thread as it walks); 64 of 60: 2.8 us.
+// nodes: one node at a time, through L1).  7 trees of up to 500 nodes, 40 deep: 7.1 us (12.8
+// with one node a look-up and the words stored by each thread as it walks); 64 of 60: 2.5 us.
 
 constexpr int kTreeThreads = 128;
 constexpr int kTreeWords = 32;
@@ -112,7 +112,8 @@ paged_tree_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict
 // Record of node path[i] -> position past + i.  The path rises, so path[i] >= i: a
 // record's new place is never that of a node that comes later in the path, and 32 steps
 // of the path at a time may be moved one after the other, each batch read whole
-// before it is written.
+// before it is written.  A block a sequence, a warp 4 records of a batch.  Bound: the chain path ->
+// page -> record (64 trees of 60: 2.2 us, 7 of up to 500 with paths of up to 60: 2.9).
 
 constexpr int kAcceptWarps = 8;
 constexpr int kPerWarp = 32 / kAcceptWarps;
