@@ -602,3 +602,69 @@ def test_well_formed_calls_are_taken_and_others_are_not():
     assert native.attend(*attend, None, None, torch.zeros(256, dtype=torch.uint8, device=DEV), None) is False  # too small
     assert native.attend(*batch, s["q"], 1e40, None, s["out"], s["lse"], True, None, None, None, None) is False
     torch.cuda.synchronize()
+
+
+def test_a_captured_step_behind_copies_and_joined_streams():
+    # what is before a call in a graph may be a copy, or the join of two streams
+    c = Batch([(20, 300), (9, 100)], 16)
+    s = step_state(c, 16, 70)
+    c.kv_ref = s["kv"].clone()
+    step(s)
+    torch.cuda.synchronize()
+    pinned = {k: s[k].cpu().pin_memory() for k in ("parents", "path", "lat", "rope", "sl")}
+    side, stream, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        s["parents"].copy_(pinned["parents"], non_blocking=True)
+        smla.smla_paged_tree(s["parents"], s["cu"], s["sl"], s["mask"], s["pos"], status=s["status"])
+        side.wait_stream(stream)
+        with torch.cuda.stream(side):
+            s["lat"].copy_(pinned["lat"], non_blocking=True)
+            s["rope"].copy_(pinned["rope"], non_blocking=True)
+        s["kv"].copy_(c.kv_ref)
+        stream.wait_stream(side)
+        smla.smla_paged_append(s["lat"], s["rope"], s["kv"], s["table"], s["cu"], s["sl"], s["turns"], q_rope=s["q_rope"],
+                               q_out=s["q"][..., 512:], positions=s["pos"], status=s["status"])
+        s["out"].fill_(7.0)
+        smla.smla_paged_attend_tree(s["q"], s["kv"], s["table"], s["cu"], s["sl"], s["mask"], 1 / 24, None, s["out"], s["lse"],
+                                    status=s["status"])
+        s["path"].copy_(pinned["path"], non_blocking=True)
+        smla.smla_paged_accept(s["kv"], s["table"], s["cu"], s["sl"], s["path"], s["new"], status=s["status"])
+    for seed in (70, 71):
+        new_trees(c, s, seed)
+        pinned["parents"].copy_(s["parents"].cpu())
+        pinned["path"].copy_(s["path"].cpu())
+        for k in ("mask", "pos", "parents", "path", "lat", "rope", "lse", "new"):
+            s[k].fill_(0)
+        torch.cuda.synchronize()
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        check_step(c, s)
+
+
+@pytest.mark.parametrize("kernel", ["few", "narrow32", "narrow64", "pair", "pair_128"])
+def test_many_launches_at_once_give_the_same_bits(kernel):
+    # cold and warm caches, three streams, two batches of unlike shapes beside each other
+    heads, lens = KERNELS[kernel]
+    work = []
+    for seed, part in ((1, lens), (2, lens[:3] + [(3, 1500)] + (EMPTY if (0, 0) in lens else []))):
+        c = Batch(part, 16, seed=seed)
+        _, sets = random_trees(c, seed)
+        mask = words_of(sets, -(-max(n for n, _ in part) // 32)).to(DEV)
+        q, _, out, lse, _ = tree_attend(c, heads, mask.cpu())
+        work.append((c, q.to(DEV), mask, c.cache(), c.dev(), out, lse))
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device=DEV)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(18):
+        c, q, mask, kv, tabs, out, lse = work[i % 2]
+        with torch.cuda.stream(streams[i % 3]):
+            if i % 4 == 0:
+                flush.fill_(i)
+            o, z = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+            smla.smla_paged_attend_tree(q, kv, *tabs, mask, 1 / 24, None, o, z)
+            got.append((o, z, out, lse))
+    torch.cuda.synchronize()
+    for o, z, out, lse in got:
+        assert torch.equal(o, out) and torch.equal(z, lse)
