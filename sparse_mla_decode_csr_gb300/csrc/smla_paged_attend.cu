@@ -157,6 +157,13 @@ struct AttendArgs {
   int32_t mask_words;
 };
 
+// What a sequence needs for its row tiles.
+struct Seq {
+  int32_t row0, rows;  // its token rows
+  int32_t past;        // position of the first one (negative: rows before the sequence's start)
+  int32_t tiles;       // row tiles
+};
+
 struct Misc {
   uint64_t k_full[2], q_full, p_full, s_empty[2];  // used in the even CTA
   uint64_t k_ready[2], v_land[2], v_full[2];
@@ -166,6 +173,7 @@ struct Misc {
   uint64_t wait_ns;
   int32_t stall;
   int32_t first_seq, first_j;
+  Seq first;  // first_seq's
   int64_t first_slot, beg, end, total;
   int64_t warp_sum[16];
   // pair and narrow kernels: the units ahead, in a ring (see scheduler_role)
@@ -397,13 +405,6 @@ __device__ __forceinline__ int64_t div_up_to_64(int64_t n, int64_t d) {
   return n / d;
 }
 
-// What a sequence needs for its row tiles.
-struct Seq {
-  int32_t row0, rows;  // its token rows
-  int32_t past;        // position of the first one (negative: rows before the sequence's start)
-  int32_t tiles;       // row tiles
-};
-
 __device__ __forceinline__ Seq seq_at(const AttendArgs& a, int32_t b) {
   Seq s;
   s.row0 = cu_at(a.b, b);
@@ -472,7 +473,7 @@ struct Units {
     seq = ms->first_seq;
     j = ms->first_j;
     s.tiles = 0;
-    if (slot < end && seq < a.b.n_seqs) s = seq_at(a, seq);
+    if (slot < end && seq < a.b.n_seqs) s = ms->first;
   }
 
   // The next unit of this worker; false when there is none.
@@ -624,9 +625,10 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
   const int32_t per = (a.b.n_seqs + kThreads - 1) / kThreads;
   const int32_t s0 = min(tid * per, a.b.n_seqs), s1 = min(s0 + per, a.b.n_seqs);
   int64_t sum = 0;
+  Seq q{};  // the thread's last
 #pragma unroll 1
   for (int32_t s = s0; s < s1; ++s) {
-    const Seq q = seq_at(a, s);
+    q = seq_at(a, s);
     sum += slots_before(a, q, q.tiles);
     if (worker == 0 && q.rows > 0 && q.past > a.coverage - q.rows && a.b.status)  // positions past the table
       atomicOr(a.b.status, SMLA_STATUS_INDEX_OOB);
@@ -655,39 +657,45 @@ __device__ __forceinline__ void find_range(const AttendArgs& a, Misc* ms, int32_
     ms->total = total;
     if (beg >= end) ms->first_slot = end;  // nothing to do
   }
-  if (beg < end && before <= beg && beg < before + sum) {
-    int64_t slot = before;
-    int32_t s = s0;
-    int64_t n = 0;
+  // the warp that has that sequence looks for the row tile in it
+  const bool mine = beg < end && before <= beg && beg < before + sum;
+  const uint32_t owner = __ballot_sync(0xffffffffu, mine);
+  if (owner == 0) return;
+  int64_t slot = before;
+  int32_t s = s0;
+  if (mine && per > 1) {
 #pragma unroll 1
     for (;; ++s) {
-      const Seq q = seq_at(a, s);
-      n = slots_before(a, q, q.tiles);
+      q = seq_at(a, s);
+      const int64_t n = slots_before(a, q, q.tiles);
       if (slot + n > beg) break;
       slot += n;
     }
-    ms->first_seq = s;
-    ms->first_slot = slot;
   }
-  __syncthreads();
+  __syncwarp();
+  const int from = __ffs(owner) - 1;
+  s = __shfl_sync(0xffffffffu, s, from);
+  slot = __shfl_sync(0xffffffffu, slot, from);
+  q.row0 = __shfl_sync(0xffffffffu, q.row0, from);
+  q.rows = __shfl_sync(0xffffffffu, q.rows, from);
+  q.past = __shfl_sync(0xffffffffu, q.past, from);
+  q.tiles = __shfl_sync(0xffffffffu, q.tiles, from);
   // the last row tile of that sequence that starts at or before beg: each step looks
   // at 32 of them
-  if (warp == 0 && beg < end) {
-    const Seq q = seq_at(a, ms->first_seq);
-    const int64_t at = beg - ms->first_slot;
-    int32_t lo = 0, n = q.tiles;
-    while (n > 1) {
-      const int32_t step = (n + 31) >> 5, off = lane * step;
-      const bool in = off < n && slots_before(a, q, lo + off) <= at;
-      const int32_t last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
-      lo += last * step;
-      n = min(step, n - last * step);
-    }
-    __syncwarp();
-    if (lane == 0) {
-      ms->first_j = lo;
-      ms->first_slot += slots_before(a, q, lo);
-    }
+  int32_t lo = 0, n = q.tiles;
+  while (n > 1) {
+    const int32_t step = (n + 31) >> 5, off = lane * step;
+    const bool in = off < n && slots_before(a, q, lo + off) <= beg - slot;
+    const int32_t last = __popc(__ballot_sync(0xffffffffu, in)) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  __syncwarp();
+  if (lane == 0) {
+    ms->first_seq = s;
+    ms->first_j = lo;
+    ms->first_slot = slot + slots_before(a, q, lo);
+    ms->first = q;
   }
 }
 
@@ -1574,9 +1582,12 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
                  : "memory");
     tc_fence_before();
   }
+  // (the peer's barriers are ready when it arrives here; the range is found meanwhile)
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   find_range<kAttendThreads>(a, ms, pair);
   __syncthreads();
-  cluster_sync();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   tc_fence_after();
   const uint32_t tmem = ms->tmem;
   auto leave = [&]() {
