@@ -45,9 +45,9 @@
 // What bounds the pair kernel: shared memory.  For a tile of 64 keys the operands' reads
 // (1248 cycles), the loaders' and softmax warps' accesses (579) and the bulk copies (512) keep
 // its port busy for ~2340.  One chunk of 2048 tokens, 64 heads, after 8192 earlier
-// positions: 2352 us = 1117 TFLOP/s, 57% of the measured bf16 peak; 7 chunks of up to 300
+// positions: 2365 us = 1111 TFLOP/s, 57% of the measured bf16 peak; 7 chunks of up to 300
 // tokens, 16 heads, up to 4927 positions: 203 us; 32 trees of up to 60 nodes, 64 heads, up to
-// 2000 positions: 295 us.  A row-tile change costs 4 to 5 us beside its tiles.
+// 2000 positions: 296 us.  A row-tile change costs 4 to 5 us beside its tiles.
 //
 // Trees (kTree): of its sequence's token rows a row sees those in its mask, whatever their
 // order, instead of the ones up to its own.  Only tiles that reach past the history look at it.
@@ -570,7 +570,7 @@ __device__ __forceinline__ void scheduler_role(const AttendArgs& a, Misc* ms) {
       for (uint32_t i = 0; i < 64; ++i) {
         if (n != 0 && mbar_try_wait(&ms->job_empty[n % kJobs], ((n - kJobs) / kJobs) & 1)) return true;
         if (n == 0 && *reinterpret_cast<volatile int32_t*>(&ms->progress) == INT32_MAX) return true;
-        __nanosleep(100);
+        __nanosleep(200);  // (looking more often costs the other roles up to 0.6%)
       }
       const uint64_t now = globaltimer();
       const int32_t p = *reinterpret_cast<volatile int32_t*>(&ms->progress);
@@ -1655,8 +1655,8 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // limit, the same for 17, 32 and 64 rows: 3.0 TB/s of records over all SMs), whose
 // largest stall is the wait for their own global loads, and for short rows the ~10 us
 // until the first scores and the partials' way through L2.  4 x 64 heads over up to 16384
-// positions: 36 us; 64 x 64 heads over 4096: 87 us; 64 trees of up to 4 nodes, 16 heads,
-// over up to 4096: 68 us.
+// positions: 35 us; 64 x 64 heads over 4096: 86 us; 64 trees of up to 4 nodes, 16 heads,
+// over up to 4096: 66 us.
 
 // Loads of 16 rows and 32 columns by the whole warp: lane l gets columns 8 j + 2 (l % 4)
 // and the next of rows l / 4 and l / 4 + 8, as o[4 j], o[4 j + 1] and o[4 j + 2], o[4 j + 3].
