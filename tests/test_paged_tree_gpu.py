@@ -668,3 +668,40 @@ def test_many_launches_at_once_give_the_same_bits(kernel):
     torch.cuda.synchronize()
     for o, z, out, lse in got:
         assert torch.equal(o, out) and torch.equal(z, lse)
+
+
+def test_calls_without_pages_or_table():
+    c = Batch([(3, 9)], 16)
+    s = step_state(c, 16, 80)
+    for kv, table in ((torch.empty(0, 16, REC, dtype=torch.uint8, device=DEV), torch.zeros(1, 3, dtype=I32, device=DEV)),
+                      (torch.zeros(2, 16, REC, dtype=torch.uint8, device=DEV), torch.zeros(1, 0, dtype=I32, device=DEV))):
+        s["kv"], s["table"] = kv, table
+        s["status"].zero_()
+        s["path"][0] = torch.tensor([0, 2, -1, -1, -1, -1], dtype=I32)
+        step(s)
+        assert int(s["status"]) == smla.STATUS_INDEX_OOB
+        pos = [6 + len(x) - 1 for x in c.sets]
+        assert s["pos"].tolist() == pos and s["new"].tolist() == [8]
+        check_rotated(s["q"][..., 512:], s["q_rope"].cpu(), pos)
+        assert (s["out"] == 0).all() and torch.isneginf(s["lse"]).all() and (s["kv"] == 0).all()
+
+
+def test_lengths_and_boundaries_that_say_nothing_sensible():
+    # negative lengths count as zero, boundaries are clamped or name rows twice: every access stays
+    # inside the tensors, and rows of no sequence stay as they are
+    c = Batch([(4, 40), (3, 30), (2, 2)], 16, behind=4)
+    s = step_state(c, 16, 81)
+    for cu, lens in (([0, 4, 7, 9], [-5, -2 ** 31, 0]), ([-7, 4, 4, 1000], [40, 30, 2]), ([0, 6, 3, 9], [40, 30, 2]),
+                     ([13, 13, 0, 0], [40, 30, 2]), ([5, 5, 5, 5], [2 ** 31 - 1] * 3), ([0, 4, 7, 9], [2 ** 31 - 1, 7, 2 ** 30])):
+        s["cu"].copy_(torch.tensor(cu, dtype=I32))
+        s["sl"].copy_(torch.tensor(lens, dtype=I32))
+        for k in ("mask", "pos"):
+            s[k].fill_(0)
+        step(s)
+        step(s, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    s["cu"].copy_(torch.tensor([5, 5, 5, 5], dtype=I32))
+    s["out"].fill_(7.0), s["mask"].fill_(7), s["pos"].fill_(7)
+    before = s["kv"].clone()
+    step(s)
+    assert (s["out"] == 7.0).all() and (s["mask"] == 7).all() and (s["pos"] == 7).all() and torch.equal(s["kv"], before)
