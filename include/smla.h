@@ -501,8 +501,10 @@ int smla_paged_attend_tree(const smla_paged_attend_params* params, const uint32_
  * that is no node of the tree or does not rise, which sets SMLA_STATUS_INDEX_OOB.
  * A record whose old or new place is masked stays where it is.  Records of the tree behind
  * the accepted ones are left as they are.  path int32 [n_seqs][path_stride],
- * path_len used; new_lens int32 [n_seqs], which may be the batch's seq_lens.  As in
- * smla_paged_write, the rows' positions have to lie in different slots. */
+ * path_len used; new_lens int32 [n_seqs], which may be the batch's seq_lens; the batch's
+ * n_rows clamps the boundaries as in the other calls, and with none of it every new length
+ * is the old one.  As in smla_paged_write, the rows' positions have to lie in different
+ * slots. */
 int smla_paged_accept(const smla_paged_batch* batch, const int32_t* path, int64_t path_stride, int32_t path_len,
                       int32_t* new_lens, void* stream);
 
