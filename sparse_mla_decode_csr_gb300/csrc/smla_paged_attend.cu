@@ -176,7 +176,7 @@ struct Misc {
   Seq first;  // first_seq's
   int64_t first_slot, beg, end, total;
   int64_t warp_sum[16];
-  // pair and narrow kernels: the units ahead, in a ring (see scheduler_role)
+  // pair kernel: the units ahead, in a ring (see scheduler_role)
   uint4 job[kJobs][3];
   uint64_t job_full[kJobs], job_empty[kJobs];
   int32_t progress;  // tiles that the softmax warps have come to; INT32_MAX: they are done
@@ -508,7 +508,7 @@ struct Units {
   }
 };
 
-// A unit as the roles of the pair and narrow kernels get it.
+// A unit as the roles of the pair kernel get it.
 struct Job {
   int32_t tokens;  // 0: there is no more
   int32_t seq, row0, pos0, end, t0, t1;
@@ -553,7 +553,12 @@ __device__ __forceinline__ bool next_thread(Misc* ms, uint32_t& n, Job& u) {
 // CTAs, kJobs ahead of the softmax warps.  (Each role looking units up by itself cost up to
 // 10,000 cycles at each unit's end, three quarters of them instruction fetches: the roles'
 // loops leave nothing else in the instruction cache.)  A slot of the ring is free once
-// the softmax warps are through with its unit's tiles, when every other role is too.
+// the softmax warps are through with its unit's tiles: every other role has then read the
+// unit, since a tile needs what each of them does for it, and a loader group looks ahead, at
+// the next two tiles' units, before it stores a tile.  Only loader group 1 has no tile
+// before its first one, tile 1.  If unit 0 has one tile, that group reads it just to pass on, and
+// nothing of unit 0 waits for that; so slot 0 is first taken again when unit 1 is done too,
+// which has tile 1 then.  (Units 0 to 3 are there by then, and tile 1 needs no later one.)
 //
 // It also keeps the limit of all waits: when the softmax warps get no further for longer,
 // it sets `dead` in both CTAs, which ends every other role and lets the softmax warps run
@@ -562,7 +567,7 @@ __device__ __forceinline__ void scheduler_role(const AttendArgs& a, Misc* ms) {
   Units units;
   units.start(a, ms);
   const int64_t G = max(min(int64_t(a.workers), ms->total), int64_t(1));
-  // until the softmax warps have freed the slot of unit n - kJobs, or (n = 0) are done
+  // until the softmax warps are through with unit n - kJobs, or (n = 0) with all
   int32_t seen = -1;
   uint64_t since = globaltimer(), limit = ms->wait_ns;
   auto wait = [&](uint32_t n) {
@@ -589,7 +594,7 @@ __device__ __forceinline__ void scheduler_role(const AttendArgs& a, Misc* ms) {
     const uint32_t slot = n % kJobs;
     Unit u;
     more = units.next(a, u);
-    if (n >= kJobs) fine = wait(n);
+    if (n >= kJobs) fine = wait(n) && (n > kJobs || wait(n + 1));
     if (!fine) break;
     uint32_t w[12];
     w[0] = more ? u.tokens : 0, w[1] = u.seq, w[2] = u.row0, w[3] = u.pos0;
