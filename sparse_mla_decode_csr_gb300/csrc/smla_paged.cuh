@@ -77,22 +77,46 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int th
   return cudaLaunchKernelEx(&config, kernel, Params(args)...);
 }
 
+// How a batch's arrays are read.  The read-only path is for memory that nothing writes while the
+// kernel is resident, which a dependent may be while the kernel before it still writes
+// (lengths by an accept, positions and masks by a tree, any of them by a copy of the user's):
+// dependents load past it, behind their wait (both are volatile).
+enum Loads { kReadOnly, kFresh };
+
+template <Loads kLoads>
+__device__ __forceinline__ int32_t load_i32(const int32_t* p) {
+  if constexpr (kLoads == kReadOnly) return __ldg(p);
+  int32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+__device__ __forceinline__ uint64_t load_fresh_u64(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.global.b64 %0, [%1];" : "=l"(v) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+
 __device__ __forceinline__ uint32_t page_of(const PagedArgs& a, uint32_t pos) {
   const uint32_t t = __umulhi(a.page_mul, pos);
   return (t + ((pos - t) >> a.page_sh1)) >> a.page_sh2;
 }
 
 // cu_rows[b] clamped to the token tensors' rows.
+template <Loads kLoads = kReadOnly>
 __device__ __forceinline__ int32_t cu_at(const PagedArgs& a, int32_t b) {
-  const int32_t v = __ldg(a.cu + b);
+  const int32_t v = load_i32<kLoads>(a.cu + b);
   return v < 0 ? 0 : v > a.n_rows ? a.n_rows : v;
 }
 
 // Length of sequence b, at least 0.
-__device__ __forceinline__ int32_t seq_len_at(const PagedArgs& a, int32_t b) { return max(__ldg(a.seq_lens + b), 0); }
+template <Loads kLoads = kReadOnly>
+__device__ __forceinline__ int32_t seq_len_at(const PagedArgs& a, int32_t b) {
+  return max(load_i32<kLoads>(a.seq_lens + b), 0);
+}
 
 // Record of position pos of sequence b, or nullptr when it is masked (page ids
 // >= n_pages and positions past the table are flagged).
+template <Loads kLoads = kReadOnly>
 __device__ __forceinline__ uint8_t* record_at(const PagedArgs& a, int32_t b, int32_t pos) {
   if (pos < 0) return nullptr;
   const uint32_t page = page_of(a, uint32_t(pos));
@@ -100,7 +124,7 @@ __device__ __forceinline__ uint8_t* record_at(const PagedArgs& a, int32_t b, int
     if (a.status) atomicOr(a.status, SMLA_STATUS_INDEX_OOB);
     return nullptr;
   }
-  const int32_t id = __ldg(a.table + int64_t(b) * a.table_stride + page);
+  const int32_t id = load_i32<kLoads>(a.table + int64_t(b) * a.table_stride + page);
   if (id < 0) return nullptr;
   if (id >= a.n_pages) {
     if (a.status) atomicOr(a.status, SMLA_STATUS_INDEX_OOB);
@@ -112,13 +136,14 @@ __device__ __forceinline__ uint8_t* record_at(const PagedArgs& a, int32_t b, int
 // The last sequence b with cu_rows[b] <= r (0 if there is none), found by the
 // whole warp: each step looks at 32 boundaries, so that 1024 sequences take
 // two loads one after the other instead of a binary search's ten.
+template <Loads kLoads = kReadOnly>
 __device__ __forceinline__ int32_t seq_of_row(const PagedArgs& a, int32_t r) {
   const int lane = threadIdx.x & 31;
   int32_t lo = 0, n = a.n_seqs;
   while (n > 1) {
     const int32_t step = (n + 31) >> 5;
     const int32_t off = lane * step;
-    const bool in = off < n && __ldg(a.cu + lo + off) <= r;
+    const bool in = off < n && load_i32<kLoads>(a.cu + lo + off) <= r;
     const int32_t cnt = __popc(__ballot_sync(0xffffffffu, in));
     if (cnt == 0) return lo;
     lo += (cnt - 1) * step;

@@ -109,16 +109,16 @@ __global__ void __launch_bounds__(32 * kWarps) paged_append_kernel(const __grid_
         if (head < a.heads) q[i][j] = __ldcs(reinterpret_cast<const uint4*>(src + chunk_at(j) * 16));
     }
   }
-  const uint64_t turns = __ldg(a.turns + lane);  // of pair `lane`
-  const int32_t given = a.positions != nullptr ? __ldg(a.positions + row) : 0;
-  const int32_t b = seq_of_row(a.b, row);
-  const int32_t end = cu_at(a.b, b + 1);
-  if (row >= end || cu_at(a.b, b) > row) return;  // no sequence's row
-  const int32_t pos = seq_len_at(a.b, b) - (end - row);
+  const uint64_t turns = load_fresh_u64(a.turns + lane);  // of pair `lane`
+  const int32_t given = a.positions != nullptr ? load_i32<kFresh>(a.positions + row) : 0;
+  const int32_t b = seq_of_row<kFresh>(a.b, row);
+  const int32_t end = cu_at<kFresh>(a.b, b + 1);
+  if (row >= end || cu_at<kFresh>(a.b, b) > row) return;  // no sequence's row
+  const int32_t pos = seq_len_at<kFresh>(a.b, b) - (end - row);
   const float2 cs = rotation(a, turns, a.positions != nullptr ? given : pos);
   if (record) {
     uint64_t at = 0;
-    if (lane == 0) at = reinterpret_cast<uint64_t>(record_at(a.b, b, pos));
+    if (lane == 0) at = reinterpret_cast<uint64_t>(record_at<kFresh>(a.b, b, pos));
     uint8_t* rec = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, at, 0));
     if (rec == nullptr) return;
     write_latent<kDtype>(rec, lat);

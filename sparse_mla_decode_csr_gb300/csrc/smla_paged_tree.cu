@@ -31,21 +31,21 @@ constexpr int kTreePitch = kTreeWords + 1;  // (a column's threads hit different
 constexpr int kStagedNodes = 2048;
 
 __global__ void __launch_bounds__(kTreeThreads)
-paged_tree_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict__ parents, uint32_t* __restrict__ mask,
-                  int64_t mask_stride, int32_t mask_words, int32_t* __restrict__ positions) {
+paged_tree_kernel(const __grid_constant__ PagedArgs a, const int32_t* parents, uint32_t* mask,
+                  int64_t mask_stride, int32_t mask_words, int32_t* positions) {
   __shared__ int2 staged[kStagedNodes];  // parent and grandparent, -1: none
   __shared__ uint32_t bits[kTreeThreads * kTreePitch];
   wait_for_primary();
   const int32_t b = blockIdx.x, tid = threadIdx.x;
-  const int32_t row0 = cu_at(a, b), n = cu_at(a, b + 1) - row0;
+  const int32_t row0 = cu_at<kFresh>(a, b), n = cu_at<kFresh>(a, b + 1) - row0;
   const int32_t step = gridDim.y * kTreeThreads;
   if (int32_t(blockIdx.y) * kTreeThreads >= n) return;
-  const int32_t past = seq_len_at(a, b) - n;
+  const int32_t past = seq_len_at<kFresh>(a, b) - n;
   const bool near = n <= kStagedNodes;
   bool odd = false;
   // the parent of a node, -1 for a root
   auto parent = [&](int32_t i) {
-    const int32_t up = __ldg(parents + row0 + i);
+    const int32_t up = load_i32<kFresh>(parents + row0 + i);
     odd |= up >= i;
     return up < i && up >= 0 ? up : -1;
   };
@@ -120,20 +120,19 @@ constexpr int kPerWarp = 32 / kAcceptWarps;
 constexpr int kRecordChunks = kRecordBytes / 16;  // 41: a lane's one or two
 
 __global__ void __launch_bounds__(32 * kAcceptWarps)
-paged_accept_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restrict__ path, int64_t path_stride,
+paged_accept_kernel(const __grid_constant__ PagedArgs a, const int32_t* path, int64_t path_stride,
                     int32_t path_len, int32_t* new_lens) {
   wait_for_primary();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t b = blockIdx.x;
-  const int32_t row0 = cu_at(a, b), n = max(cu_at(a, b + 1) - row0, 0);
-  // (new_lens may be seq_lens: not through the read-only path)
-  const int32_t past = max(*reinterpret_cast<const volatile int32_t*>(a.seq_lens + b), 0) - n;
+  const int32_t row0 = cu_at<kFresh>(a, b), n = max(cu_at<kFresh>(a, b + 1) - row0, 0);
+  const int32_t past = seq_len_at<kFresh>(a, b) - n;  // (new_lens may be seq_lens)
   const int32_t* steps = path + int64_t(b) * path_stride;
   int32_t accepted = 0, before = -1;
   for (int32_t i0 = 0; i0 < path_len; i0 += 32) {
     // lane l: step i0 + l; the path ends at the first step that is no higher node
     const int32_t i = i0 + lane;
-    const int32_t node = i < path_len ? __ldg(steps + i) : -1;
+    const int32_t node = i < path_len ? load_i32<kFresh>(steps + i) : -1;
     int32_t last = __shfl_up_sync(0xffffffffu, node, 1);
     if (lane == 0) last = before;
     const uint32_t bad = __ballot_sync(0xffffffffu, node < 0 || node >= n || node <= last);
@@ -142,8 +141,8 @@ paged_accept_kernel(const __grid_constant__ PagedArgs a, const int32_t* __restri
     uint8_t* from = nullptr;
     uint8_t* to = nullptr;
     if (lane < good && node != i && lane / kPerWarp == warp) {
-      from = record_at(a, b, past + node);
-      to = record_at(a, b, past + i);
+      from = record_at<kFresh>(a, b, past + node);
+      to = record_at<kFresh>(a, b, past + i);
     }
     uint4 v[kPerWarp][2];
     uint8_t* dst[kPerWarp];
