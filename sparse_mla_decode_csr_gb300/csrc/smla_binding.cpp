@@ -159,6 +159,18 @@ bool vector_of(const at::Tensor* t, at::ScalarType type, int64_t n) {
   return is(t, type, 1) && t->size(0) == n && (n <= 1 || t->stride(0) == 1);
 }
 
+// Lets the other Python threads run while a call is made (a launch may wait for room in its queue, an
+// allocation for the driver).  The arguments' properties are read before; the caller keeps them.
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
 template <bool (*kCall)(Args&)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   bool done = false;
@@ -182,6 +194,7 @@ bool copy(Args& a) {
   b.status = status_of(a, a.tensor(true));
   if (!a.ok) return false;
   b.n_rows = r.n;
+  const Unlocked unlocked;
   const int rc = kWrite ? smla_paged_write(&b, r.latent, r.latent_stride, r.rope, r.rope_stride, r.dtype, a.stream())
                         : smla_paged_read(&b, r.latent, r.latent_stride, r.rope, r.rope_stride, r.dtype, a.stream());
   return rc == SMLA_OK;
@@ -220,6 +233,7 @@ bool append(Args& a) {
   p.dtype = r.dtype;
   p.turns = static_cast<const uint64_t*>(turns->data_ptr());
   p.positions = data<int32_t>(pos);
+  const Unlocked unlocked;
   return smla_paged_append(&p, a.stream()) == SMLA_OK;
 }
 
@@ -236,6 +250,7 @@ bool tree(Args& a) {
   int64_t stride = 0;
   int32_t words = 0;
   if (mask && !take_mask(mask, n, &stride, &words)) return false;
+  const Unlocked unlocked;
   return smla_paged_tree(data<int32_t>(parents), data<int32_t>(cu), data<int32_t>(lens), n, int32_t(seqs),
                          data<uint32_t>(mask), stride, words, data<int32_t>(pos), status, a.stream()) == SMLA_OK;
 }
@@ -272,6 +287,7 @@ bool attend(Args& a) {
   p.lse = data<float>(lse);
   // without a workspace a block of this call's own, on its stream: calls on other streams and
   // other captured graphs never share it
+  const Unlocked unlocked;
   at::Tensor own;
   void* workspace = given ? given->data_ptr() : nullptr;
   size_t bytes = given ? given->nbytes() : 0;
@@ -304,6 +320,7 @@ bool accept(Args& a) {
     return false;
   const int64_t width = path->size(1);
   if (b.n_seqs && width > 1 && path->stride(1) != 1) return false;
+  const Unlocked unlocked;
   return smla_paged_accept(&b, data<int32_t>(path), b.n_seqs > 1 ? path->stride(0) : width, int32_t(width),
                            data<int32_t>(lens), a.stream()) == SMLA_OK;
 }
