@@ -52,7 +52,7 @@ typedef enum smla_status {
   SMLA_ERR_WORKSPACE = -5,  /* workspace missing or smaller than smla_decode_workspace_size */
   SMLA_ERR_SPLITS = -6,     /* num_splits outside [0, SMLA_MAX_SPLITS] */
   SMLA_ERR_DEVICE = -7,     /* no CUDA device, or the current device is not sm_103 */
-  SMLA_ERR_LAUNCH = -8      /* a kernel launch failed (see cudaGetLastError) */
+  SMLA_ERR_LAUNCH = -8      /* a kernel launch failed (an error that was there before is none of its own) */
 } smla_status;
 
 /* Bits a decode call ORs into *status (when status != NULL). */

@@ -1879,8 +1879,7 @@ static cudaError_t launch_fp8_hp(const DecodeLaunch& L) {
   args.tile_slots = kTileSlots;
   e = launch_trim(L, args);
   if (e != cudaSuccess) return e;
-  decode_fp8_kernel<HP><<<L.plan.grid * L.plan.head_groups, kThreads, smem, L.stream>>>(args);
-  e = cudaGetLastError();
+  e = launch(decode_fp8_kernel<HP>, dim3(unsigned(L.plan.grid * L.plan.head_groups)), kThreads, size_t(smem), L.stream, args);
   if (e != cudaSuccess || !L.plan.merge_kernel) return e;
   return launch_merge(L, args);
 }

@@ -272,8 +272,7 @@ cudaError_t launch_hp(const DecodeLaunch& L) {
   cudaError_t e = cudaFuncSetAttribute(decode_simt_kernel<HP>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
-  decode_simt_kernel<HP><<<L.plan.grid, kThreads, smem, L.stream>>>(make_decode_args(L));
-  return cudaGetLastError();
+  return launch(decode_simt_kernel<HP>, dim3(unsigned(L.plan.grid)), kThreads, smem, L.stream, make_decode_args(L));
 }
 
 }  // namespace

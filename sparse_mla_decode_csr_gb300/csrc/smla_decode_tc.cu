@@ -1434,8 +1434,7 @@ cudaError_t launch_tc_hp(const DecodeLaunch& L) {
   DecodeArgs args = make_decode_args(L);
   e = launch_trim(L, args);
   if (e != cudaSuccess) return e;
-  decode_tc_kernel<HP><<<L.plan.grid, kThreadsTC, smem, L.stream>>>(args);
-  e = cudaGetLastError();
+  e = launch(decode_tc_kernel<HP>, dim3(unsigned(L.plan.grid)), kThreadsTC, size_t(smem), L.stream, args);
   if (e != cudaSuccess || !L.plan.merge_kernel) return e;
   return launch_merge(L, args);
 }
@@ -1445,9 +1444,9 @@ cudaError_t launch_tc_hp(const DecodeLaunch& L) {
 cudaError_t launch_trim(const DecodeLaunch& L, DecodeArgs& args) {
   if (!(L.plan.trim_kernel && L.ws.lens_off >= 0)) return cudaSuccess;
   int32_t* lens_trim = reinterpret_cast<int32_t*>(static_cast<char*>(L.workspace) + L.ws.lens_off);
-  trim_rows_kernel<<<unsigned(L.p.n_q), 32 * kTrimWarps, 0, L.stream>>>(args, lens_trim);
+  const cudaError_t e = launch(trim_rows_kernel, dim3(unsigned(L.p.n_q)), 32 * kTrimWarps, 0, L.stream, args, lens_trim);
   args.lens = lens_trim;  // the caller's lens already capped these
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_merge(const DecodeLaunch& L, const DecodeArgs& args) {
@@ -1455,10 +1454,9 @@ cudaError_t launch_merge(const DecodeLaunch& L, const DecodeArgs& args) {
   // rows shared by many CTAs (few rows over the grid) split each head's parts
   // over a CTA's eight warps
   if (int64_t(L.plan.grid) > 8 * int64_t(L.p.n_q))
-    merge_rows_kernel<kMergeSplit><<<unsigned(pairs), 32 * kMergeSplit, 0, L.stream>>>(args);
-  else
-    merge_rows_kernel<1><<<unsigned((pairs + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0, L.stream>>>(args);
-  return cudaGetLastError();
+    return launch(merge_rows_kernel<kMergeSplit>, dim3(unsigned(pairs)), 32 * kMergeSplit, 0, L.stream, args);
+  return launch(merge_rows_kernel<1>, dim3(unsigned((pairs + kMergeWarps - 1) / kMergeWarps)), 32 * kMergeWarps, 0, L.stream,
+                args);
 }
 
 cudaError_t tc_set_wait_limit(uint64_t ns, int stall) {

@@ -8,6 +8,32 @@
 
 namespace smla {
 
+// A launch that answers for itself: cudaGetLastError behind a launch would report, and take
+// away, an error that another part of the process left.  (One of its own is taken away: the status
+// of the call carries it.)  `dependent`: see launch_dependent.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_kernel(bool dependent, void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                                 cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = attr;
+  config.numAttrs = dependent ? 1 : 0;
+  const cudaError_t err = cudaLaunchKernelEx(&config, kernel, Params(args)...);
+  if (err != cudaSuccess) cudaGetLastError();
+  return err;
+}
+template <typename... Params, typename... Args>
+inline cudaError_t launch(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                          const Args&... args) {
+  return launch_kernel(false, kernel, grid, threads, smem, stream, args...);
+}
+
 constexpr int kRecordBytes = SMLA_RECORD_BYTES;
 constexpr int kLatent = SMLA_LATENT_DIM;
 constexpr int kRope = SMLA_ROPE_DIM;

@@ -83,10 +83,9 @@ cudaError_t launch_pack(const void* latent, int64_t latent_stride, const void* r
                         int64_t rope_stride, int64_t n, void* kv_out, cudaStream_t stream) {
   int64_t blocks = (n + kWarpsPerBlock - 1) / kWarpsPerBlock;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  pack_records_kernel<<<unsigned(blocks), 32 * kWarpsPerBlock, 0, stream>>>(
-      static_cast<const uint16_t*>(latent), latent_stride, static_cast<const uint16_t*>(rope),
-      rope_stride, n, static_cast<uint8_t*>(kv_out));
-  return cudaGetLastError();
+  return launch(pack_records_kernel, dim3(unsigned(blocks)), 32 * kWarpsPerBlock, 0, stream,
+                static_cast<const uint16_t*>(latent), latent_stride, static_cast<const uint16_t*>(rope), rope_stride, n,
+                static_cast<uint8_t*>(kv_out));
 }
 
 }  // namespace smla

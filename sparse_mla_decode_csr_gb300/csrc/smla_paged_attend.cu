@@ -2565,20 +2565,18 @@ AttendPlan paged_attend_plan(const smla_paged_attend_params& p, int num_sms) {
 static cudaError_t launch_narrow(void (*kernel)(AttendArgs), int smem, const AttendArgs& a, cudaStream_t stream) {
   const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (err != cudaSuccess) return err;
-  kernel<<<a.workers, kNarrowThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch(kernel, dim3(unsigned(a.workers)), kNarrowThreads, size_t(smem), stream, a);
 }
 
 template <bool kTree>
-static cudaError_t launch_kernel(const AttendArgs& a, const AttendPlan& plan, cudaStream_t stream) {
+static cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& plan, cudaStream_t stream) {
   if (plan.narrow == 16) return launch_narrow(paged_attend_few_kernel<kTree>, kNarrowSmem<16>, a, stream);
   if (plan.narrow == 32) return launch_narrow(paged_attend_narrow_kernel<32, kTree>, kNarrowSmem<32>, a, stream);
   if (plan.narrow == 64) return launch_narrow(paged_attend_narrow_kernel<64, kTree>, kNarrowSmem<64>, a, stream);
   const cudaError_t err =
       cudaFuncSetAttribute(paged_attend_kernel<kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttendSmem);
   if (err != cudaSuccess) return err;
-  paged_attend_kernel<kTree><<<2 * plan.workers, kAttendThreads, kAttendSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch(paged_attend_kernel<kTree>, dim3(unsigned(2 * plan.workers)), kAttendThreads, kAttendSmem, stream, a);
 }
 
 cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const TreeMasks& tree, const AttendPlan& plan,
@@ -2608,7 +2606,7 @@ cudaError_t launch_paged_attend(const smla_paged_attend_params& p, const TreeMas
   a.mask = tree.mask;
   a.mask_stride = tree.stride;
   a.mask_words = tree.words;
-  const cudaError_t err = tree.words < 0 ? launch_kernel<false>(a, plan, stream) : launch_kernel<true>(a, plan, stream);
+  const cudaError_t err = tree.words < 0 ? launch_attend<false>(a, plan, stream) : launch_attend<true>(a, plan, stream);
   if (err != cudaSuccess || plan.workers == 1) return err;
   // Row tiles of 8 parts or more on average: several warps share a row's parts, and the
   // grid is as large as the row tiles, not as the workers (4 x 64 heads, 38 parts: 42.9 us

@@ -181,19 +181,17 @@ unsigned grid_of(const PagedArgs& a, int rows) {
 }
 
 template <int kDtype>
-void write_typed(const PagedArgs& a, const uint8_t* lat, int64_t ls, const uint8_t* rope, int64_t rs, cudaStream_t st) {
-  paged_write_kernel<kDtype><<<grid_of(a, 1), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+cudaError_t write_typed(const PagedArgs& a, const uint8_t* lat, int64_t ls, const uint8_t* rope, int64_t rs, cudaStream_t st) {
+  return launch(paged_write_kernel<kDtype>, dim3(grid_of(a, 1)), 32 * kWarps, 0, st, a, lat, ls, rope, rs);
 }
 
 template <int kDtype>
-void read_typed(const PagedArgs& a, uint8_t* lat, int64_t ls, uint8_t* rope, int64_t rs, cudaStream_t st) {
+cudaError_t read_typed(const PagedArgs& a, uint8_t* lat, int64_t ls, uint8_t* rope, int64_t rs, cudaStream_t st) {
   if constexpr (kDtype != SMLA_DTYPE_F32) {
-    if (a.n_rows > kOneRowLimit) {
-      paged_read_kernel<2, kDtype><<<grid_of(a, 2), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
-      return;
-    }
+    if (a.n_rows > kOneRowLimit)
+      return launch(paged_read_kernel<2, kDtype>, dim3(grid_of(a, 2)), 32 * kWarps, 0, st, a, lat, ls, rope, rs);
   }
-  paged_read_kernel<1, kDtype><<<grid_of(a, 1), 32 * kWarps, 0, st>>>(a, lat, ls, rope, rs);
+  return launch(paged_read_kernel<1, kDtype>, dim3(grid_of(a, 1)), 32 * kWarps, 0, st, a, lat, ls, rope, rs);
 }
 
 }  // namespace
@@ -203,10 +201,9 @@ cudaError_t launch_paged_write(const smla_paged_batch& b, const void* latent, in
   const PagedArgs a = make_paged_args(b);
   const uint8_t* l = static_cast<const uint8_t*>(latent);
   const uint8_t* r = static_cast<const uint8_t*>(rope);
-  if (dtype == SMLA_DTYPE_BF16) write_typed<SMLA_DTYPE_BF16>(a, l, ls, r, rs, st);
-  else if (dtype == SMLA_DTYPE_F16) write_typed<SMLA_DTYPE_F16>(a, l, ls, r, rs, st);
-  else write_typed<SMLA_DTYPE_F32>(a, l, ls, r, rs, st);
-  return cudaGetLastError();
+  if (dtype == SMLA_DTYPE_BF16) return write_typed<SMLA_DTYPE_BF16>(a, l, ls, r, rs, st);
+  if (dtype == SMLA_DTYPE_F16) return write_typed<SMLA_DTYPE_F16>(a, l, ls, r, rs, st);
+  return write_typed<SMLA_DTYPE_F32>(a, l, ls, r, rs, st);
 }
 
 cudaError_t launch_paged_read(const smla_paged_batch& b, void* latent, int64_t ls, void* rope, int64_t rs,
@@ -214,10 +211,9 @@ cudaError_t launch_paged_read(const smla_paged_batch& b, void* latent, int64_t l
   const PagedArgs a = make_paged_args(b);
   uint8_t* l = static_cast<uint8_t*>(latent);
   uint8_t* r = static_cast<uint8_t*>(rope);
-  if (dtype == SMLA_DTYPE_BF16) read_typed<SMLA_DTYPE_BF16>(a, l, ls, r, rs, st);
-  else if (dtype == SMLA_DTYPE_F16) read_typed<SMLA_DTYPE_F16>(a, l, ls, r, rs, st);
-  else read_typed<SMLA_DTYPE_F32>(a, l, ls, r, rs, st);
-  return cudaGetLastError();
+  if (dtype == SMLA_DTYPE_BF16) return read_typed<SMLA_DTYPE_BF16>(a, l, ls, r, rs, st);
+  if (dtype == SMLA_DTYPE_F16) return read_typed<SMLA_DTYPE_F16>(a, l, ls, r, rs, st);
+  return read_typed<SMLA_DTYPE_F32>(a, l, ls, r, rs, st);
 }
 
 }  // namespace smla

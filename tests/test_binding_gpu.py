@@ -1,4 +1,4 @@
-"""The paged calls of _smla.so beside the rest of a process: other Python threads."""
+"""The calls beside the rest of a process: other Python threads, errors of other libraries."""
 
 import ctypes
 import threading
@@ -75,3 +75,46 @@ def test_a_launch_that_blocks_leaves_other_threads_running(name, cudart):
     torch.cuda.synchronize()
     assert max(longest) > 0.3, "no launch waited"
     assert gap < max(longest) / 2
+
+
+def decode_calls():
+    """The decode by each kernel, its form without allocation, and the record writer."""
+    n, h = 40, 16
+    lat, rope = torch.randn(n, 512, device=DEV).bfloat16(), torch.randn(n, 64, device=DEV).bfloat16()
+    kv = torch.zeros(n, 656, dtype=torch.uint8, device=DEV)
+    smla.smla_pack_records(lat, rope, kv)
+    q, out = torch.randn(2, h, 576, device=DEV).bfloat16(), torch.empty(2, h, 512, device=DEV).bfloat16()
+    idx = torch.arange(n, dtype=torch.int32, device=DEV)
+    ptr = torch.tensor([0, 20, 40], dtype=torch.int32, device=DEV)
+    args = (q, kv, n, idx, ptr, None, 1 / 24, None, out, torch.empty(2, h, device=DEV))
+    found = {"pack": lambda: smla.smla_pack_records(lat, rope, kv), "noalloc": lambda: smla.smla_decode_noalloc(*args)}
+    for kernel in (smla.KERNEL_CUDA_CORE, smla.KERNEL_TENSOR_CORE_BF16, smla.KERNEL_TENSOR_CORE_FP8):
+        for padded in (False, True):
+            kw = dict(kernel=kernel, has_invalid=padded)
+            size = smla.smla_decode_workspace_size(2, h, 0, n, **kw)
+            ws = torch.zeros(size, dtype=torch.uint8, device=DEV)
+            found[f"decode_{kernel}_{padded}"] = lambda ws=ws, kw=kw: smla.smla_decode(*args, workspace_tensor=ws, **kw)
+    return found
+
+
+def test_an_error_of_another_library_is_no_failure_of_a_launch(cudart, monkeypatch):
+    # the last error of the process's runtime, made by a call that names no device: not a launch's of
+    # these calls, which go through at the first try, and still there behind them (except where a
+    # kernel's shared memory is set, when the runtime itself drops it)
+    everything = {**calls(), **decode_calls()}
+    for call in everything.values():
+        call()
+    torch.cuda.synchronize()
+
+    def second_try(*_):
+        raise AssertionError("the call was made again")
+
+    monkeypatch.setattr(smla, "_current_device", second_try)
+    for name, call in everything.items():
+        bad = cudart.cudaSetDevice(4096)
+        assert bad != 0
+        call()
+        if name in ("write", "read", "append", "tree", "accept", "pack"):
+            assert cudart.cudaPeekAtLastError() == bad, name
+    cudart.cudaGetLastError()
+    torch.cuda.synchronize()
