@@ -418,6 +418,13 @@ def _fail(code: int, what: str, why: str):
     raise SmlaError(code, f"{what}: {why}")
 
 
+def _made(what: str, answer) -> bool:
+    """Whether _smla.so has made the call; raises when it has and a launch failed."""
+    if answer is True or answer is False:
+        return answer
+    raise SmlaError(answer, what)
+
+
 def _launch_stream(stream, device: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
@@ -507,7 +514,7 @@ def smla_paged_write(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.T
     skipped and set STATUS_INDEX_OOB.  The rows' positions must lie in different
     slots.  An infinite latent takes its whole block of 128 values to the scale
     2^120, where ordinary values become zero.  See include/smla.h."""
-    if _native.write(kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status):
+    if _made("smla_paged_write", _native.write(kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status)):
         return
     _paged_copy("smla_paged_write", _write_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
@@ -520,7 +527,7 @@ def smla_paged_read(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows: 
     [rows, 64] (bf16, f16 or f32).  Batch as smla_paged_write: row r of sequence
     b gets position seq_lens[b] - (cu_rows[b + 1] - r); masked positions give
     zeros, rows of no sequence are left as they were.  See include/smla.h."""
-    if _native.read(kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status):
+    if _made("smla_paged_read", _native.read(kv_cache, block_table, cu_rows, seq_lens, latent, rope, stream, status)):
         return
     _paged_copy("smla_paged_read", _read_packed, kv_cache, block_table, cu_rows, seq_lens, latent, rope,
                 stream, status)
@@ -538,8 +545,8 @@ def smla_paged_attend_workspace_size(n_rows: int, num_heads: int, n_seqs: int, p
 
 def _attend(what: str, q, kv_cache, block_table, cu_rows, seq_lens, mask, sm_scale, sink, out, lse, stream, causal,
             status, workspace_tensor) -> None:
-    if _native.attend(kv_cache, block_table, cu_rows, seq_lens, q, sm_scale, sink, out, lse, causal, stream, status,
-                      workspace_tensor, mask):
+    if _made(what, _native.attend(kv_cache, block_table, cu_rows, seq_lens, q, sm_scale, sink, out, lse, causal, stream, status,
+                                  workspace_tensor, mask)):
         return
     if q.dtype != torch.bfloat16 or q.dim() != 3 or q.shape[2] != QK_DIM:
         _fail(SMLA_ERR_SHAPE, what, f"q is bf16 [rows, heads, {QK_DIM}]")
@@ -657,10 +664,10 @@ def smla_paged_append(latent: torch.Tensor, rope: torch.Tensor, kv_cache: torch.
     dims (2k, 2k + 1), or (k, k + 32) without interleaved; rope_scale
     multiplies the results.  Batch and masked rows as smla_paged_write.  See
     include/smla.h."""
-    if _native.append(kv_cache, block_table, cu_rows, seq_lens, latent, rope, turns, q_rope, q_out, positions,
-                      interleaved, rope_scale, stream, status):
-        return
     what = "smla_paged_append"
+    if _made(what, _native.append(kv_cache, block_table, cu_rows, seq_lens, latent, rope, turns, q_rope, q_out, positions,
+                                  interleaved, rope_scale, stream, status)):
+        return
     n, dtype, ls, rs = _rows(what, latent, rope)
     if turns.dtype != torch.int64 or turns.shape != (ROPE_DIM // 2,) or not turns.is_contiguous():
         _fail(SMLA_ERR_SHAPE, what, f"turns is int64 [{ROPE_DIM // 2}], made by smla_rotation_turns")
@@ -713,9 +720,9 @@ def smla_paged_tree(parents: torch.Tensor, cu_rows: torch.Tensor, seq_lens: torc
     position of node 0 plus the node's depth.  A parent that is not a lower
     node, or a node that the words cannot hold, sets STATUS_INDEX_OOB.  See
     include/smla.h."""
-    if _native.tree(parents, cu_rows, seq_lens, mask, positions, stream, status):
-        return
     what = "smla_paged_tree"
+    if _made(what, _native.tree(parents, cu_rows, seq_lens, mask, positions, stream, status)):
+        return
     i32 = torch.int32
     if parents.dtype != i32 or cu_rows.dtype != i32 or seq_lens.dtype != i32 or parents.dim() != 1 or \
             cu_rows.dim() != 1 or seq_lens.dim() != 1:
@@ -766,9 +773,9 @@ def smla_paged_accept(kv_cache: torch.Tensor, block_table: torch.Tensor, cu_rows
     the position of node 0 plus the number of nodes.  An entry that is no node or
     does not rise ends the path and sets STATUS_INDEX_OOB.  n_rows: rows of the
     token tensors, which clamp cu_rows in the other calls.  See include/smla.h."""
-    if _native.accept(kv_cache, block_table, cu_rows, seq_lens, path, new_lens, n_rows, stream, status):
-        return
     what = "smla_paged_accept"
+    if _made(what, _native.accept(kv_cache, block_table, cu_rows, seq_lens, path, new_lens, n_rows, stream, status)):
+        return
     batch = _paged_batch(what, kv_cache, block_table, cu_rows, seq_lens, int(n_rows), status)
     n_seqs = seq_lens.shape[0]
     if path.dtype != torch.int32 or path.dim() != 2 or path.shape[0] != n_seqs:

@@ -4,7 +4,9 @@
 // dozen tensors (tree masks: 3 us and 7), so the tensors' properties are read here.
 // A function returns True when it has made its C call with success.  It returns False, and has
 // enqueued nothing, when anything is not as the call wants it or is less common (a stream
-// given by hand): the caller then goes through the checks in Python, which name the fault.
+// given by hand): the caller then goes through the checks in Python, which name the fault.  A
+// launch that failed is returned as its status: an attend has two, the first of which may have
+// gone through, so the call is not made again.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -72,6 +74,8 @@ struct Args {
     }
     return float(d);
   }
+  // Whether all arguments were as asked for, and there are no more.
+  bool fine() const { return ok && at == n; }
   // Fails the call unless `c`.
   bool want(bool c) {
     ok = ok && c;
@@ -171,56 +175,58 @@ class Unlocked {
   PyThreadState* state_;
 };
 
-template <bool (*kCall)(Args&)>
+// What a call returns: the status of its C call, or that it is not for these functions.
+constexpr int kNotTaken = 1;
+
+template <int (*kCall)(Args&)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  bool done = false;
+  int rc = kNotTaken;
   try {
     Args a(args, n);
-    done = kCall(a) && a.at == n;
+    rc = kCall(a);
   } catch (...) {  // (an allocation: the calls in Python raise it again)
   }
-  return PyBool_FromLong(done);
+  return rc == SMLA_ERR_LAUNCH ? PyLong_FromLong(rc) : PyBool_FromLong(rc == SMLA_OK);
 }
 
 // write and read: kv, table, cu, lens, latent, rope, stream, status
 template <bool kWrite>
-bool copy(Args& a) {
+int copy(Args& a) {
   smla_paged_batch b{};
   Rows r;
   take_batch(a, b);
-  if (!a.ok) return false;
+  if (!a.ok) return kNotTaken;
   take_rows(a, r);
   a.want(a.none());
   b.status = status_of(a, a.tensor(true));
-  if (!a.ok) return false;
+  if (!a.fine()) return kNotTaken;
   b.n_rows = r.n;
   const Unlocked unlocked;
-  const int rc = kWrite ? smla_paged_write(&b, r.latent, r.latent_stride, r.rope, r.rope_stride, r.dtype, a.stream())
-                        : smla_paged_read(&b, r.latent, r.latent_stride, r.rope, r.rope_stride, r.dtype, a.stream());
-  return rc == SMLA_OK;
+  return kWrite ? smla_paged_write(&b, r.latent, r.latent_stride, r.rope, r.rope_stride, r.dtype, a.stream())
+                : smla_paged_read(&b, r.latent, r.latent_stride, r.rope, r.rope_stride, r.dtype, a.stream());
 }
 
 // append: kv, table, cu, lens, latent, rope, turns, q_rope, q_out, positions, interleaved, rope_scale,
 // stream, status
-bool append(Args& a) {
+int append(Args& a) {
   smla_paged_append_params p{};
   Rows r;
   take_batch(a, p.batch);
-  if (!a.ok) return false;
+  if (!a.ok) return kNotTaken;
   take_rows(a, r);
   const at::Tensor *turns = a.tensor(), *q = a.tensor(true), *out = a.tensor(true), *pos = a.tensor(true);
   p.interleaved = a.flag();
   p.rope_scale = a.number();
   a.want(a.none());
   p.batch.status = status_of(a, a.tensor(true));
-  if (!a.ok || !vector_of(turns, at::kLong, SMLA_ROPE_DIM / 2) || (q == nullptr) != (out == nullptr)) return false;
-  if (pos && !vector_of(pos, at::kInt, r.n)) return false;
+  if (!a.fine() || !vector_of(turns, at::kLong, SMLA_ROPE_DIM / 2) || (q == nullptr) != (out == nullptr)) return kNotTaken;
+  if (pos && !vector_of(pos, at::kInt, r.n)) return kNotTaken;
   if (q) {
-    if (q->dim() != 3 || q->size(1) >= kMaxSize) return false;
+    if (q->dim() != 3 || q->size(1) >= kMaxSize) return kNotTaken;
     const int64_t heads = q->size(1);
     if (!take_heads(q, r.type, r.n, heads, SMLA_ROPE_DIM, &p.q_rope_stride_row, &p.q_rope_stride_head) ||
         !take_heads(out, at::kBFloat16, r.n, heads, SMLA_ROPE_DIM, &p.q_out_stride_row, &p.q_out_stride_head))
-      return false;
+      return kNotTaken;
     p.num_heads = int32_t(heads);
     p.q_rope = q->data_ptr();
     p.q_out = out->data_ptr();
@@ -234,33 +240,33 @@ bool append(Args& a) {
   p.turns = static_cast<const uint64_t*>(turns->data_ptr());
   p.positions = data<int32_t>(pos);
   const Unlocked unlocked;
-  return smla_paged_append(&p, a.stream()) == SMLA_OK;
+  return smla_paged_append(&p, a.stream());
 }
 
 // tree: parents, cu, lens, mask, positions, stream, status
-bool tree(Args& a) {
+int tree(Args& a) {
   const at::Tensor *parents = a.tensor(), *cu = a.tensor(), *lens = a.tensor(), *mask = a.tensor(true), *pos = a.tensor(true);
   a.want(a.none());
   int32_t* status = status_of(a, a.tensor(true));
-  if (!a.ok || parents->dim() != 1 || lens->dim() != 1) return false;
+  if (!a.fine() || parents->dim() != 1 || lens->dim() != 1) return kNotTaken;
   const int64_t n = parents->size(0), seqs = lens->size(0);
   if (seqs >= kMaxSize || !vector_of(parents, at::kInt, n) || !vector_of(lens, at::kInt, seqs) ||
       !vector_of(cu, at::kInt, seqs + 1) || (pos && !vector_of(pos, at::kInt, n)))
-    return false;
+    return kNotTaken;
   int64_t stride = 0;
   int32_t words = 0;
-  if (mask && !take_mask(mask, n, &stride, &words)) return false;
+  if (mask && !take_mask(mask, n, &stride, &words)) return kNotTaken;
   const Unlocked unlocked;
   return smla_paged_tree(data<int32_t>(parents), data<int32_t>(cu), data<int32_t>(lens), n, int32_t(seqs),
-                         data<uint32_t>(mask), stride, words, data<int32_t>(pos), status, a.stream()) == SMLA_OK;
+                         data<uint32_t>(mask), stride, words, data<int32_t>(pos), status, a.stream());
 }
 
 // attend and attend_tree: kv, table, cu, lens, q, sm_scale, sink, out, lse, causal, stream, status,
 // workspace, mask (None: attend)
-bool attend(Args& a) {
+int attend(Args& a) {
   smla_paged_attend_params p{};
   take_batch(a, p.batch);
-  if (!a.ok) return false;
+  if (!a.ok) return kNotTaken;
   const at::Tensor* q = a.tensor();
   p.sm_scale = a.number();
   const at::Tensor *sink = a.tensor(true), *out = a.tensor(), *lse = a.tensor(true);
@@ -268,17 +274,17 @@ bool attend(Args& a) {
   a.want(a.none());
   p.batch.status = status_of(a, a.tensor(true));
   const at::Tensor *given = a.tensor(true), *mask = a.tensor(true);
-  if (!a.ok || q->dim() != 3 || q->size(1) >= kMaxSize) return false;
+  if (!a.fine() || q->dim() != 3 || q->size(1) >= kMaxSize) return kNotTaken;
   const int64_t n = q->size(0), heads = q->size(1);
   if (!take_heads(q, at::kBFloat16, n, heads, SMLA_QK_DIM, &p.q_stride_row, &p.q_stride_head) ||
       !take_heads(out, at::kBFloat16, n, heads, SMLA_LATENT_DIM, &p.out_stride_row, &p.out_stride_head))
-    return false;
-  if (sink && !vector_of(sink, at::kFloat, heads)) return false;
-  if (lse && !(is(lse, at::kFloat, 2) && lse->size(0) == n && lse->size(1) == heads && lse->is_contiguous())) return false;
-  if (given && !given->is_contiguous()) return false;
+    return kNotTaken;
+  if (sink && !vector_of(sink, at::kFloat, heads)) return kNotTaken;
+  if (lse && !(is(lse, at::kFloat, 2) && lse->size(0) == n && lse->size(1) == heads && lse->is_contiguous())) return kNotTaken;
+  if (given && !given->is_contiguous()) return kNotTaken;
   int64_t mask_stride = 0;
   int32_t words = 0;
-  if (mask && !take_mask(mask, n, &mask_stride, &words)) return false;
+  if (mask && !take_mask(mask, n, &mask_stride, &words)) return kNotTaken;
   p.batch.n_rows = n;
   p.num_heads = int32_t(heads);
   p.q = q->data_ptr();
@@ -298,34 +304,33 @@ bool attend(Args& a) {
       workspace = own.data_ptr();
     }
   }
-  const int rc = mask ? smla_paged_attend_tree(&p, data<uint32_t>(mask), mask_stride, words, workspace, bytes, a.stream())
-                      : smla_paged_attend(&p, workspace, bytes, a.stream());
-  return rc == SMLA_OK;
+  return mask ? smla_paged_attend_tree(&p, data<uint32_t>(mask), mask_stride, words, workspace, bytes, a.stream())
+              : smla_paged_attend(&p, workspace, bytes, a.stream());
 }
 
 // accept: kv, table, cu, lens, path, new_lens, n_rows, stream, status
-bool accept(Args& a) {
+int accept(Args& a) {
   smla_paged_batch b{};
   take_batch(a, b);
   const at::Tensor *path = a.tensor(), *lens = a.tensor();
   b.n_rows = PyLong_AsLongLong(a.next());
   if (b.n_rows == -1 && PyErr_Occurred()) {
     PyErr_Clear();
-    return false;
+    return kNotTaken;
   }
   a.want(a.none());
   b.status = status_of(a, a.tensor(true));
-  if (!a.ok || !is(path, at::kInt, 2) || path->size(0) != b.n_seqs || path->size(1) >= kMaxSize ||
+  if (!a.fine() || !is(path, at::kInt, 2) || path->size(0) != b.n_seqs || path->size(1) >= kMaxSize ||
       !vector_of(lens, at::kInt, b.n_seqs))
-    return false;
+    return kNotTaken;
   const int64_t width = path->size(1);
-  if (b.n_seqs && width > 1 && path->stride(1) != 1) return false;
+  if (b.n_seqs && width > 1 && path->stride(1) != 1) return kNotTaken;
   const Unlocked unlocked;
   return smla_paged_accept(&b, data<int32_t>(path), b.n_seqs > 1 ? path->stride(0) : width, int32_t(width),
-                           data<int32_t>(lens), a.stream()) == SMLA_OK;
+                           data<int32_t>(lens), a.stream());
 }
 
-template <bool (*kCall)(Args&)>
+template <int (*kCall)(Args&)>
 PyMethodDef method(const char* name) {
   return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<kCall>)), METH_FASTCALL, nullptr};
 }

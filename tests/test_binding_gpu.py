@@ -118,3 +118,30 @@ def test_an_error_of_another_library_is_no_failure_of_a_launch(cudart, monkeypat
             assert cudart.cudaPeekAtLastError() == bad, name
     cudart.cudaGetLastError()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_launch_that_fails_is_raised_and_not_made_again(name, cudart, monkeypatch):
+    # a stream whose capture has been made invalid (by a synchronisation) takes no launch
+    call, stream, graph = calls()[name], torch.cuda.Stream(), ctypes.c_void_p()
+    call()
+    torch.cuda.synchronize()
+    handle, relaxed = ctypes.c_void_p(stream.cuda_stream), 2
+
+    def second_try(*_):
+        raise AssertionError("the call was made again")
+
+    monkeypatch.setattr(smla, "_current_device", second_try)
+    assert cudart.cudaStreamBeginCapture(handle, relaxed) == 0
+    try:
+        assert cudart.cudaStreamSynchronize(handle) != 0
+        with torch.cuda.stream(stream):
+            with pytest.raises(smla.SmlaError) as e:
+                call()
+        assert e.value.code == -8
+    finally:
+        cudart.cudaStreamEndCapture(handle, ctypes.byref(graph))
+        cudart.cudaGetLastError()
+    assert not graph
+    call()
+    torch.cuda.synchronize()
