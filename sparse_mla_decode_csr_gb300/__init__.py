@@ -202,7 +202,11 @@ def _load():
 
 lib = _load()
 
-from . import _smla as _native  # noqa: E402  (built beside libsmla.so, which it calls)
+try:
+    from . import _smla as _native  # noqa: E402  (built beside libsmla.so, which it calls)
+except ImportError as e:
+    raise ImportError("_smla.so is not built for this Python and PyTorch: run "
+                      "`python -c \"import __graft_entry__ as g; g.build()\"`") from e
 
 EXPORTED_SYMBOLS = ("smla_plan", "smla_decode_workspace_size", "smla_decode", "smla_decode_noalloc",
                     "smla_pack_records", "smla_paged_write", "smla_paged_read",

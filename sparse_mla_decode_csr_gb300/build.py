@@ -3,7 +3,8 @@
 Each translation unit under csrc/ compiles in parallel to _build/*.o, then one
 link step makes sparse_mla_decode_csr_gb300/libsmla.so from the CUDA sources and
 another _smla.so from smla_binding.cpp, which reads PyTorch's tensors and calls
-libsmla.so.  Objects are rebuilt only when a source or header is newer than them.
+libsmla.so.  Objects are rebuilt only when a source or header is newer than them, the
+binding's also when it was made for another Python or PyTorch.
 """
 
 from __future__ import annotations
@@ -43,15 +44,31 @@ def _headers():
         glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
+def _torch(*path: str) -> str:
+    return os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), *path)
+
+
+def _made_for(src: str) -> str:
+    """What an object is made for besides its sources: the Python and PyTorch whose headers it takes."""
+    if src.endswith(".cu"):
+        return ""
+    with open(_torch("version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{_torch()}\n{f.read()}"
+
+
 def _stale(obj: str, src: str) -> bool:
     if not os.path.exists(obj):
         return True
     t = os.path.getmtime(obj)
-    return any(os.path.getmtime(f) > t for f in [src] + _headers())
-
-
-def _torch(*path: str) -> str:
-    return os.path.join(os.path.dirname(importlib.util.find_spec("torch").origin), *path)
+    if any(os.path.getmtime(f) > t for f in [src] + _headers()):
+        return True
+    what, stamp = _made_for(src), obj + ".for"
+    if not what:
+        return False
+    if not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        return f.read() != what
 
 
 def _run(cmd, what: str, verbose: bool) -> None:
@@ -75,12 +92,15 @@ def _compile(src: str, verbose: bool) -> str:
             cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden"] + \
                 [x for d in include for x in ("-isystem" if d != INCLUDE else "-I", d)]
         _run(cmd + ["-c", src, "-o", obj], f"compiling {src}", verbose)
+        if _made_for(src):
+            with open(obj + ".for", "w") as f:
+                f.write(_made_for(src))
     return obj
 
 
-def _link(out: str, objs, cmd, verbose: bool, force: bool) -> None:
+def _link(out: str, objs, cmd, verbose: bool, force: bool, libs=()) -> None:
     if force or not os.path.exists(out) or any(os.path.getmtime(o) > os.path.getmtime(out) for o in objs):
-        _run(cmd + ["-o", out + ".tmp"] + objs, f"linking {out}", verbose)
+        _run(cmd + ["-o", out + ".tmp", *objs, *libs], f"linking {out}", verbose)
         os.replace(out + ".tmp", out)
 
 
@@ -96,10 +116,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
     cuda = [o for s, o in zip(sources, objs) if s.endswith(".cu")]
     _link(LIB, cuda, [nvcc()] + ARCH + ["-shared", "-cudart", "shared"], verbose, force)
     if not TRACE:
-        # (the library goes behind the object that needs it)
-        libs = [f"-L{PKG}", "-Wl,-rpath,$ORIGIN", f"-L{_torch('lib')}"]
-        names = ["-l:libsmla.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-        _link(BINDING, [o for o in objs if o not in cuda], ["g++", "-shared", "-Wl,--no-as-needed"] + libs + names, verbose, force)
+        # (libraries go behind the object that needs them)
+        libs = [f"-L{PKG}", "-Wl,-rpath,$ORIGIN", f"-L{_torch('lib')}", "-l:libsmla.so", "-ltorch_python", "-ltorch_cpu",
+                "-lc10", "-lc10_cuda"]
+        _link(BINDING, [o for o in objs if o not in cuda], ["g++", "-shared"], verbose, force, libs)
     return LIB
 
 
