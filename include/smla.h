@@ -432,9 +432,10 @@ int smla_rotation_turns(const double* inv_freq, uint64_t* turns);
 /* smla_paged_write with the rope of keys and queries rotated on the way.  With t the
  * turn of pair k at a row's rotation position, p * inv_freq[k] radians,
  *   (x, y) -> rope_scale * (x cos t - y sin t, x sin t + y cos t),
- * the pair being dims 2k and 2k + 1 (interleaved) or k and k + 32.  The angle is exact
- * modulo a turn for every int32 position; the products are f32, and each result is
- * rounded once to bf16.
+ * the pair being dims 2k and 2k + 1 (interleaved) or k and k + 32.  Whole turns drop out
+ * exactly at every int32 position (but for the table's 2^-64 of a turn, times the position);
+ * what is left of the angle is cut after 2^-32 of a turn and rounded to f32, by 2^-26 of a
+ * turn at most.  Cosine, sine and the products are f32, and each result is rounded once to bf16.
  *   latent, rope, dtype  as in smla_paged_write (rope before the rotation)
  *   turns       device, smla_rotation_turns
  *   rope_scale  finite; it enters cosine and sine
@@ -487,7 +488,8 @@ int smla_paged_tree(const int32_t* parents, const int32_t* cu_rows, const int32_
  * sequence's row j, a row sees the key if bit j % 32 of word j / 32 of its mask is set,
  * and of earlier positions all.  Rows behind the masks' words are not seen; bits behind the
  * sequence's rows mean nothing.  With causal = 1 a row in addition sees no position
- * behind its own (in the cache), which for trees changes nothing.  A row that sees
+ * behind its own (in the cache), which for smla_paged_tree's masks changes no result and
+ * passes over the keys of later nodes.  A row that sees
  * nothing gives out = 0 and lse = -inf; what a row may not see never reaches it.  mask
  * uint32 [n_rows][mask_stride], mask_words used (NULL with mask_words = 0: the history
  * alone).  Workspace, accuracy and the choice of the kernel as smla_paged_attend. */
@@ -516,7 +518,10 @@ int smla_device_check(void);
 
 /* Limit, in ns, of every in-kernel pipeline wait of the tensor-core kernels
  * launched after this call on the current device (process-wide); 0 restores
- * the default of 2 s.  A wait that runs out sets SMLA_STATUS_TIMEOUT: the CTA
+ * the default of 2 s.  (In smla_paged_attend's kernel for more than 64 rows a sequence
+ * it is the time within which a pair of CTAs has to get on to its next tile of keys,
+ * whichever wait that is; a pair that then still stands ends after 2 s more.)
+ * A wait that runs out sets SMLA_STATUS_TIMEOUT: the CTA
  * then skips its remaining waits, still issues its pending copies and MMAs,
  * waits (2 s at most each) until they have completed, frees its tensor memory
  * and exits, so that the CUDA context stays usable.  out, lse, n_valid and the

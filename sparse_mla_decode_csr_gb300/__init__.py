@@ -391,7 +391,7 @@ def smla_pack_records(latent: torch.Tensor, rope: torch.Tensor, kv_out: torch.Te
 # These calls can take less time on the GPU than their checks do here.  Well-formed calls
 # on the current stream are therefore made by _smla.so (csrc/smla_binding.cpp), which
 # answers False to all others and does nothing for them: they go through the checks
-# here, which name what is wrong.  The checks read each tensor's properties once, the
+# here, which name what is wrong.  A launch that failed there is raised.  The checks read each tensor's properties once, the
 # messages are made on failure, and the C structs are packed as bytes.
 
 _BATCH_FORMAT = "PqqiiPqPPqi4xP"
@@ -757,8 +757,9 @@ def smla_paged_attend_tree(q: torch.Tensor, kv_cache: torch.Tensor, block_table:
     """smla_paged_attend for trees of drafted tokens: of its sequence's token rows a
     row sees row j if bit j % 32 of word j // 32 of its mask (int32 [rows, words],
     e.g. of smla_paged_tree) is set, and of earlier positions all.  With causal
-    a row in addition sees no position behind its own.  Everything else, the
-    workspace's size included, as smla_paged_attend.  See include/smla.h."""
+    a row in addition sees no position behind its own (the same for trees, and the
+    keys of later nodes are passed over).  Everything else, the workspace's size
+    included, as smla_paged_attend.  See include/smla.h."""
     what = "smla_paged_attend_tree"
     if mask is None:
         _fail(SMLA_ERR_NULL, what, "mask is int32 [rows, words]")

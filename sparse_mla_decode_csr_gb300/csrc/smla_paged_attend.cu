@@ -45,9 +45,9 @@
 // What bounds the pair kernel: shared memory.  For a tile of 64 keys the operands' reads
 // (1248 cycles), the loaders' and softmax warps' accesses (579) and the bulk copies (512) keep
 // its port busy for ~2340.  One chunk of 2048 tokens, 64 heads, after 8192 earlier
-// positions: 2365 us = 1111 TFLOP/s, 57% of the measured bf16 peak; 7 chunks of up to 300
-// tokens, 16 heads, up to 4927 positions: 203 us; 32 trees of up to 60 nodes, 64 heads, up to
-// 2000 positions: 296 us.  A row-tile change costs 4 to 5 us beside its tiles.
+// positions: 2340 us = 1123 TFLOP/s, 58% of the measured bf16 peak; 7 chunks of up to 300
+// tokens, 16 heads, up to 4927 positions: 202 us; 32 trees of up to 60 nodes, 64 heads, up to
+// 2000 positions: 295 us.  A row-tile change costs 4 to 5 us beside its tiles.
 //
 // Trees (kTree): of its sequence's token rows a row sees those in its mask, whatever their
 // order, instead of the ones up to its own.  Only tiles that reach past the history look at it.
@@ -1657,11 +1657,11 @@ paged_attend_kernel(const __grid_constant__ AttendArgs a) {
 // two blocks of PV each.
 //
 // What bounds it: the loaders (2.1 us a tile of 64 records by eight warps at the register
-// limit, the same for 17, 32 and 64 rows: 3.0 TB/s of records over all SMs), whose
-// largest stall is the wait for their own global loads, and for short rows the ~10 us
-// until the first scores and the partials' way through L2.  4 x 64 heads over up to 16384
-// positions: 35 us; 64 x 64 heads over 4096: 86 us; 64 trees of up to 4 nodes, 16 heads,
-// over up to 4096: 66 us.
+// limit, the same for 17, 32 and 64 rows, with masks and without: 3.1 TB/s of records over all
+// SMs), whose largest stall is the wait for their own global loads, and for short rows the
+// ~10 us until the first scores and the partials' way through L2.  4 x 64 heads over up to
+// 16384 positions: 35 us; 64 x 64 heads over 4096: 83 us; 64 trees of up to 4 nodes, 16 heads,
+// over up to 4096: 66 us; of up to 2: 61 us.
 
 // Loads of 16 rows and 32 columns by the whole warp: lane l gets columns 8 j + 2 (l % 4)
 // and the next of rows l / 4 and l / 4 + 8, as o[4 j], o[4 j + 1] and o[4 j + 2], o[4 j + 3].
@@ -2045,10 +2045,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1) paged_attend_narrow_kernel(
 // warp takes 24 of the keys.  Per tile: S read, maxima exchanged, P stored, then warp 0
 // issues the next QK, warps 1 and 2 two blocks of O^T += V^T P^T each.
 //
-// 64 x 16 heads over up to 4096 positions: 53 us (131 MB of records: 2.5 TB/s; 60 us with
+// 64 x 16 heads over up to 4096 positions: 51 us (131 MB of records: 2.6 TB/s; 60 us with
 // eight loaders, tiles of 64 keys and Q in shared memory, 62 us with Q in tensor memory
-// and a third stage instead of more loaders); one token, 16 heads, 500 positions: 15 us.
-// Bound: 2.2 us a tile of 96 keys (4.3 TB/s of records over all SMs), still the loaders,
+// and a third stage instead of more loaders); one token, 16 heads, 500 positions: 13.6 us.
+// Bound: 2.2 us a tile of 96 keys (4.4 TB/s of records over all SMs), still the loaders,
 // and ~18 us of start, partials and merge.
 
 // QK of tile g, by warp 0.
@@ -2510,13 +2510,13 @@ paged_merge_pair_kernel(const __grid_constant__ AttendArgs a) {
 // device.  Any split is computed correctly by either.  Measured at 64 sequences of
 // 4096 positions (graph replays, us; rows: few-row kernel / narrow tiles of 32 / of 64 /
 // pair kernel):
-//   16: 62 / 77 / 77 / 89    24: - / 78 / 78 / 90    32: 105 / 80 / 82 / 89
-//   64: 192 / 139 / 87 / 92    96: 277 / 200 / 146 / 95    128: - / - / 152 / 98
+//   16: 61 / 73 / 73 / 86    24: - / 74 / 75 / 87    32: 103 / 77 / 77 / 86
+//   64: 189 / 135 / 82 / 90    96: 269 / 195 / 141 / 92    128: - / - / 147 / 95
 // One kernel serves the whole call, so a batch of unlike sequences gets what its mean
-// gives: 63 single tokens and one of two, 16 heads, take 77 us in tiles of 32 (63 without
-// the second token); 63 tokens and a chunk of 512 177 us in one call, 63 + 97 as two;
-// 255 tokens and the chunk 373, 191 + 97 as two.  Empty sequences count: a chunk of 2048
-// tokens, 4 heads, takes 84 us alone or among 64 sequences, 276 among 512.
+// gives: 63 single tokens and one of two, 16 heads, take 73 us in tiles of 32 (60 without
+// the second token); 63 tokens and a chunk of 512 152 us in one call, 61 + 86 as two;
+// 255 tokens and the chunk 359, 187 + 86 as two.  Empty sequences count: a chunk of 2048
+// tokens, 4 heads, takes 74 us alone or among 64 sequences, 272 among 512.
 static int narrow_rows(const smla_paged_attend_params& p) {
   if (p.num_heads > kCtaRows) return 0;
   const int64_t mean = (p.batch.n_rows * p.num_heads + p.batch.n_seqs - 1) / p.batch.n_seqs;
