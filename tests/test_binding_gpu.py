@@ -145,3 +145,47 @@ def test_a_launch_that_fails_is_raised_and_not_made_again(name, cudart, monkeypa
     assert not graph
     call()
     torch.cuda.synchronize()
+
+
+def test_threads_with_streams_of_their_own_get_what_one_gets():
+    # four Python threads make whole steps at once, each on its stream, over batches of its own
+    def batch(i):
+        return [[(20, 300), (9, 100)], [(3, 40), (2, 9)], [(1, 700)] * 9, [(60, 200)]][i]
+
+    def state(i):
+        c = Batch(batch(i), 16, seed=i)
+        return step_state(c, 16, 90 + i)
+
+    def bits_of(s):
+        return [s[k] for k in ("mask", "pos", "q", "kv", "out", "lse", "new")]
+
+    want = []
+    for i in range(4):
+        s = state(i)
+        step(s)
+        torch.cuda.synchronize()
+        want.append(bits_of(s))
+    states = [[state(i) for _ in range(12)] for i in range(4)]
+    streams, failed = [torch.cuda.Stream() for _ in range(4)], []
+    torch.cuda.synchronize()
+    start = threading.Barrier(4)
+
+    def work(i):
+        try:
+            with torch.cuda.stream(streams[i]):
+                start.wait(10)
+                for s in states[i]:
+                    step(s)
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == []
+    for i in range(4):
+        for s in states[i]:
+            assert all(torch.equal(a, b) for a, b in zip(bits_of(s), want[i]))
